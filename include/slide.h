@@ -459,6 +459,184 @@ SLIDE_API slide_status slide_deliver_bf16(slide_state *st, int32_t layer, void *
  * in, the update and the copies out of a layer overlap). */
 SLIDE_API slide_status slide_streamed_timeline(slide_state *st, double *out, int64_t cap);
 
+/* ---- Matrix optimizer: orthogonalised momentum (Muon) -----------------------
+ *
+ * What is computed, for a batch of rows x cols matrices:
+ *   slide_orthogonalize:
+ *     X = G / (||G||_F + eps)
+ *     `steps` times, with that step's (a, b, c):   A = X X^T  (X^T X if rows > cols)
+ *                                                  X = a X + (b A + c A A) X   (X on the left if rows > cols)
+ *     out = bf16(X)
+ *   slide_muon_step, with R gradient replicas g_r and mu = momentum:
+ *     g   = (sum_r g_r, in FP32, replica order) / R
+ *     mom = mu*mom + (1-mu)*g
+ *     u   = mu*mom + (1-mu)*g   if nesterov, else mom
+ *     O   = X of u, as above, not rounded
+ *     th  = th*(1 - lr*wd) - (lr*scale)*O,    w = bf16_round_nearest_even(th)
+ *   mom and th are FP32 and updated in place; momentum's and theta's lines are
+ *   one FP32 operation each, the scalars formed in double and rounded once.
+ *   The products run on FP16 operands (scaled by powers of two) with FP32
+ *   accumulators, and the diagonals of the left factors and the iterate itself
+ *   stay in FP32.  Against the polynomial in 64 bits (2-norm of the difference
+ *   over 2-norm) X is off by 5e-4 to 1.3e-3 for gradients' spectra, from noise
+ *   to a few strong directions, and by up to 3e-2 for a matrix of one repeated
+ *   value, whose roundings all have one sign.
+ * Zeros give zeros; a NaN or an infinity in a matrix makes that matrix's
+ * result NaN and touches no other matrix of the batch. */
+enum { SLIDE_TYPE_BF16 = 0, SLIDE_TYPE_FP32 = 1 };
+
+typedef struct {
+    int32_t steps;       /* 1..16 */
+    const float *coeffs; /* host array [3*steps] of (a, b, c), read during the call; NULL = (3.4445,
+                            -4.7750, 2.0315) at every step.  A polynomial that lets the spectral
+                            norm grow beyond 64 is refused. */
+    float eps;           /* >= 0, finite */
+} slide_ortho_params;
+
+typedef struct {
+    float lr, momentum, weight_decay; /* lr >= 0, 0 <= momentum < 1, weight_decay >= 0, all finite */
+    float scale;                      /* of the orthogonal factor, >= 0; 0 = 0.2*sqrt(max(rows, cols)), which
+                                         gives the update the RMS of a typical AdamW update */
+    int32_t nesterov;
+    slide_ortho_params ortho;
+} slide_muon_hparams;
+
+/* Device bytes of the workspace that slide_orthogonalize and slide_muon_step
+ * need for this shape (any number of steps).  0 <= batch <= 65535, rows and
+ * cols at most 2^20, the smaller of the two at most 16384.
+ * Defined by: no passage; the pages describe no orthogonalised update. */
+SLIDE_API slide_status slide_ortho_workspace(int32_t batch, int32_t rows, int32_t cols, int64_t *bytes);
+
+/* The Newton-Schulz orthogonal factor of `batch` matrices.
+ *   x: device pointer to x_type values (BF16 or FP32); element (i, j) of
+ *     matrix b at b*x_batch_stride + i*x_row_stride + j, in elements
+ *     (x_batch_stride 0 repeats one matrix); row stride >= cols.  Aligned to
+ *     its type; four-element vectors are used where base and strides allow.
+ *   bf16_out: device pointer to BF16 values, strides likewise; the matrices
+ *     must not overlap.  May not overlap x.
+ *   workspace: device memory, 256-byte aligned, at least
+ *     slide_ortho_workspace bytes, contents irrelevant; in use until the
+ *     enqueued work has run, so calls that may overlap need one each.
+ * Stream-ordered on the current device; returns before the GPU finishes.
+ * Empty matrices or batches do nothing.
+ * Defined by: no passage; the pages describe no orthogonalised update. */
+SLIDE_API slide_status slide_orthogonalize(int32_t batch, int32_t rows, int32_t cols, const void *x, int32_t x_type,
+                                           int64_t x_row_stride, int64_t x_batch_stride, void *bf16_out,
+                                           int64_t out_row_stride, int64_t out_batch_stride,
+                                           const slide_ortho_params *params, void *workspace,
+                                           int64_t workspace_bytes, slide_stream_t stream);
+
+/* The Muon step of `batch` contiguous rows x cols matrices lying one after
+ * another: grad_replicas (host array of n_replicas device pointers, BF16 or
+ * FP32 by grads_type), master, momentum (FP32, updated in place) and bf16_out
+ * (BF16, written), each batch*rows*cols values, 16-byte aligned, caller-owned.
+ * The workspace is slide_orthogonalize's.  Stream-ordered.
+ * Defined by: "SlideDP: Scaling Host-Resident LLM Fine-Tuning Across Multiple
+ * GPUs", Core method (R replicas reduced on the GPU, one aggregated update of
+ * the FP32 master per iteration, cast to BF16 for the next delivery); the
+ * update rule itself is in no passage. */
+SLIDE_API slide_status slide_muon_step(int32_t batch, int32_t rows, int32_t cols, int32_t n_replicas,
+                                       const void *const *grad_replicas, int32_t grads_type, float *master,
+                                       float *momentum, void *bf16_out, const slide_muon_hparams *hp,
+                                       void *workspace, int64_t workspace_bytes, slide_stream_t stream);
+
+/* Status of the last slide_orthogonalize or slide_muon_step with this
+ * workspace: waits for `stream` and returns SLIDE_ERR_TIMEOUT if a bounded
+ * wait inside a product ran out (2 s; that call's results are undefined),
+ * else SLIDE_OK.
+ * Defined by: no passage; it completes the two calls above. */
+SLIDE_API slide_status slide_ortho_status(const void *workspace, slide_stream_t stream);
+
+/* `batch` matrices of rows x cols inside a layer's flat parameters. */
+typedef struct {
+    int64_t offset; /* of the first, in parameters; a multiple of 8 */
+    int32_t batch, rows, cols;
+} slide_matrix_block;
+
+/* One step of one layer (HBM residency) whose matrices are updated by Muon and
+ * the rest (norms, embeddings) by AdamW: each block as in slide_muon_step with
+ * the layer's m as momentum (its v is left alone), and every parameter outside
+ * the blocks as in slide_layer_step.  t_layer becomes t_layer + 1.
+ *   blocks: host array [n_blocks], ascending and disjoint; where parameters
+ *     follow a block, its end must be a multiple of 8 too.
+ *   adam: max_grad_norm must be <= 0 (an orthogonalised update has no use of
+ *     a gradient's norm).  States with SLIDE_FLAG_CHECK_FINITE are refused.
+ *   workspace: at least the largest slide_ortho_workspace of the blocks; the
+ *     blocks use it one after another.
+ * The other arguments as in slide_layer_step.  Trace events are not recorded.
+ * Defined by: the passages of slide_layer_step ("SlideDP: Scaling
+ * Host-Resident LLM Fine-Tuning Across Multiple GPUs", Core method); the
+ * update rule of the matrices is in no passage. */
+SLIDE_API slide_status slide_layer_muon_step(slide_state *st, int32_t layer, const slide_matrix_block *blocks,
+                                             int32_t n_blocks, const void *const *grad_replicas,
+                                             const slide_muon_hparams *muon, const slide_adam_hparams *adam,
+                                             void *workspace, int64_t workspace_bytes, slide_stream_t stream,
+                                             void *bf16_out);
+
+/* ---- Routing to experts -----------------------------------------------------
+ *
+ * For each token with logits x[0..E-1] (BF16 or FP32, computed in FP32):
+ *   s      = 1/(1 + exp(-x))  or  softmax(x)
+ *   key    = s + bias  (a softmax without a bias: key = x, whose order is the
+ *            same; sums of a group always use s)
+ *   groups: E/n_groups consecutive experts each; the top_groups best are kept,
+ *            ranked by the sum of their best two keys or by their best key
+ *   chosen = the top_k largest keys among the kept groups, largest first
+ *   w      = s[chosen];  w = w / (sum w + 1e-20) if renormalize;  w = w * scale
+ *   load[e] += number of tokens that chose e
+ * The bias only moves the choice, never the weights.  Ties go to the lowest
+ * index, for groups and experts.  Each line that enters a choice is one FP32
+ * operation, rounded.
+ *   - A token whose mask is 0 is not read: experts -1, weights 0, no load.
+ *   - An expert with logit or key -inf cannot be chosen; where fewer than
+ *     top_k are left, the last places hold expert -1 and weight 0.
+ *   - A logit of +inf counts as the largest finite value in a softmax.
+ *   - A NaN among a token's logits or keys gives experts -1 and weights NaN:
+ *     no expert is called for it, and the NaN shows. */
+enum { SLIDE_SCORE_SOFTMAX = 0, SLIDE_SCORE_SIGMOID = 1 };
+enum { SLIDE_GROUP_TOP2 = 0, SLIDE_GROUP_MAX = 1 };
+
+typedef struct {
+    int32_t n_experts;   /* 1..1024 */
+    int32_t top_k;       /* 1..32, at most the experts of top_groups groups */
+    int32_t score;       /* SLIDE_SCORE_* */
+    int32_t n_groups;    /* divides n_experts; 1 = no groups */
+    int32_t top_groups;  /* 1..n_groups */
+    int32_t group_score; /* SLIDE_GROUP_* */
+    int32_t renormalize;
+    float scale;         /* finite */
+} slide_route_config;
+
+/* Route `tokens` tokens.  logits: device, rows logits_stride elements apart;
+ * bias: FP32 [E] or NULL; token_mask: bytes [tokens] or NULL; weights FP32 and
+ * experts int32, [tokens][top_k] contiguous; load: int64 [E], added to, or
+ * NULL.  Pointers aligned to their types; 16-byte loads are used where base
+ * and stride allow.  Stream-ordered on the current device.
+ * Defined by: no passage; the pages name mixture-of-experts models only. */
+SLIDE_API slide_status slide_route_experts(int64_t tokens, const void *logits, int32_t logits_type,
+                                           int64_t logits_stride, const float *bias, const uint8_t *token_mask,
+                                           const slide_route_config *cfg, float *weights, int32_t *experts,
+                                           int64_t *load, slide_stream_t stream);
+
+/* Gradient of the weights with respect to the logits, the choice held fixed:
+ * d_logits (type of the logits, every element of its [tokens][E] written) from
+ * d_weights [tokens][top_k] and the experts that slide_route_experts chose.
+ * Places with an expert outside [0, E) and tokens whose mask is 0 contribute
+ * nothing.  The configuration's groups play no part.  d_logits must not
+ * overlap the logits.
+ * Defined by: no passage; the pages name mixture-of-experts models only. */
+SLIDE_API slide_status slide_route_experts_backward(int64_t tokens, const void *logits, int32_t logits_type,
+                                                    int64_t logits_stride, const int32_t *experts,
+                                                    const float *d_weights, const uint8_t *token_mask,
+                                                    const slide_route_config *cfg, void *d_logits,
+                                                    int64_t d_logits_stride, slide_stream_t stream);
+
+/* The balancing bias after a step's tokens: bias[e] += rate * sign(mean load -
+ * load[e]), compared in integers; then load = 0.  rate >= 0, finite.
+ * Defined by: no passage; the pages name mixture-of-experts models only. */
+SLIDE_API slide_status slide_route_bias_step(int32_t n_experts, int64_t *load, float *bias, float rate,
+                                             slide_stream_t stream);
+
 /* Message of the last error on this host thread ("" if none).
  * Defined by: no passage; error reporting of this C ABI. */
 SLIDE_API const char *slide_last_error(void);

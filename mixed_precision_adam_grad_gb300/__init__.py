@@ -13,7 +13,10 @@ from ._binding import (SlideError, SlideState, hparams, LIB_PATH,  # noqa: F401
                        slide_layer_set, slide_layer_get,
                        slide_layer_ptrs, slide_layer_last_clip_coef, slide_layer_status,
                        slide_trace_events, slide_adamw_step_noalloc, slide_noalloc_status,
-                       slide_streamed_timeline, slide_deliver_bf16)
+                       slide_streamed_timeline, slide_deliver_bf16, slide_ortho_workspace,
+                       slide_orthogonalize, slide_muon_step, slide_ortho_status, slide_layer_muon_step,
+                       slide_route_experts, slide_route_experts_backward, slide_route_bias_step,
+                       ortho_params, muon_hparams, route_config)
 
 
 def __getattr__(name):

@@ -40,6 +40,12 @@ SLIDE_FLAG_BF16_COPY_IN_HBM = 8
 SLIDE_FLAG_HOST_HUGE_PAGES = 16
 SLIDE_FLAG_HOST_INPUTS = 32
 SLIDE_MAX_REPLICAS = 8
+SLIDE_TYPE_BF16 = 0
+SLIDE_TYPE_FP32 = 1
+SLIDE_SCORE_SOFTMAX = 0
+SLIDE_SCORE_SIGMOID = 1
+SLIDE_GROUP_TOP2 = 0
+SLIDE_GROUP_MAX = 1
 SLIDE_DELIVER_FULL = 0
 SLIDE_DELIVER_SHARDED = 1
 
@@ -61,6 +67,24 @@ class slide_config(C.Structure):
                 ("window_layers", C.c_int32), ("device", C.c_int32),
                 ("timeout_ms", C.c_uint32), ("flags", C.c_uint32), ("chunk_bytes", C.c_int64),
                 ("chunk_bytes_d2h", C.c_int64), ("host_arena", C.c_void_p), ("host_arena_bytes", C.c_int64)]
+
+
+class slide_ortho_params(C.Structure):
+    _fields_ = [("steps", C.c_int32), ("coeffs", C.POINTER(C.c_float)), ("eps", C.c_float)]
+
+
+class slide_muon_hparams(C.Structure):
+    _fields_ = [("lr", C.c_float), ("momentum", C.c_float), ("weight_decay", C.c_float), ("scale", C.c_float),
+                ("nesterov", C.c_int32), ("ortho", slide_ortho_params)]
+
+
+class slide_matrix_block(C.Structure):
+    _fields_ = [("offset", C.c_int64), ("batch", C.c_int32), ("rows", C.c_int32), ("cols", C.c_int32)]
+
+
+class slide_route_config(C.Structure):
+    _fields_ = [("n_experts", C.c_int32), ("top_k", C.c_int32), ("score", C.c_int32), ("n_groups", C.c_int32),
+                ("top_groups", C.c_int32), ("group_score", C.c_int32), ("renormalize", C.c_int32), ("scale", C.c_float)]
 
 
 SLIDE_GRAD_FN = C.CFUNCTYPE(C.c_int, C.c_void_p, C.c_int32, C.POINTER(C.c_void_p), C.c_void_p)
@@ -110,6 +134,19 @@ def _load():
     L.slide_adamw_step_noalloc.restype = S
     L.slide_noalloc_status.argtypes = [P]
     L.slide_noalloc_status.restype = S
+    I, I64 = C.c_int32, C.c_int64
+    L.slide_ortho_workspace.argtypes = [I, I, I, C.POINTER(I64)]
+    L.slide_orthogonalize.argtypes = [I, I, I, P, I, I64, I64, P, I64, I64, C.POINTER(slide_ortho_params), P, I64, P]
+    L.slide_muon_step.argtypes = [I, I, I, I, C.POINTER(P), I, P, P, P, C.POINTER(slide_muon_hparams), P, I64, P]
+    L.slide_ortho_status.argtypes = [P, P]
+    L.slide_layer_muon_step.argtypes = [P, I, C.POINTER(slide_matrix_block), I, C.POINTER(P),
+                                        C.POINTER(slide_muon_hparams), C.POINTER(slide_adam_hparams), P, I64, P, P]
+    L.slide_route_experts.argtypes = [I64, P, I, I64, P, P, C.POINTER(slide_route_config), P, P, P, P]
+    L.slide_route_experts_backward.argtypes = [I64, P, I, I64, P, P, P, C.POINTER(slide_route_config), P, I64, P]
+    L.slide_route_bias_step.argtypes = [I, P, P, C.c_float, P]
+    for f in (L.slide_ortho_workspace, L.slide_orthogonalize, L.slide_muon_step, L.slide_ortho_status,
+              L.slide_layer_muon_step, L.slide_route_experts, L.slide_route_experts_backward, L.slide_route_bias_step):
+        f.restype = S
     L.slide_last_error.argtypes = []
     L.slide_last_error.restype = C.c_char_p
     L.slide_abi_version.argtypes = []
@@ -360,3 +397,120 @@ def slide_deliver_bf16(st: SlideState, layer: int, dst, route=SLIDE_DELIVER_FULL
     ptrs = [_ptr(d) for d in dst]
     arr = (C.c_void_p * max(1, len(ptrs)))(*ptrs)
     _check(_lib().slide_deliver_bf16(C.c_void_p(st.handle), layer, arr, len(ptrs), route, _stream(stream)))
+
+
+def _workspace(ws, workspace_bytes):
+    """(address, bytes) of a workspace: a tensor or array says its own size."""
+    if workspace_bytes is None:
+        if hasattr(ws, "numel"):
+            workspace_bytes = ws.numel() * ws.element_size()
+        elif ws is None:
+            workspace_bytes = 0
+        else:
+            raise TypeError("workspace_bytes is needed with an address")
+    return _ptr(ws), workspace_bytes
+
+
+def ortho_params(steps=5, coeffs=None, eps=1e-7) -> slide_ortho_params:
+    """coeffs: (a, b, c) for each step, or None for (3.4445, -4.7750, 2.0315)."""
+    p = slide_ortho_params(steps, None, eps)
+    if coeffs is not None:
+        flat = [float(x) for t in coeffs for x in t]
+        if len(flat) != 3 * steps:
+            raise ValueError("coeffs: one (a, b, c) for each step")
+        p._keep = (C.c_float * max(1, len(flat)))(*flat)
+        p.coeffs = C.cast(p._keep, C.POINTER(C.c_float))
+    return p
+
+
+def muon_hparams(lr=1e-5, momentum=0.95, weight_decay=0.01, scale=0.0, nesterov=True, steps=5, coeffs=None,
+                 eps=1e-7) -> slide_muon_hparams:
+    """scale 0: 0.2*sqrt(max(rows, cols))."""
+    o = ortho_params(steps, coeffs, eps)
+    hp = slide_muon_hparams(lr, momentum, weight_decay, scale, int(bool(nesterov)), o)
+    hp._keep = getattr(o, "_keep", None)
+    return hp
+
+
+def slide_ortho_workspace(batch: int, rows: int, cols: int) -> int:
+    out = C.c_int64()
+    _check(_lib().slide_ortho_workspace(batch, rows, cols, C.byref(out)))
+    return out.value
+
+
+def slide_orthogonalize(batch: int, rows: int, cols: int, x, bf16_out, params: slide_ortho_params, workspace,
+                        x_type=SLIDE_TYPE_BF16, x_row_stride=None, x_batch_stride=None, out_row_stride=None,
+                        out_batch_stride=None, workspace_bytes=None, stream=None) -> None:
+    """The Newton-Schulz orthogonal factor of a batch of matrices, in BF16.
+    Strides in elements; None = contiguous."""
+    ws, nbytes = _workspace(workspace, workspace_bytes)
+    xr = cols if x_row_stride is None else x_row_stride
+    orow = cols if out_row_stride is None else out_row_stride
+    _check(_lib().slide_orthogonalize(batch, rows, cols, _ptr(x), x_type, xr,
+                                      rows * xr if x_batch_stride is None else x_batch_stride, _ptr(bf16_out), orow,
+                                      rows * orow if out_batch_stride is None else out_batch_stride, C.byref(params),
+                                      ws, nbytes, _stream(stream)))
+
+
+def slide_muon_step(batch: int, rows: int, cols: int, grad_replicas, master, momentum, bf16_out,
+                    hp: slide_muon_hparams, workspace, grads_type=SLIDE_TYPE_BF16, workspace_bytes=None,
+                    stream=None) -> None:
+    """The Muon step of a batch of contiguous matrices (see include/slide.h)."""
+    ptrs = [_ptr(g) for g in grad_replicas]
+    arr = (C.c_void_p * max(1, len(ptrs)))(*ptrs)
+    ws, nbytes = _workspace(workspace, workspace_bytes)
+    _check(_lib().slide_muon_step(batch, rows, cols, len(ptrs), arr, grads_type, _ptr(master), _ptr(momentum),
+                                  _ptr(bf16_out), C.byref(hp), ws, nbytes, _stream(stream)))
+
+
+def slide_ortho_status(workspace, stream=None) -> int:
+    """Status of the last call with this workspace (SLIDE_OK or
+    SLIDE_ERR_TIMEOUT); raises on other errors."""
+    rc = _lib().slide_ortho_status(_ptr(workspace), _stream(stream))
+    if rc not in (SLIDE_OK, SLIDE_ERR_TIMEOUT):
+        _check(rc)
+    return rc
+
+
+def slide_layer_muon_step(st: SlideState, layer: int, blocks, grad_replicas, muon: slide_muon_hparams,
+                          adam: slide_adam_hparams, workspace, workspace_bytes=None, stream=None,
+                          bf16_out=None) -> None:
+    """blocks: (offset, batch, rows, cols) of the layer's matrices, ascending;
+    they are updated by Muon, everything else by AdamW."""
+    ptrs = [_ptr(g) for g in grad_replicas]
+    arr = (C.c_void_p * max(1, len(ptrs)))(*ptrs)
+    bl = (slide_matrix_block * max(1, len(blocks)))(*[slide_matrix_block(*b) for b in blocks])
+    ws, nbytes = _workspace(workspace, workspace_bytes)
+    _check(_lib().slide_layer_muon_step(C.c_void_p(st.handle), layer, bl, len(blocks), arr, C.byref(muon),
+                                        C.byref(adam), ws, nbytes, _stream(stream), _ptr(bf16_out)))
+
+
+def route_config(n_experts: int, top_k: int, score=SLIDE_SCORE_SIGMOID, n_groups=1, top_groups=1,
+                 group_score=SLIDE_GROUP_TOP2, renormalize=True, scale=1.0) -> slide_route_config:
+    return slide_route_config(n_experts, top_k, score, n_groups, top_groups, group_score, int(bool(renormalize)), scale)
+
+
+def slide_route_experts(tokens: int, logits, weights, experts, cfg: slide_route_config, bias=None, token_mask=None,
+                        load=None, logits_type=SLIDE_TYPE_FP32, logits_stride=None, stream=None) -> None:
+    """Scores, choice and weights of each token's experts (see include/slide.h)."""
+    _check(_lib().slide_route_experts(tokens, _ptr(logits), logits_type,
+                                      cfg.n_experts if logits_stride is None else logits_stride, _ptr(bias),
+                                      _ptr(token_mask), C.byref(cfg), _ptr(weights), _ptr(experts), _ptr(load),
+                                      _stream(stream)))
+
+
+def slide_route_experts_backward(tokens: int, logits, experts, d_weights, d_logits, cfg: slide_route_config,
+                                 token_mask=None, logits_type=SLIDE_TYPE_FP32, logits_stride=None,
+                                 d_logits_stride=None, stream=None) -> None:
+    """d_logits from d_weights, the choice held fixed."""
+    _check(_lib().slide_route_experts_backward(tokens, _ptr(logits), logits_type,
+                                               cfg.n_experts if logits_stride is None else logits_stride,
+                                               _ptr(experts), _ptr(d_weights), _ptr(token_mask), C.byref(cfg),
+                                               _ptr(d_logits),
+                                               cfg.n_experts if d_logits_stride is None else d_logits_stride,
+                                               _stream(stream)))
+
+
+def slide_route_bias_step(n_experts: int, load, bias, rate: float, stream=None) -> None:
+    """bias += rate * sign(mean load - load); load = 0."""
+    _check(_lib().slide_route_bias_step(n_experts, _ptr(load), _ptr(bias), rate, _stream(stream)))

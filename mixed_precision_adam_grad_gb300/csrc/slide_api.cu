@@ -586,6 +586,96 @@ slide_status slide_layer_step(slide_state *st, int32_t layer, const void *const 
     return rc;
 }
 
+slide_status slide_layer_muon_step(slide_state *st, int32_t layer, const slide_matrix_block *blocks,
+                                   int32_t n_blocks, const void *const *grad_replicas,
+                                   const slide_muon_hparams *muon, const slide_adam_hparams *adam, void *workspace,
+                                   int64_t workspace_bytes, slide_stream_t stream, void *bf16_out)
+{
+    slide_status rc = check_layer(st, layer);
+    if (rc != SLIDE_OK)
+        return rc;
+    if (st->cfg.residency != SLIDE_RESIDENCY_HBM)
+        return fail(SLIDE_ERR_STATE, "slide_layer_muon_step needs the HBM residency");
+    if (st->cfg.flags & SLIDE_FLAG_CHECK_FINITE)
+        return fail(SLIDE_ERR_STATE, "slide_layer_muon_step does not support SLIDE_FLAG_CHECK_FINITE");
+    if ((rc = check_muon_hparams(muon)) != SLIDE_OK || (rc = check_hparams(adam)) != SLIDE_OK)
+        return rc;
+    if (adam->max_grad_norm > 0.0f)
+        return fail(SLIDE_ERR_INVALID_ARG, "slide_layer_muon_step has no clip: max_grad_norm must be <= 0");
+    if (n_blocks < 0 || (n_blocks > 0 && !blocks))
+        return fail(SLIDE_ERR_INVALID_ARG, "n_blocks < 0 or blocks is NULL");
+    if (!grad_replicas)
+        return fail(SLIDE_ERR_INVALID_ARG, "grad_replicas is NULL");
+    LayerState &L = st->layers[layer];
+    const int R = st->cfg.n_replicas;
+    const bool f32g = (st->cfg.flags & SLIDE_FLAG_FP32_GRADS) != 0;
+    const size_t gsize = f32g ? 4 : 2;
+    for (int r = 0; r < R; ++r)
+        if (L.n > 0 && (!grad_replicas[r] || !aligned16(grad_replicas[r])))
+            return fail(SLIDE_ERR_INVALID_ARG, "gradient replica pointer is NULL or not 16-byte aligned");
+    uint16_t *w = bf16_out ? (uint16_t *)bf16_out : L.w;
+    if (!aligned16(w))
+        return fail(SLIDE_ERR_INVALID_ARG, "bf16_out is not 16-byte aligned");
+    // every block is checked before anything is enqueued
+    int64_t end = 0, need = 0;
+    for (int32_t k = 0; k < n_blocks; ++k) {
+        const slide_matrix_block &b = blocks[k];
+        int64_t bytes = 0;
+        if ((rc = slide_ortho_workspace(b.batch, b.rows, b.cols, &bytes)) != SLIDE_OK)
+            return rc;
+        const int64_t each = (int64_t)b.rows * b.cols;
+        if (b.offset < end || b.offset % 8 != 0 || b.offset > L.n || (each > 0 && b.batch > (L.n - b.offset) / each))
+            return fail(SLIDE_ERR_INVALID_ARG, "blocks must be ascending, disjoint, inside the layer, at multiples of 8");
+        if (b.offset > end && end % 8 != 0)
+            return fail(SLIDE_ERR_INVALID_ARG, "a block that parameters follow must end at a multiple of 8");
+        end = b.offset + each * b.batch;
+        if (each > 0 && b.batch > 0 && bytes > need)
+            need = bytes;
+    }
+    if (end < L.n && end % 8 != 0)
+        return fail(SLIDE_ERR_INVALID_ARG, "a block that parameters follow must end at a multiple of 8");
+    if (need > 0 && (!workspace || ((uintptr_t)workspace & 255u) != 0 || workspace_bytes < need))
+        return fail(SLIDE_ERR_INVALID_ARG, "workspace is NULL, not 256-byte aligned or too small for the blocks");
+    DeviceGuard guard(st->device);
+    if (!guard.ok)
+        return fail(SLIDE_ERR_CUDA, "cudaSetDevice failed");
+    const int64_t t = L.t + 1;
+    const AdamScalars sc = adam_scalars_for(*adam, t);
+    auto replicas_at = [&](int64_t off) {
+        ReplicaPtrs g{};
+        for (int r = 0; r < R; ++r)
+            g.p[r] = (const char *)grad_replicas[r] + off * (int64_t)gsize;
+        return g;
+    };
+    auto adam_range = [&](int64_t from, int64_t to) {
+        if (from >= to)
+            return SLIDE_OK;
+        cudaError_t e = launch_grad_reduce_adamw_cast(
+            replicas_at(from), R, to - from, L.theta + from, L.m + from, L.v + from, w + from, sc, &L.scratch, 0, 0.0f,
+            false, st->device, (cudaStream_t)stream, (st->cfg.flags & SLIDE_FLAG_TEST_PIPELINE_STALL) != 0, f32g);
+        return e == cudaSuccess ? SLIDE_OK : fail_cuda(e, "grad_reduce_adamw_cast launch");
+    };
+    int64_t done = 0;
+    for (int32_t k = 0; k < n_blocks && rc == SLIDE_OK; ++k) {
+        const slide_matrix_block &b = blocks[k];
+        rc = adam_range(done, b.offset);
+        if (rc == SLIDE_OK) {
+            const ReplicaPtrs g = replicas_at(b.offset);
+            rc = slide_muon_step(b.batch, b.rows, b.cols, R, g.p, f32g ? SLIDE_TYPE_FP32 : SLIDE_TYPE_BF16,
+                                 L.theta + b.offset, L.m + b.offset, w + b.offset, muon, workspace, workspace_bytes,
+                                 stream);
+        }
+        done = b.offset + (int64_t)b.rows * b.cols * b.batch;
+    }
+    if (rc == SLIDE_OK)
+        rc = adam_range(done, L.n);
+    if (rc != SLIDE_OK)
+        return rc;
+    L.t = t;
+    clear_error();
+    return SLIDE_OK;
+}
+
 slide_status slide_layer_step_host(slide_state *st, int32_t layer, const void *const *host_grad_replicas,
                                    const slide_adam_hparams *hp, slide_stream_t stream, void *host_bf16_out)
 {

@@ -80,6 +80,7 @@ void clear_error();
 // Per-step scalars for update t (1-based) from the FP32 hyper-parameters.
 AdamScalars adam_scalars_for(const slide_adam_hparams &hp, int64_t t);
 slide_status check_hparams(const slide_adam_hparams *hp);
+slide_status check_muon_hparams(const slide_muon_hparams *hp);  // ortho.cu
 
 // Most copy-in or write-back chunks a streamed unit may have.
 constexpr int64_t kMaxChunksPerUnit = 65536;
