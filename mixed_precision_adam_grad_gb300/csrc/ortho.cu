@@ -21,11 +21,12 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
-#include <cstring>
+#include <cstdlib>
 
 #include "slide.h"
 #include "slide_ortho.h"
 #include "slide_state.h"
+#include "sm103_ptx.h"
 
 namespace slide {
 namespace {
@@ -41,47 +42,58 @@ constexpr int kPrepThreads = 256;
 // ---- preparation ------------------------------------------------------------
 
 struct SourceArgs {
-    // kSrcMatrix: x; kSrcMuon: g[0..R-1] and the momentum
-    ReplicaPtrs g;
+    ReplicaPtrs g;            // the matrix, or the R replicas of a Muon step
     int R;
     int64_t row_stride, batch_stride;
-    float *mom;
+    int rows, cols;
+    int rblk, cblk;           // blocks of 128
+    int vec;                  // rows can be read eight values at a time
+    // Muon step only: contiguous
+    float *mom, *u;
     float mu, one_minus_mu;
     int nesterov;
-    int rows, cols;
-    int rblk, cblk, c32;      // blocks of 128; T32 tiles of a row block
-    int64_t out_stride;
-    float *out;               // T32, not normalised
     double *parts;            // [batch][kNormParts]
-    int vec;                  // rows can be read four values at a time
     unsigned *status;
 };
 
 __device__ __forceinline__ float widen(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
 __device__ __forceinline__ float widen(float x) { return x; }
 
+// Values at .. at+7 of a row, of which n lie inside it.
 template <typename T>
-__device__ __forceinline__ void load4(const void *base, int64_t at, int n, bool vec, float (&v)[4])
+__device__ __forceinline__ void load8(const void *base, int64_t at, int n, bool vec, float (&v)[8])
 {
     const T *p = static_cast<const T *>(base) + at;
-    if (vec && n == 4) {
+    if (vec && n >= 8) {
         if constexpr (sizeof(T) == 2) {
-            const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(p));
-            v[0] = __uint_as_float(w.x << 16);
-            v[1] = __uint_as_float(w.x & 0xffff0000u);
-            v[2] = __uint_as_float(w.y << 16);
-            v[3] = __uint_as_float(w.y & 0xffff0000u);
+            const uint4 w = *reinterpret_cast<const uint4 *>(p);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[2 * e] = __uint_as_float(u[e] << 16);
+                v[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+            }
         } else {
-            const float4 w = __ldcs(reinterpret_cast<const float4 *>(p));
-            v[0] = w.x;
-            v[1] = w.y;
-            v[2] = w.z;
-            v[3] = w.w;
+            const float4 w = *reinterpret_cast<const float4 *>(p), x = *reinterpret_cast<const float4 *>(p + 4);
+            v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w, v[4] = x.x, v[5] = x.y, v[6] = x.z, v[7] = x.w;
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < 8; ++e)
             v[e] = e < n ? widen(p[e]) : 0.0f;
+    }
+}
+
+__device__ __forceinline__ void store8(float *p, int n, bool vec, const float (&v)[8])
+{
+    if (vec && n >= 8) {
+        reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n)
+                p[e] = v[e];
     }
 }
 
@@ -103,64 +115,57 @@ __device__ __forceinline__ double block_sum(double x)
     return t;
 }
 
-// Reads the matrix (or forms Muon's update from the replicas and the
-// momentum), writes it in T32 tiles, zero beyond its edges, and a partial sum
-// of its squares per block.
+// A block of threads passes over 128 x 128 blocks of a matrix; a thread has
+// eight columns of every 16th row.
+constexpr int kRowsAtOnce = kPrepThreads / 16;
+
+// A partial sum of the matrix's squares per block of threads; for a Muon step
+// the squares are those of the update, which is formed from the replicas and
+// the momentum on the way and kept in u.
 template <typename T, bool MUON>
 __global__ void __launch_bounds__(kPrepThreads) k_ortho_source(const __grid_constant__ SourceArgs a)
 {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
-    if (blockIdx.x == 0 && b == 0 && threadIdx.x == 0)
-        *a.status = 0;
+    const int b = blockIdx.y, r0 = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * 8;
+    ptx::launch_dependents();
+    if (blockIdx.x == 0 && b == 0 && threadIdx.x <= kMaxPhases)
+        a.status[threadIdx.x] = 0;
     double sum = 0.0;
     for (int blk = blockIdx.x; blk < a.rblk * a.cblk; blk += gridDim.x) {
         const int rb = blk / a.cblk, cb = blk - rb * a.cblk;
-        const int col = cb * 128 + lane * 4;
-        const int n = min(4, a.cols - col);
+        const int col = cb * 128 + c0, n = a.cols - col;
         float part = 0.0f;
-        for (int r = warp; r < 128; r += kPrepThreads / 32) {
-            const int row = rb * 128 + r;
-            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (row < a.rows && n > 0) {
+        if (n > 0) {
+#pragma unroll MUON ? 1 : 4
+            for (int r = r0; r < 128; r += kRowsAtOnce) {
+                const int row = rb * 128 + r;
+                if (row >= a.rows)
+                    break;
                 const int64_t at = (int64_t)b * a.batch_stride + (int64_t)row * a.row_stride + col;
+                float v[8];
+                load8<T>(a.g.p[0], at, n, a.vec, v);
                 if constexpr (MUON) {
-                    float m[4];
-                    load4<T>(a.g.p[0], at, n, a.vec, v);
+                    float m[8];
+                    load8<float>(a.mom, at, n, a.vec, m);
                     for (int k = 1; k < a.R; ++k) {
-                        float w[4];
-                        load4<T>(a.g.p[k], at, n, a.vec, w);
+                        float w[8];
+                        load8<T>(a.g.p[k], at, n, a.vec, w);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
+                        for (int e = 0; e < 8; ++e)
                             v[e] = __fadd_rn(v[e], w[e]);
                     }
-                    load4<float>(a.mom, at, n, a.vec, m);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int e = 0; e < 8; ++e) {
                         const float g = __fmul_rn(a.one_minus_mu, __fdiv_rn(v[e], (float)a.R));
                         m[e] = __fadd_rn(__fmul_rn(m[e], a.mu), g);
                         v[e] = a.nesterov ? __fadd_rn(__fmul_rn(m[e], a.mu), g) : m[e];
                     }
-                    if (a.vec && n == 4) {
-                        __stcs(reinterpret_cast<float4 *>(a.mom + at), make_float4(m[0], m[1], m[2], m[3]));
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if (e < n)
-                                a.mom[at + e] = m[e];
-                            else
-                                v[e] = 0.0f;
-                        }
-                    }
-                } else {
-                    load4<T>(a.g.p[0], at, n, a.vec, v);
+                    store8(a.mom + at, n, a.vec, m);
+                    store8(a.u + at, n, a.vec, v);
                 }
-            }
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                part = fmaf(v[e], v[e], part);
-            float *tile = a.out + (int64_t)b * a.out_stride +
-                          ((int64_t)rb * a.c32 + cb * 4 + (lane >> 3)) * kTileElems32 + r * 32;
-            reinterpret_cast<float4 *>(tile)[(lane & 7) ^ (r & 7)] = make_float4(v[0], v[1], v[2], v[3]);
+                for (int e = 0; e < 8; ++e)
+                    part = fmaf(v[e], v[e], part);
+            }
         }
         sum += (double)part;
     }
@@ -170,49 +175,57 @@ __global__ void __launch_bounds__(kPrepThreads) k_ortho_source(const __grid_cons
 }
 
 struct ScaleArgs {
-    const float *x;   // T32
-    __half *out;      // T16
-    int64_t x_stride;
-    int tiles;        // T16 tiles per matrix (the padding's among them)
+    const void *x;
+    int64_t row_stride, batch_stride;
+    int rows, cols, rblk, cblk, vec;
+    OrthoPair out;
+    int c64;           // tiles of a row block
+    int64_t out_stride;
     int n_parts;
     const double *parts;
-    float *inv;       // [batch]
     float eps, scale;
 };
 
-// inv = 1 / (|G|_F + eps), and the normalised matrix as FP16 operands.
-__global__ void __launch_bounds__(kPrepThreads) k_ortho_scale(const ScaleArgs a)
+// X = G / (|G|_F + eps) as a pair of FP16 matrices in tiles, zero beyond the
+// matrix's edges.
+template <typename T>
+__global__ void __launch_bounds__(kPrepThreads) k_ortho_scale(const __grid_constant__ ScaleArgs a)
 {
     __shared__ float s_inv;
-    const int b = blockIdx.y;
+    const int b = blockIdx.y, r0 = threadIdx.x >> 4, c8 = threadIdx.x & 15;
+    ptx::launch_dependents();
+    ptx::wait_for_previous_grid();
     double x = 0.0;
     for (int i = threadIdx.x; i < a.n_parts; i += kPrepThreads)
         x += a.parts[(int64_t)b * kNormParts + i];
     x = block_sum(x);
-    if (threadIdx.x == 0) {
-        s_inv = (float)(1.0 / (sqrt(x) + (double)a.eps));
-        if (x == 0.0 && a.eps == 0.0f)
-            s_inv = 0.0f;  // a matrix of zeros stays one
-        if (blockIdx.x == 0)
-            a.inv[b] = s_inv;
-    }
+    if (threadIdx.x == 0)  // a matrix of zeros stays one, whatever eps
+        s_inv = x == 0.0 && a.eps == 0.0f ? 0.0f : (float)(1.0 / (sqrt(x) + (double)a.eps));
     __syncthreads();
     const float inv = s_inv, scale = a.scale;
-    for (int t = blockIdx.x; t < a.tiles; t += gridDim.x) {
-        const float4 *src = reinterpret_cast<const float4 *>(a.x + (int64_t)b * a.x_stride + (int64_t)t * kTileElems16);
-        uint4 *dst = reinterpret_cast<uint4 *>(a.out + (int64_t)b * a.x_stride + (int64_t)t * kTileElems16);
-        for (int i = threadIdx.x; i < kTileElems16 / 8; i += kPrepThreads) {
-            const int r = i >> 3, c = (i & 7) ^ (r & 7);  // chunk c (8 columns) of row r
-            const float4 *row = src + (c >> 2) * (kTileElems32 / 4) + r * 8;
-            const float4 u = row[(2 * (c & 3)) ^ (r & 7)], w = row[(2 * (c & 3) + 1) ^ (r & 7)];
-            const float f[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
-            uint32_t h[4];
+    for (int blk = blockIdx.x; blk < a.rblk * a.cblk; blk += gridDim.x) {
+        const int rb = blk / a.cblk, cb = blk - rb * a.cblk;
+        const int col = cb * 128 + c8 * 8, n = a.cols - col;
+        const int64_t tile = (int64_t)b * a.out_stride + ((int64_t)rb * a.c64 + 2 * cb + (c8 >> 3)) * kTileElems;
+#pragma unroll 4
+        for (int r = r0; r < 128; r += kRowsAtOnce) {
+            const int row = rb * 128 + r;
+            float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+            if (row < a.rows && n > 0)
+                load8<T>(a.x, (int64_t)b * a.batch_stride + (int64_t)row * a.row_stride + col, n, a.vec, v);
+            uint32_t hi[4], lo[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const __half2 p = __floats2half2_rn(f[2 * e] * inv * scale, f[2 * e + 1] * inv * scale);
-                h[e] = *reinterpret_cast<const uint32_t *>(&p);
+                const float y = v[2 * e] * inv * scale, z = v[2 * e + 1] * inv * scale;
+                const __half2 p = __floats2half2_rn(y, z);
+                const float2 f = __half22float2(p);
+                const __half2 q = __floats2half2_rn((y - f.x) * kLoScale, (z - f.y) * kLoScale);
+                hi[e] = *reinterpret_cast<const uint32_t *>(&p);
+                lo[e] = *reinterpret_cast<const uint32_t *>(&q);
             }
-            dst[i] = make_uint4(h[0], h[1], h[2], h[3]);
+            const int64_t at = tile + r * 64 + (((c8 & 7) ^ (r & 7)) * 8);
+            *reinterpret_cast<uint4 *>(a.out.hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(a.out.lo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
     }
 }
@@ -252,16 +265,16 @@ Shape shape_of(int batch, int rows, int cols)
 }
 
 struct Work {
-    unsigned *status;
-    float *inv;
+    unsigned *status;          // and the phases' counters
     double *parts;
-    float *x32;
-    __half *x16[2];
-    __half *g16, *o16;
-    float *d;
+    __half *x_hi[2], *x_lo;
+    float *u;                  // a Muon step's update
+    OrthoPair g;
+    __half *o[2];              // B without its diagonal, of this step and the one before
+    float *d[2];               // a + the diagonal of B
     // grouped form
-    __half *t16, *q16[2];
-    float *g32, *t32, *q32, *dq;
+    OrthoPair t, q[2];
+    float *dq;
     int64_t x_elems, m_elems;  // per matrix
     int64_t bytes;
 };
@@ -278,24 +291,32 @@ Work layout(const Shape &s, char *base)
     w.x_elems = (int64_t)s.rpad * s.cpad * 128 * 128;
     w.m_elems = (int64_t)s.mpad * s.mpad * 128 * 128;
     const int64_t xb = w.x_elems * s.batch, mb = w.m_elems * s.batch;
-    w.status = (unsigned *)take(4);
-    w.inv = (float *)take(4 * (int64_t)s.batch);
+    auto pair = [&](int64_t n) {
+        OrthoPair p;
+        p.hi = (__half *)take(2 * n);
+        p.lo = (__half *)take(2 * n);
+        return p;
+    };
+    w.status = (unsigned *)take(4 * (1 + kMaxPhases));
     w.parts = (double *)take(8 * (int64_t)s.batch * kNormParts);
-    w.x32 = (float *)take(4 * xb);
-    w.x16[0] = (__half *)take(2 * xb);
-    w.x16[1] = (__half *)take(2 * xb);
-    w.g16 = (__half *)take(2 * mb);
-    w.o16 = (__half *)take(2 * mb);
-    w.d = (float *)take(4 * (int64_t)s.batch * s.mpad * 128);
+    w.x_hi[0] = (__half *)take(2 * xb);
+    w.x_lo = (__half *)take(2 * xb);
+    w.g = pair(mb);
+    const int64_t db = 4 * (int64_t)s.batch * s.mpad * 128;
+    w.o[0] = (__half *)take(2 * mb);
+    w.d[0] = (float *)take(db);
     if (s.grouped) {
-        w.t16 = (__half *)take(2 * mb);
-        w.q16[0] = (__half *)take(2 * mb);
-        w.q16[1] = (__half *)take(2 * mb);
-        w.g32 = (float *)take(4 * mb);
-        w.t32 = (float *)take(4 * mb);
-        w.q32 = (float *)take(4 * mb);
-        w.dq = (float *)take(4 * (int64_t)s.batch * s.mpad * 128);
+        w.o[1] = (__half *)take(2 * mb);
+        w.d[1] = (float *)take(db);
+        w.t = pair(mb);
+        w.q[0] = pair(mb);
+        w.q[1] = pair(mb);
+        w.dq = (float *)take(db);
     }
+    // the update is read before the first product writes the second copy of X
+    w.x_hi[1] = (__half *)take(2 * xb > 4 * (int64_t)s.batch * s.rows * s.cols ? 2 * xb
+                                                                               : 4 * (int64_t)s.batch * s.rows * s.cols);
+    w.u = (float *)w.x_hi[1];
     w.bytes = off;
     return w;
 }
@@ -364,21 +385,30 @@ struct Finish {
 
 bool test_stall() { return getenv("SLIDE_TEST_PIPELINE_STALL") != nullptr; }
 
-// The products, from the matrix in w.x32 and w.x16[0] to the caller's array.
+// The products, from the matrix in x_hi[0] and x_lo to the caller's array.
 cudaError_t enqueue_products(const Shape &s, const Work &w, const Schedule &sc, const Finish &f, int device,
                              cudaStream_t stream)
 {
     const int xc64 = 2 * s.cpad, mc64 = 2 * s.mpad, mdim = s.mpad * 128;
     const int kn = s.tall ? (s.rows + 63) / 64 : (s.cols + 63) / 64;
     const int km = (s.m + 63) / 64;
-    const bool stall = test_stall();
+
+    OrthoPlan plan{};
+    plan.batch = s.batch;
+    plan.status = w.status;
+    plan.rows = s.rows;
+    plan.cols = s.cols;
+    plan.w = f.w;
+    plan.w_row = f.w_row;
+    plan.w_batch = f.w_batch;
+    plan.theta = f.theta;
+    plan.decay = f.decay;
+    plan.step = f.step;
+    plan.test_stall = test_stall();
 
     OrthoGemm base{};
     base.nprob = 1;
-    base.batch = s.batch;
     base.d_stride = mdim;
-    base.status = w.status;
-    base.test_stall = stall;
 
     OrthoGemm mm = base;  // a symmetric m x m product of symmetric factors
     mm.a_kind = mm.b_kind = kOperandSym;
@@ -388,11 +418,23 @@ cudaError_t enqueue_products(const Shape &s, const Work &w, const Schedule &sc, 
     mm.mblk = mm.nblk = s.mblk;
     mm.sym = 1;
 
+    auto add = [&](const OrthoGemm &g, int epi) {
+        plan.ph[plan.n_phases] = g;
+        plan.ph[plan.n_phases++].epi = epi;
+    };
     int cur = 0;
-    cudaError_t e = cudaSuccess;
     for (int k0 = 0; k0 < sc.steps;) {
         const int p = s.grouped ? (sc.steps - k0 < kGroupSteps ? sc.steps - k0 : kGroupSteps) : 1;
         const bool last = k0 + p == sc.steps;
+        if (plan.n_phases + 3 * kGroupSteps + 1 > kMaxPhases) {
+            // the next group goes into a launch of its own, whose counters start at zero again
+            cudaError_t e = launch_ortho_products(plan, device, stream);
+            if (e == cudaSuccess)
+                e = cudaMemsetAsync(w.status + 1, 0, sizeof(unsigned) * kMaxPhases, stream);
+            if (e != cudaSuccess)
+                return e;
+            plan.n_phases = 0;
+        }
         // G = X X^T (wide) or X^T X (tall)
         OrthoGemm g = base;
         g.a_kind = g.b_kind = s.tall ? kOperandMN : kOperandK;
@@ -403,115 +445,134 @@ cudaError_t enqueue_products(const Shape &s, const Work &w, const Schedule &sc, 
         g.sym = 1;
         g.out_c64 = mc64;
         g.out_stride = w.m_elems;
-        g.alpha = 1.0f / (sc.sx[k0] * sc.sx[k0]);
-        g.s16 = sc.sg[k0];
-        g.p[0].a = g.p[0].b = w.x16[cur];
-        g.p[0].out16 = w.g16;
-        g.p[0].out32 = p > 1 ? w.g32 : nullptr;
-        if ((e = launch_ortho_gemm(g, kEpiGram, device, stream)) != cudaSuccess)
-            return e;
+        g.p[0].a = g.p[0].b = w.x_hi[cur];
+        g.p[0].alpha = 1.0f / (sc.sx[k0] * sc.sx[k0]);
+        g.p[0].out.hi = w.g.hi;
+        g.p[0].out.lo = p > 1 ? w.g.lo : nullptr;
+        g.p[0].s_out = sc.sg[k0];
+        add(g, kEpiGram);
         int qcur = 0;
         for (int j = 0; j < p; ++j) {
-            const int k = k0 + j;
+            const int k = k0 + j, now = j & 1;
             const float sg = sc.sg[k];
             // B = bG + cG^2
             OrthoGemm b = mm;
-            b.alpha = sc.c[k] / (sg * sg);
-            b.c16_scale = sc.b[k] / sg;
             b.coef_a = sc.a[k];
-            b.s16 = sg;
-            b.s16b = 1.0f;
-            b.p[0].a = b.p[0].b = b.p[0].c16 = w.g16;
-            b.p[0].out16 = w.o16;
-            b.p[0].dvec_out = w.d;
-            if (j == 0 && p > 1) {
-                b.p[0].out32 = w.q32;
-                b.p[0].out16b = w.q16[0];
-            }
-            if ((e = launch_ortho_gemm(b, kEpiPoly, device, stream)) != cudaSuccess)
-                return e;
+            b.p[0].a = b.p[0].b = w.g.hi;
+            b.p[0].c = w.g;
+            b.p[0].alpha = sc.c[k] / (sg * sg);
+            b.p[0].c_scale = sc.b[k] / sg;
+            b.p[0].out.hi = w.o[now];
+            b.p[0].s_out = sg;
+            b.p[0].dvec_out = w.d[now];
+            add(b, kEpiPoly);
             if (p == 1)
                 break;
-            if (j > 0) {  // Q <- R Q
-                OrthoGemm q = mm;
-                q.alpha = 1.0f / sg;
-                q.s16 = 1.0f;
-                q.diag_out = j + 1 == p;
-                q.p[0].a = w.o16;
-                q.p[0].b = w.q16[qcur];
-                q.p[0].c32 = w.q32;
-                q.p[0].dvec = w.d;
-                q.p[0].out32 = j + 1 == p ? nullptr : w.q32;
-                q.p[0].out16 = w.q16[qcur ^ 1];
-                q.p[0].dvec_out = w.dq;
-                if ((e = launch_ortho_gemm(q, kEpiSym, device, stream)) != cudaSuccess)
-                    return e;
+            // with R = aI + B = diag(d) + O: T = R G and Q <- R Q, in one launch
+            OrthoGemm t = mm;
+            t.nprob = 0;
+            if (j + 1 < p) {
+                OrthoProduct &x = t.p[t.nprob++];
+                x.a = w.o[now];
+                x.b = w.g.hi;
+                x.c = w.g;
+                x.c_scale = 1.0f / sg;
+                x.dvec = w.d[now];
+                x.alpha = 1.0f / (sg * sg);
+                x.out = w.t;
+                x.s_out = sg;
+            }
+            if (j > 0) {
+                OrthoProduct &x = t.p[t.nprob++];
+                x.a = w.o[now];
+                x.dvec = w.d[now];
+                if (j == 1) {  // Q is the first step's R still: (d + O)(d' + O')
+                    const float s0 = sc.sg[k0];
+                    x.b = x.c.hi = w.o[0];
+                    x.c.lo = w.o[1];
+                    x.c_scale = 1.0f / s0;
+                    x.c_scale2 = 1.0f / sg;
+                    x.dvec2 = w.d[0];
+                    x.alpha = 1.0f / (sg * s0);
+                } else {
+                    x.b = w.q[qcur].hi;
+                    x.c = w.q[qcur];
+                    x.c_scale = 1.0f;
+                    x.alpha = 1.0f / sg;
+                }
+                x.out.hi = w.q[qcur ^ 1].hi;
+                x.out.lo = j + 1 < p ? w.q[qcur ^ 1].lo : nullptr;
+                x.s_out = 1.0f;
+                x.diag_out = j + 1 == p;
+                x.dvec_out = w.dq;
                 qcur ^= 1;
             }
-            if (j + 1 < p) {
-                OrthoGemm t = mm;  // T = R G
-                t.alpha = 1.0f / (sg * sg);
-                t.s16 = sg;
-                t.p[0].a = w.o16;
-                t.p[0].b = w.g16;
-                t.p[0].c32 = w.g32;
-                t.p[0].dvec = w.d;
-                t.p[0].out32 = w.t32;
-                t.p[0].out16 = w.t16;
-                if ((e = launch_ortho_gemm(t, kEpiSym, device, stream)) != cudaSuccess)
-                    return e;
-                t.s16 = sc.sg[k + 1];  // G <- R T
-                t.p[0].b = w.t16;
-                t.p[0].c32 = w.t32;
-                t.p[0].out32 = j + 2 < p ? w.g32 : nullptr;
-                t.p[0].out16 = w.g16;
-                if ((e = launch_ortho_gemm(t, kEpiSym, device, stream)) != cudaSuccess)
-                    return e;
+            if (t.nprob > 0)
+                add(t, kEpiSym);
+            if (j + 1 < p) {  // G <- R T
+                OrthoGemm n = mm;
+                OrthoProduct &x = n.p[0];
+                x.a = w.o[now];
+                x.b = w.t.hi;
+                x.c = w.t;
+                x.c_scale = 1.0f / sg;
+                x.dvec = w.d[now];
+                x.alpha = 1.0f / (sg * sg);
+                x.out = w.g;
+                x.s_out = sc.sg[k + 1];
+                add(n, kEpiSym);
             }
         }
-        // X <- Q X, the diagonal of Q on the FP32 copy of X
+        // X <- Q X, the diagonal of Q on both halves of X
         OrthoGemm x = base;
-        const __half *q16 = p == 1 ? w.o16 : w.q16[qcur];
+        const __half *q = p == 1 ? w.o[0] : w.q[qcur].hi;
         x.a_kind = s.tall ? kOperandK : kOperandSym;
         x.b_kind = s.tall ? kOperandSym : kOperandMN;
         x.a_c64 = s.tall ? xc64 : mc64;
         x.b_c64 = s.tall ? mc64 : xc64;
         x.a_stride = s.tall ? w.x_elems : w.m_elems;
         x.b_stride = s.tall ? w.m_elems : w.x_elems;
-        x.p[0].a = s.tall ? w.x16[cur] : q16;
-        x.p[0].b = s.tall ? q16 : w.x16[cur];
         x.k64 = km;
         x.mblk = s.rblk;
         x.nblk = s.cblk;
         x.out_c64 = xc64;
         x.out_stride = w.x_elems;
         x.d_by_col = s.tall;
-        x.alpha = 1.0f / ((p == 1 ? sc.sg[k0] : 1.0f) * sc.sx[k0]);
-        x.c_inv = k0 == 0 ? w.inv : nullptr;
-        x.p[0].c32 = w.x32;
-        x.p[0].dvec = p == 1 ? w.d : w.dq;
-        if (last) {
-            x.rows = s.rows;
-            x.cols = s.cols;
-            x.w = f.w;
-            x.w_row = f.w_row;
-            x.w_batch = f.w_batch;
-            x.theta = f.theta;
-            x.decay = f.decay;
-            x.step = f.step;
-        } else {
-            x.s16 = sc.sx[k0 + p];
-            x.p[0].out32 = w.x32;
-            x.p[0].out16 = w.x16[cur ^ 1];
+        x.p[0].a = s.tall ? w.x_hi[cur] : q;
+        x.p[0].b = s.tall ? q : w.x_hi[cur];
+        x.p[0].alpha = 1.0f / ((p == 1 ? sc.sg[k0] : 1.0f) * sc.sx[k0]);
+        x.p[0].c.hi = w.x_hi[cur];
+        x.p[0].c.lo = w.x_lo;
+        x.p[0].c_scale = 1.0f / sc.sx[k0];
+        x.p[0].dvec = p == 1 ? w.d[0] : w.dq;
+        if (!last) {
+            x.p[0].out.hi = w.x_hi[cur ^ 1];
+            x.p[0].out.lo = w.x_lo;
+            x.p[0].s_out = sc.sx[k0 + p];
         }
-        if ((e = launch_ortho_gemm(x, last ? f.epi : kEpiApply, device, stream)) != cudaSuccess)
-            return e;
+        add(x, last ? f.epi : kEpiApply);
         cur ^= 1;
         k0 += p;
     }
-    return cudaSuccess;
+    return launch_ortho_products(plan, device, stream);
 }
 
+template <typename Kernel, typename Args>
+cudaError_t launch_behind(Kernel k, dim3 grid, const Args &a, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kPrepThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, a);
+}
+
+// The norms (and a Muon step's update), then the normalised operands.
 cudaError_t enqueue_source(const Shape &s, const Work &w, const Schedule &sc, SourceArgs a, bool fp32, bool muon,
                            float eps, cudaStream_t stream)
 {
@@ -519,9 +580,7 @@ cudaError_t enqueue_source(const Shape &s, const Work &w, const Schedule &sc, So
     a.cols = s.cols;
     a.rblk = s.rblk;
     a.cblk = s.cblk;
-    a.c32 = 4 * s.cpad;
-    a.out_stride = w.x_elems;
-    a.out = w.x32;
+    a.u = w.u;
     a.parts = w.parts;
     a.status = w.status;
     const int64_t blocks = (int64_t)s.rblk * s.cblk;
@@ -542,19 +601,26 @@ cudaError_t enqueue_source(const Shape &s, const Work &w, const Schedule &sc, So
     if (e != cudaSuccess)
         return e;
     ScaleArgs c{};
-    c.x = w.x32;
-    c.out = w.x16[0];
-    c.x_stride = w.x_elems;
-    c.tiles = s.rblk * 2 * s.cpad;
+    c.x = muon ? w.u : a.g.p[0];
+    c.row_stride = a.row_stride;
+    c.batch_stride = a.batch_stride;
+    c.rows = s.rows;
+    c.cols = s.cols;
+    c.rblk = s.rblk;
+    c.cblk = s.cblk;
+    c.vec = a.vec;
+    c.out.hi = w.x_hi[0];
+    c.out.lo = w.x_lo;
+    c.c64 = 2 * s.cpad;
+    c.out_stride = w.x_elems;
     c.n_parts = parts;
     c.parts = w.parts;
-    c.inv = w.inv;
     c.eps = eps;
     c.scale = sc.sx[0];
-    const int per = (1216 + s.batch - 1) / s.batch;
-    const dim3 grid2(c.tiles < per ? c.tiles : per, s.batch);
-    k_ortho_scale<<<grid2, kPrepThreads, 0, stream>>>(c);
-    return cudaGetLastError();
+    const int64_t per = (1216 + s.batch - 1) / s.batch;
+    const dim3 grid2((unsigned)(blocks < per ? blocks : per), s.batch);
+    return muon || fp32 ? launch_behind(k_ortho_scale<float>, grid2, c, stream)
+                        : launch_behind(k_ortho_scale<uint16_t>, grid2, c, stream);
 }
 
 slide_status check_shape(int32_t batch, int32_t rows, int32_t cols)
@@ -658,8 +724,8 @@ extern "C" slide_status slide_orthogonalize(int32_t batch, int32_t rows, int32_t
     a.g.p[0] = x;
     a.row_stride = x_row_stride;
     a.batch_stride = x_batch_stride;
-    const size_t v4 = x_type == SLIDE_TYPE_FP32 ? 16 : 8;
-    a.vec = !misaligned(x, v4) && x_row_stride % 4 == 0 && (batch == 1 || x_batch_stride % 4 == 0);
+    const int64_t per16 = x_type == SLIDE_TYPE_FP32 ? 4 : 8;  // elements of 16 bytes
+    a.vec = !misaligned(x, 16) && x_row_stride % per16 == 0 && (batch == 1 || x_batch_stride % per16 == 0);
     e = enqueue_source(s, w, sc, a, x_type == SLIDE_TYPE_FP32, false, params->eps, (cudaStream_t)stream);
     if (e != cudaSuccess)
         return fail_cuda(e, "orthogonalisation: preparation launch");
@@ -723,7 +789,7 @@ extern "C" slide_status slide_muon_step(int32_t batch, int32_t rows, int32_t col
     a.mu = hp->momentum;
     a.one_minus_mu = (float)(1.0 - (double)hp->momentum);
     a.nesterov = hp->nesterov != 0;
-    a.vec = cols % 4 == 0;
+    a.vec = cols % (grads_type == SLIDE_TYPE_FP32 ? 4 : 8) == 0;
     e = enqueue_source(s, w, sc, a, grads_type == SLIDE_TYPE_FP32, true, hp->ortho.eps, (cudaStream_t)stream);
     if (e != cudaSuccess)
         return fail_cuda(e, "muon step: preparation launch");

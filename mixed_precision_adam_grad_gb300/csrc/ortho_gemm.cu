@@ -10,7 +10,17 @@
 // A CTA is persistent over output tiles: warp 0 streams operand tiles into a
 // ring of kStages stages, warp 1 issues the matrix instructions, and warps 2-9
 // read finished accumulators from tensor memory, which holds two output tiles,
-// so an epilogue overlaps the next tile's products.
+// so an epilogue overlaps the next tile's products.  An epilogue warp takes 32
+// rows x 64 columns at a time: it copies their C into its own buffer (for the
+// first chunk of a tile before the product is ready), replaces it by the
+// result and writes that from there, all with bulk copies of 4 KiB.
+//
+// One launch runs all the products of an iteration, one phase after the other:
+// a CTA whose tiles of a phase are written counts itself in, and the producers
+// wait for the count of all CTAs before they read a phase's results (a
+// cooperative launch, so all CTAs are resident).  Between two products of a
+// small matrix lie 3 us this way, where a launch each, even with programmatic
+// serialisation, left 7 to 9 us.
 //
 // Why FP16 and where FP32 stays: FP16 rounds 8 times finer than BF16 at the
 // same rate, and the iterates are bounded (the matrix is normalised first), so
@@ -37,23 +47,25 @@ constexpr int kSlot = 16384;                      // one operand block: 128 x 64
 constexpr int kStageBytes = 2 * kSlot;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (2 + kEpiWarps) * 32;
-constexpr int kBounce = 32 * 33;                  // floats of a warp's transposing buffer
-constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiWarps * kBounce * 4;
+constexpr int kPiece = 4096;                      // 32 rows of a tile
+constexpr int kEpiBytes = 2 * kPiece;             // an epilogue warp's buffer: hi and lo
+constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiWarps * kEpiBytes;
 constexpr unsigned kStatusWaitLimit = 2u;
+constexpr unsigned kFullMask = 0xffffffffu;
 
 struct Tile {
     int prob, b, i, j;
 };
 
 template <int CG>
-__device__ __forceinline__ Tile decode(const OrthoGemm &g, int t)
+__device__ __forceinline__ Tile decode(const OrthoGemm &g, int batch, int t)
 {
     const int mt = (g.mblk + CG - 1) / CG, nt = (g.nblk + CG - 1) / CG;
     const int per = g.sym ? mt * (mt + 1) / 2 : mt * nt;
     const int z = t / per, r = t - z * per;
     Tile x;
-    x.prob = z / g.batch;
-    x.b = z - x.prob * g.batch;
+    x.prob = z / batch;
+    x.b = z - x.prob * batch;
     if (g.sym) {
         int j = (int)((sqrtf(8.0f * (float)r + 1.0f) - 1.0f) * 0.5f);
         while (j * (j + 1) / 2 > r)
@@ -73,10 +85,10 @@ __device__ __forceinline__ Tile decode(const OrthoGemm &g, int t)
 }
 
 template <int CG>
-__device__ __forceinline__ int tile_count(const OrthoGemm &g)
+__host__ __device__ __forceinline__ int tile_count(const OrthoGemm &g, int batch)
 {
     const int mt = (g.mblk + CG - 1) / CG, nt = (g.nblk + CG - 1) / CG;
-    return (g.sym ? mt * (mt + 1) / 2 : mt * nt) * g.batch * g.nprob;
+    return (g.sym ? mt * (mt + 1) / 2 : mt * nt) * batch * g.nprob;
 }
 
 // Whether step k of the operand whose tile has index t (in units of CG blocks)
@@ -92,149 +104,175 @@ __device__ __forceinline__ void load_operand(uint32_t slot, const __half *m, int
                                              uint32_t bar)
 {
     if (mn) {
-        const __half *t = m + ((int64_t)(k >> 1) * c64 + 2 * blk) * kTileElems16 + (k & 1) * (kTileElems16 / 2);
+        const __half *t = m + ((int64_t)(k >> 1) * c64 + 2 * blk) * kTileElems + (k & 1) * (kTileElems / 2);
         bulk_load(slot, t, kSlot / 2, bar);
-        bulk_load(slot + kSlot / 2, t + kTileElems16, kSlot / 2, bar);
+        bulk_load(slot + kSlot / 2, t + kTileElems, kSlot / 2, bar);
     } else {
-        bulk_load(slot, m + ((int64_t)blk * c64 + k) * kTileElems16, kSlot, bar);
+        bulk_load(slot, m + ((int64_t)blk * c64 + k) * kTileElems, kSlot, bar);
     }
 }
 
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
+__device__ __forceinline__ uint32_t pack_half2(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
+__device__ __forceinline__ float2 unpack_half2(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2 *>(&u)); }
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr)
 {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
 }
 
-// Row r's 32 values at chunk offset `c` (4 chunks of 8) of a T16 tile.
-__device__ __forceinline__ void store16(__half *tile, int r, int c, const float (&v)[32], float s)
+__device__ __forceinline__ float lds32(uint32_t addr)
 {
-    uint4 *row = reinterpret_cast<uint4 *>(tile + r * 64);
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// Columns 32h..32h+31 of the lane's row of a 64-column piece, as hi (and lo).
+__device__ __forceinline__ void put_hi(uint32_t piece, int lane, int h, const float (&v)[32], float s)
+{
+    const uint32_t row = piece + lane * 128;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        uint4 x;
-        x.x = pack_half2(v[8 * q] * s, v[8 * q + 1] * s);
-        x.y = pack_half2(v[8 * q + 2] * s, v[8 * q + 3] * s);
-        x.z = pack_half2(v[8 * q + 4] * s, v[8 * q + 5] * s);
-        x.w = pack_half2(v[8 * q + 6] * s, v[8 * q + 7] * s);
-        row[(c + q) ^ (r & 7)] = x;
+        uint32_t u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            u[e] = pack_half2(__floats2half2_rn(v[8 * q + 2 * e] * s, v[8 * q + 2 * e + 1] * s));
+        sts128(row + (((4 * h + q) ^ (lane & 7)) << 4), make_uint4(u[0], u[1], u[2], u[3]));
     }
 }
 
-__device__ __forceinline__ void store32(float *tile, int r, const float (&v)[32])
+__device__ __forceinline__ void put_pair(uint32_t hi, uint32_t lo, int lane, int h, const float (&v)[32], float s)
 {
-    float4 *row = reinterpret_cast<float4 *>(tile + r * 32);
+    const uint32_t at = lane * 128;
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-        row[q ^ (r & 7)] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+    for (int q = 0; q < 4; ++q) {
+        uint32_t u[4], w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float x = v[8 * q + 2 * e] * s, y = v[8 * q + 2 * e + 1] * s;
+            const __half2 p = __floats2half2_rn(x, y);
+            const float2 f = __half22float2(p);
+            u[e] = pack_half2(p);
+            w[e] = pack_half2(__floats2half2_rn((x - f.x) * kLoScale, (y - f.y) * kLoScale));
+        }
+        const uint32_t c = ((4 * h + q) ^ (lane & 7)) << 4;
+        sts128(hi + at + c, make_uint4(u[0], u[1], u[2], u[3]));
+        sts128(lo + at + c, make_uint4(w[0], w[1], w[2], w[3]));
+    }
 }
 
+// What an epilogue reads of C.
+template <int EPI>
+constexpr int kReadsOf = EPI == kEpiGram ? 0 : EPI == kEpiPoly ? 1 : 2;
+
+__device__ __forceinline__ void read_half(uint32_t piece, int lane, int h, uint32_t *w)
+{
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint4 x = lds128(piece + lane * 128 + (((4 * h + q) ^ (lane & 7)) << 4));
+        w[4 * q] = x.x, w[4 * q + 1] = x.y, w[4 * q + 2] = x.z, w[4 * q + 3] = x.w;
+    }
+}
+
+// One 64-column chunk (c of the tile's) of this warp's 32 rows.  buf: its C,
+// replaced by the result.
 template <int CG, int EPI>
-__device__ __forceinline__ void epilogue_chunk(const OrthoGemm &g, const Tile &x, int ib, int jb, int row, int q,
-                                               const uint32_t (&acc)[32], float *bounce, int lane)
+__device__ __forceinline__ void epilogue_chunk(const OrthoPlan &plan, const OrthoGemm &g, const Tile &x, int ib, int c, int row, int lane,
+                                               uint32_t acc_addr, uint32_t buf)
 {
-    // q: 32-column chunk of the 128-block jb
-    const OrthoOperands &p = g.p[x.prob];
-    const int64_t t16 = (int64_t)x.b * g.out_stride + ((int64_t)ib * g.out_c64 + 2 * jb + (q >> 1)) * kTileElems16;
-    const int64_t t32 = (int64_t)x.b * g.out_stride + ((int64_t)ib * g.out_c64 * 2 + 4 * jb + q) * kTileElems32;
-    const int gi = ib * 128 + row, gj = jb * 128 + q * 32;
-    const int on_diag = g.sym && gi >= gj && gi < gj + 32 ? gi - gj : -1;
-    float v[32];
-#pragma unroll
-    for (int e = 0; e < 32; ++e)
-        v[e] = __uint_as_float(acc[e]) * g.alpha;
-
-    if constexpr (EPI == kEpiPoly) {
-        const uint4 *crow = reinterpret_cast<const uint4 *>(p.c16 + t16 + row * 64);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const uint4 w = crow[((q & 1) * 4 + c) ^ (row & 7)];
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u[h]));
-                v[8 * c + 2 * h] += g.c16_scale * f.x;
-                v[8 * c + 2 * h + 1] += g.c16_scale * f.y;
-            }
-        }
+    constexpr bool kFinal = EPI == kEpiOut || EPI == kEpiMuon;
+    const OrthoProduct &p = g.p[x.prob];
+    const int jb = x.j * CG + (c >> 1);
+    const int gi = ib * 128 + row, gj = jb * 128 + (c & 1) * 64;
+    // the caller's arrays are written from FP32 in the buffer: all of C is
+    // read first; otherwise each half's result takes the place of its C
+    constexpr int kHeld = kReadsOf<EPI> == 0 ? 1 : kFinal ? 32 : 16;
+    uint32_t chi[kHeld], clo[kHeld];
+    if constexpr (kFinal) {
+        read_half(buf, lane, 0, chi);
+        read_half(buf, lane, 1, chi + 16);
+        read_half(buf + kPiece, lane, 0, clo);
+        read_half(buf + kPiece, lane, 1, clo + 16);
+        __syncwarp();
     }
-    if constexpr (EPI == kEpiSym || EPI == kEpiApply || EPI == kEpiOut || EPI == kEpiMuon) {
-        const float4 *crow = reinterpret_cast<const float4 *>(p.c32 + t32 + row * 32);
-        const float *d = p.dvec + (int64_t)x.b * g.d_stride;
-        const float inv = g.c_inv ? g.c_inv[x.b] : 1.0f;
-        const float dr = g.d_by_col ? inv : inv * d[gi];
+    float d_row = 0.0f;
+    const float *d = p.dvec + (int64_t)x.b * g.d_stride;
+    if constexpr (kReadsOf<EPI> > 1)
+        if (!g.d_by_col)
+            d_row = d[gi] * p.c_scale;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const float4 w = crow[c ^ (row & 7)];
-            float4 dc = make_float4(dr, dr, dr, dr);
-            if (g.d_by_col) {
-                const float4 k = *reinterpret_cast<const float4 *>(d + gj + 4 * c);
-                dc = make_float4(dr * k.x, dr * k.y, dr * k.z, dr * k.w);
-            }
-            v[4 * c] = fmaf(dc.x, w.x, v[4 * c]);
-            v[4 * c + 1] = fmaf(dc.y, w.y, v[4 * c + 1]);
-            v[4 * c + 2] = fmaf(dc.z, w.z, v[4 * c + 2]);
-            v[4 * c + 3] = fmaf(dc.w, w.w, v[4 * c + 3]);
-        }
-    }
-
-    if constexpr (EPI == kEpiPoly) {
-        float dd = 0.0f;
-        if (p.out32) {  // Q = aI + B, with its diagonal
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                if (e == on_diag) {
-                    v[e] += g.coef_a;
-                    dd = v[e];
-                }
-            }
-            store32(p.out32 + t32, row, v);
-            store16(p.out16b + t16, row, (q & 1) * 4, v, g.s16b);
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-                if (e == on_diag)
-                    v[e] = 0.0f;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                if (e == on_diag) {
-                    dd = v[e] + g.coef_a;
-                    v[e] = 0.0f;
-                }
-            }
-        }
-        if (on_diag >= 0)
-            p.dvec_out[(int64_t)x.b * g.d_stride + gi] = dd;
-        store16(p.out16 + t16, row, (q & 1) * 4, v, g.s16);
-    } else if constexpr (EPI == kEpiOut || EPI == kEpiMuon) {
-        // through the warp's buffer, so that a warp writes along the rows
+    for (int h = 0; h < 2; ++h) {
+        uint32_t acc[32];
+        tmem_load32(acc_addr + h * 32, acc);
+        if constexpr (kReadsOf<EPI> > 0 && !kFinal)
+            read_half(buf, lane, h, chi);
+        if constexpr (kReadsOf<EPI> > 1 && !kFinal)
+            read_half(buf + kPiece, lane, h, clo);
+        tmem_wait_load();
+        constexpr int kAt = kFinal ? 16 : 0;
+        float v[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e)
-            bounce[lane * 33 + e] = v[e];
-        __syncwarp();
-        const int col = gj + lane;
-        const int row0 = ib * 128 + (row & ~31);
-        const int lim = min(32, g.rows - row0);
-        if (col < g.cols) {
-            for (int r = 0; r < lim; ++r) {
-                float o = bounce[r * 33 + lane];
-                if constexpr (EPI == kEpiMuon) {
-                    const int64_t at = ((int64_t)x.b * g.rows + row0 + r) * g.cols + col;
-                    o = __fsub_rn(__fmul_rn(g.theta[at], g.decay), __fmul_rn(g.step, o));
-                    g.theta[at] = o;
-                    g.w[at] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
-                } else {
-                    g.w[(int64_t)x.b * g.w_batch + (int64_t)(row0 + r) * g.w_row + col] =
-                        __bfloat16_as_ushort(__float2bfloat16_rn(o));
-                }
+            v[e] = __uint_as_float(acc[e]) * p.alpha;
+        // the lane's diagonal element, if it lies among these columns
+        const int on_diag = gi - gj - 32 * h;
+        const bool has_diag = (EPI == kEpiPoly || EPI == kEpiSym) && (unsigned)on_diag < 32u;
+
+        if constexpr (EPI == kEpiPoly) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float2 f = unpack_half2(chi[e]);
+                v[2 * e] = fmaf(p.c_scale, f.x, v[2 * e]);
+                v[2 * e + 1] = fmaf(p.c_scale, f.y, v[2 * e + 1]);
             }
         }
-        __syncwarp();
-    } else {
-        if (p.out32)
-            store32(p.out32 + t32, row, v);
-        if constexpr (EPI == kEpiSym) {
-            if (g.diag_out && on_diag >= 0) {
+        if constexpr (kReadsOf<EPI> > 1) {
+            const bool two = EPI == kEpiSym && p.dvec2 != nullptr;
+            const float *by_col = two ? p.dvec2 + (int64_t)x.b * g.d_stride : d;
+            const float col_scale = two ? p.c_scale2 : p.c_scale;
+#pragma unroll
+            for (int e4 = 0; e4 < 8; ++e4) {
+                float kh[4] = {d_row, d_row, d_row, d_row}, kl[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    kl[e] = d_row * (1.0f / kLoScale);
+                if (two || g.d_by_col) {
+                    const float4 w = *reinterpret_cast<const float4 *>(by_col + gj + 32 * h + 4 * e4);
+                    kl[0] = w.x * col_scale, kl[1] = w.y * col_scale, kl[2] = w.z * col_scale, kl[3] = w.w * col_scale;
+                    if (!two) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            kh[e] = kl[e];
+                            kl[e] *= 1.0f / kLoScale;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float2 f = unpack_half2(chi[h * kAt + 2 * e4 + e]), l = unpack_half2(clo[h * kAt + 2 * e4 + e]);
+                    float *y = v + 4 * e4 + 2 * e;
+                    y[0] = fmaf(kh[2 * e], f.x, fmaf(kl[2 * e], l.x, y[0]));
+                    y[1] = fmaf(kh[2 * e + 1], f.y, fmaf(kl[2 * e + 1], l.y, y[1]));
+                }
+            }
+            if (two && has_diag) {
+                const float dd = d[gi] * by_col[gi];
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (e == on_diag)
+                        v[e] += dd;
+            }
+        }
+
+        if constexpr (EPI == kEpiPoly || EPI == kEpiSym) {
+            if (has_diag && (EPI == kEpiPoly || p.diag_out)) {
                 float dd = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
@@ -243,23 +281,172 @@ __device__ __forceinline__ void epilogue_chunk(const OrthoGemm &g, const Tile &x
                         v[e] = 0.0f;
                     }
                 }
-                p.dvec_out[(int64_t)x.b * g.d_stride + gi] = dd;
+                p.dvec_out[(int64_t)x.b * g.d_stride + gi] = EPI == kEpiPoly ? dd + g.coef_a : dd;
             }
         }
-        store16(p.out16 + t16, row, (q & 1) * 4, v, g.s16);
+        if constexpr (!kFinal) {
+            if (EPI == kEpiPoly || p.out.lo == nullptr)
+                put_hi(buf, lane, h, v, p.s_out);
+            else
+                put_pair(buf, buf + kPiece, lane, h, v, p.s_out);
+        } else {
+            // FP32 through the buffer, so that the warp writes along the rows
+            const uint32_t half = buf + h * kPiece;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                sts128(half + lane * 128 + ((q ^ (lane & 7)) << 4),
+                       make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                                  __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3])));
+            __syncwarp();
+            const int col = gj + 32 * h + lane;
+            const int row0 = ib * 128 + (row & ~31);
+            const int lim = min(32, plan.rows - row0);
+            constexpr int kAtOnce = 16;  // rows whose loads are in flight together
+            if (col < plan.cols) {
+                const int64_t next = EPI == kEpiMuon ? plan.cols : plan.w_row;
+                const int64_t at0 = EPI == kEpiMuon ? ((int64_t)x.b * plan.rows + row0) * plan.cols + col
+                                                    : (int64_t)x.b * plan.w_batch + (int64_t)row0 * plan.w_row + col;
+                float *th = EPI == kEpiMuon ? plan.theta + at0 : nullptr;
+                uint16_t *w = plan.w + at0;
+#pragma unroll
+                for (int r0 = 0; r0 < 32; r0 += kAtOnce) {
+                    float old[kAtOnce];
+                    if constexpr (EPI == kEpiMuon) {
+#pragma unroll
+                        for (int r = 0; r < kAtOnce; ++r)
+                            old[r] = r0 + r < lim ? __ldcs(th + (r0 + r) * next) : 0.0f;
+                    }
+#pragma unroll
+                    for (int r = 0; r < kAtOnce; ++r) {
+                        float o = lds32(half + (r0 + r) * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+                        if (r0 + r < lim) {
+                            if constexpr (EPI == kEpiMuon) {
+                                o = __fsub_rn(__fmul_rn(old[r], plan.decay), __fmul_rn(plan.step, o));
+                                __stcs(th + (r0 + r) * next, o);
+                            }
+                            w[(r0 + r) * next] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
+                        }
+                    }
+                }
+            }
+        }
+    }
+    fence_async_shared();  // results leave the buffer, or the next C comes into it, by the copy engine
+    __syncwarp();
+    if constexpr (!kFinal) {
+        const int64_t piece = (int64_t)x.b * g.out_stride + ((int64_t)ib * g.out_c64 + 2 * jb + (c & 1)) * kTileElems +
+                              (row & ~31) * 64;
+        if (elect_one()) {
+            bulk_store(p.out.hi + piece, buf, kPiece);
+            if (EPI != kEpiPoly && p.out.lo)
+                bulk_store(p.out.lo + piece, buf + kPiece, kPiece);
+            bulk_commit();
+        }
+        __syncwarp();
     }
 }
 
+// A Muon step's master weights of a chunk, on their way into L2 while the
+// product is not ready yet.
+__device__ __forceinline__ void prefetch_theta(const OrthoPlan &plan, const Tile &x, int row0, int col, int lane)
+{
+    const int row = row0 + lane;
+    if (row >= plan.rows || col >= plan.cols)
+        return;
+    const float *p = plan.theta + ((int64_t)x.b * plan.rows + row) * plan.cols + col;
+    const int n = min(64, plan.cols - col);
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+    if (n > 32)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p + 32));
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p + n - 1));
+}
+
+// Copy the C of chunk c into a buffer.
 template <int CG, int EPI>
-__global__ void __launch_bounds__(kThreads, 1) k_ortho_gemm(const __grid_constant__ OrthoGemm g)
+__device__ __forceinline__ void prefetch_chunk(const OrthoGemm &g, const Tile &x, int ib, int c, int quad, uint32_t buf,
+                                               uint32_t bar)
+{
+    const OrthoProduct &p = g.p[x.prob];
+    const int jb = x.j * CG + (c >> 1);
+    const int64_t piece = (int64_t)x.b * g.out_stride + ((int64_t)ib * g.out_c64 + 2 * jb + (c & 1)) * kTileElems +
+                          quad * 32 * 64;
+    mbar_expect_tx(bar, kReadsOf<EPI> * kPiece);
+    bulk_load(buf, p.c.hi + piece, kPiece, bar);
+    if constexpr (kReadsOf<EPI> > 1)
+        bulk_load(buf + kPiece, p.c.lo + piece, kPiece, bar);
+}
+
+// Shared state of a CTA, besides the operand ring and the epilogue's buffers.
+struct Shared {
+    uint64_t full[kStages], empty[kStages], peer[kStages], acc_full[2], acc_empty[2], c[kEpiWarps], phase;
+    uint32_t tmem;
+    unsigned written;        // epilogue warps whose tiles of the phase are written
+    volatile int abort;
+};
+
+// The tiles of one phase, by one epilogue warp.  n: tiles so far (of all
+// phases); seq: chunks of C asked for so far.
+template <int CG, int EPI>
+__device__ __forceinline__ bool epilogue_tiles(const OrthoPlan &plan, const OrthoGemm &g, Shared &sh, uint32_t tmem,
+                                               uint32_t mine, int warp, int lane, uint32_t rank, uint32_t &n,
+                                               uint32_t &seq)
+{
+    // warp (quad, half): rows 32*quad.., every second chunk of 64 columns
+    const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
+    const uint32_t bar = smem_addr(&sh.c[warp]);
+    const int n_tiles = tile_count<CG>(g, plan.batch);
+    for (int t = blockIdx.x / CG; t < n_tiles; t += gridDim.x / CG, ++n) {
+        const Tile x = decode<CG>(g, plan.batch, t);
+        const uint32_t buf = n & 1, use = n >> 1;
+        const int ib = x.i * CG + rank;
+        // the chunks of the tile that exist (and, of a symmetric result, are kept)
+        const int c0 = (g.sym ? max(0, 2 * (ib - x.j * CG)) : 0) + half;
+        const int c1 = ib < g.mblk ? min(2 * CG, 2 * (g.nblk - x.j * CG)) : 0;
+        auto fetch = [&](int c) {
+            if (elect_one()) {
+                bulk_wait_read<0>();  // of the store out of the buffer
+                if constexpr (kReadsOf<EPI> > 0)
+                    prefetch_chunk<CG, EPI>(g, x, ib, c, quad, mine, bar);
+            }
+            __syncwarp();
+            if constexpr (kReadsOf<EPI> > 0)
+                ++seq;
+        };
+        if (c0 < c1)
+            fetch(c0);
+        if constexpr (EPI == kEpiMuon)
+            for (int c = c0; c < c1; c += 2)
+                prefetch_theta(plan, x, ib * 128 + quad * 32, (x.j * CG + (c >> 1)) * 128 + (c & 1) * 64, lane);
+        bool ok = __all_sync(kFullMask, mbar_wait(smem_addr(&sh.acc_full[buf]), use & 1, &sh.abort));
+        tmem_fence_after();
+        for (int c = c0; c < c1 && ok; c += 2) {
+            if constexpr (kReadsOf<EPI> > 0)
+                ok = __all_sync(kFullMask, mbar_wait(bar, (seq - 1) & 1, &sh.abort));
+            if (!ok)
+                break;
+            epilogue_chunk<CG, EPI>(plan, g, x, ib, c, row, lane,
+                                    tmem + ((uint32_t)(quad * 32) << 16) + buf * 128 * CG + c * 64, mine);
+            if (c + 2 < c1)
+                fetch(c + 2);
+        }
+        if (!ok)
+            return false;
+        tmem_fence_before();
+        __syncwarp();
+        if (elect_one())
+            mbar_arrive_cluster(map_to_rank(smem_addr(&sh.acc_empty[buf]), 0));
+        __syncwarp();
+    }
+    return true;
+}
+
+template <int CG>
+__global__ void __launch_bounds__(kThreads, 1) k_ortho_products(const __grid_constant__ OrthoPlan plan)
 {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_peer[kStages], s_acc_full[2], s_acc_empty[2];
-    __shared__ uint32_t s_tmem;
-    __shared__ volatile int s_abort;
+    __shared__ Shared sh;
 
     const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u;
-    float *bounce_all = reinterpret_cast<float *>(smem_raw + (ring - smem_addr(smem_raw)) + kStages * kStageBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CG == 2 ? cluster_rank() : 0;
     const int first = blockIdx.x / CG, stride = gridDim.x / CG;
@@ -267,150 +454,172 @@ __global__ void __launch_bounds__(kThreads, 1) k_ortho_gemm(const __grid_constan
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(smem_addr(&s_full[s]), 1);
-            mbar_init(smem_addr(&s_empty[s]), 1);
-            mbar_init(smem_addr(&s_peer[s]), 1);
+            mbar_init(smem_addr(&sh.full[s]), 1);
+            mbar_init(smem_addr(&sh.empty[s]), 1);
+            mbar_init(smem_addr(&sh.peer[s]), 1);
         }
         for (int a = 0; a < 2; ++a) {
-            mbar_init(smem_addr(&s_acc_full[a]), 1);
-            mbar_init(smem_addr(&s_acc_empty[a]), CG * kEpiWarps);
+            mbar_init(smem_addr(&sh.acc_full[a]), 1);
+            mbar_init(smem_addr(&sh.acc_empty[a]), CG * kEpiWarps);
         }
-        s_abort = 0;
+        for (int w = 0; w < kEpiWarps; ++w)
+            mbar_init(smem_addr(&sh.c[w]), 1);
+        mbar_init(smem_addr(&sh.phase), 1);
+        sh.abort = 0;
+        sh.written = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_shared();
     }
     if (warp == 1)
-        tmem_alloc<CG>(smem_addr(&s_tmem), kCols);
+        tmem_alloc<CG>(smem_addr(&sh.tmem), kCols);
     tmem_fence_before();
     if constexpr (CG == 2)
         cluster_sync();
     else
         __syncthreads();
     tmem_fence_after();
-    const uint32_t tmem = s_tmem;
-    // a launch behind one whose wait ran out does nothing
-    const int total = (*(volatile unsigned *)g.status & kStatusWaitLimit) ? 0 : tile_count<CG>(g);
-    // both CTAs of a pair have to agree on that
-    int n_tiles = total;
-    if constexpr (CG == 2) {
-        __shared__ int s_total;
-        if (threadIdx.x == 0 && rank == 0) {
-            const uint32_t mine = smem_addr(&s_total);
-            for (uint32_t r = 0; r < 2; ++r)
-                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_rank(mine, r)), "r"(total) : "memory");
-        }
-        cluster_sync();
-        n_tiles = s_total;
-    }
+    const uint32_t tmem = sh.tmem;
+    wait_for_previous_grid();
+    fence_async();  // what the previous launch wrote is read by the copy engine
 
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            for (int t = first; t < n_tiles && ok && !g.test_stall; t += stride) {
-                const Tile x = decode<CG>(g, t);
+        uint32_t it = 0;
+        bool ok = true;
+        for (int f = 0; f < plan.n_phases && ok; ++f) {
+            const OrthoGemm &g = plan.ph[f];
+            if (f > 0) {  // the phase before is written, by every CTA
+                ok = __all_sync(kFullMask, counter_wait(plan.status + f, gridDim.x, plan.status, kStatusWaitLimit, &sh.abort));
+                if (!ok)
+                    break;
+                fence_async();
+                if (elect_one())
+                    mbar_arrive(smem_addr(&sh.phase));
+                __syncwarp();
+            }
+            const int n_tiles = plan.test_stall ? 0 : tile_count<CG>(g, plan.batch);
+            for (int t = first; t < n_tiles && ok; t += stride) {
+                const Tile x = decode<CG>(g, plan.batch, t);
                 const __half *a = g.p[x.prob].a + (int64_t)x.b * g.a_stride;
                 const __half *b = g.p[x.prob].b + (int64_t)x.b * g.b_stride;
                 for (int k = 0; k < g.k64; ++k, ++it) {
                     const uint32_t s = it % kStages, ph = (it / kStages) & 1;
-                    if (!mbar_wait(smem_addr(&s_empty[s]), ph ^ 1, &s_abort)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t bar = smem_addr(&s_full[s]), slot = ring + s * kStageBytes;
-                    mbar_expect_tx(bar, kStageBytes);
-                    load_operand(slot, a, g.a_c64, x.i * CG + rank, k, reads_mn<CG>(g.a_kind, x.i, k), bar);
-                    load_operand(slot + kSlot, b, g.b_c64, x.j * CG + rank, k, reads_mn<CG>(g.b_kind, x.j, k), bar);
-                }
-            }
-            if (!ok)
-                s_abort = 1;
-            // copies in flight land before the CTA ends
-            for (uint32_t d = it > kStages ? it - kStages : 0; d < it; ++d) {
-                volatile int never = 0;
-                mbar_wait(smem_addr(&s_full[d % kStages]), (d / kStages) & 1, &never);
-            }
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            uint32_t it = 0, n = 0;
-            bool ok = true;
-            for (int t = first; t < n_tiles && ok; t += stride, ++n) {
-                const Tile x = decode<CG>(g, t);
-                const uint32_t buf = n & 1, use = n >> 1;
-                if (rank == 0 && !mbar_wait(smem_addr(&s_acc_empty[buf]), (use & 1) ^ 1, &s_abort)) {
-                    ok = false;
-                    break;
-                }
-                tmem_fence_after();
-                for (int k = 0; k < g.k64; ++k, ++it) {
-                    const uint32_t s = it % kStages, ph = (it / kStages) & 1;
-                    ok = mbar_wait(smem_addr(&s_full[s]), ph, &s_abort);
-                    if (ok && CG == 2) {
-                        if (rank == 0)
-                            ok = mbar_wait(smem_addr(&s_peer[s]), ph, &s_abort);
-                        else
-                            mbar_arrive_cluster(map_to_rank(smem_addr(&s_peer[s]), 0));
-                    }
+                    ok = __all_sync(kFullMask, mbar_wait(smem_addr(&sh.empty[s]), ph ^ 1, &sh.abort));
                     if (!ok)
                         break;
-                    if (rank != 0)
-                        continue;
+                    const uint32_t bar = smem_addr(&sh.full[s]), slot = ring + s * kStageBytes;
+                    const bool a_mn = reads_mn<CG>(g.a_kind, x.i, k), b_mn = reads_mn<CG>(g.b_kind, x.j, k);
+                    if (elect_one()) {
+                        mbar_expect_tx(bar, kStageBytes);
+                        load_operand(slot, a, g.a_c64, x.i * CG + rank, k, a_mn, bar);
+                        load_operand(slot + kSlot, b, g.b_c64, x.j * CG + rank, k, b_mn, bar);
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        if (!ok) {
+            sh.abort = 1;
+            if (lane == 0)
+                atomicOr(plan.status, kStatusWaitLimit);
+        }
+        // copies in flight land before the CTA ends
+        for (uint32_t d = it > kStages ? it - kStages : 0; d < it; ++d)
+            mbar_wait(smem_addr(&sh.full[d % kStages]), (d / kStages) & 1, nullptr);
+    } else if (warp == 1) {
+        uint32_t it = 0, n = 0;
+        bool ok = true;
+        for (int f = 0; f < plan.n_phases && ok; ++f) {
+            const OrthoGemm &g = plan.ph[f];
+            const int n_tiles = tile_count<CG>(g, plan.batch);
+            for (int t = first; t < n_tiles && ok; t += stride, ++n) {
+                const Tile x = decode<CG>(g, plan.batch, t);
+                const uint32_t buf = n & 1, use = n >> 1;
+                if (rank == 0) {
+                    ok = __all_sync(kFullMask, mbar_wait(smem_addr(&sh.acc_empty[buf]), (use & 1) ^ 1, &sh.abort));
+                    if (!ok)
+                        break;
                     tmem_fence_after();
+                }
+                for (int k = 0; k < g.k64; ++k, ++it) {
+                    const uint32_t s = it % kStages, ph = (it / kStages) & 1;
+                    ok = mbar_wait(smem_addr(&sh.full[s]), ph, &sh.abort);
+                    if (CG == 2 && rank == 0)
+                        ok = ok && mbar_wait(smem_addr(&sh.peer[s]), ph, &sh.abort);
+                    ok = __all_sync(kFullMask, ok);
+                    if (!ok)
+                        break;
+                    if (CG == 2 && rank != 0) {
+                        if (elect_one())
+                            mbar_arrive_cluster(map_to_rank(smem_addr(&sh.peer[s]), 0));
+                        __syncwarp();
+                        continue;
+                    }
                     const bool a_mn = reads_mn<CG>(g.a_kind, x.i, k), b_mn = reads_mn<CG>(g.b_kind, x.j, k);
                     const uint32_t idesc = f16_idesc(128 * CG, 128 * CG, a_mn, b_mn);
                     const uint32_t slot = ring + s * kStageBytes;
-                    const uint32_t a_step = a_mn ? 2048 : 32, b_step = b_mn ? 2048 : 32;
+                    const uint64_t a_desc = operand_desc(slot, kSlot / 2), b_desc = operand_desc(slot + kSlot, kSlot / 2);
+                    const uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        mma_f16<CG>(tmem + buf * 128 * CG, operand_desc(slot + j * a_step, kSlot / 2),
-                                    operand_desc(slot + kSlot + j * b_step, kSlot / 2), idesc, k > 0 || j > 0);
-                    mma_commit<CG>(smem_addr(&s_empty[s]));
+                        for (int j = 0; j < 4; ++j)
+                            mma_f16<CG>(tmem + buf * 128 * CG, a_desc + j * a_step, b_desc + j * b_step, idesc,
+                                        k > 0 || j > 0);
+                        mma_commit<CG>(smem_addr(&sh.empty[s]));
+                        if (k + 1 == g.k64)
+                            mma_commit<CG>(smem_addr(&sh.acc_full[buf]));
+                    }
+                    __syncwarp();
                 }
-                if (ok && rank == 0)
-                    mma_commit<CG>(smem_addr(&s_acc_full[buf]));
-            }
-            if (!ok) {
-                s_abort = 1;
-                atomicOr(g.status, kStatusWaitLimit);
-            }
-            // the matrix instructions in flight end before the CTA does: the
-            // commits of the last stages have arrived
-            for (uint32_t d = it > kStages ? it - kStages : 0; d < it; ++d) {
-                volatile int never = 0;
-                mbar_wait(smem_addr(&s_empty[d % kStages]), (d / kStages) & 1, &never);
             }
         }
-    } else {
-        const int quad = warp & 3, half = (warp - 2) >> 2;
-        float *bounce = bounce_all + (warp - 2) * kBounce;
-        const int row = quad * 32 + lane;
-        uint32_t n = 0;
-        for (int t = first; t < n_tiles; t += stride, ++n) {
-            const Tile x = decode<CG>(g, t);
-            const uint32_t buf = n & 1, use = n >> 1;
-            const bool ok = mbar_wait(smem_addr(&s_acc_full[buf]), use & 1, &s_abort);
-            if (!__all_sync(0xffffffffu, ok)) {
-                s_abort = 1;
-                if (lane == 0)
-                    atomicOr(g.status, kStatusWaitLimit);
-                break;
-            }
-            tmem_fence_after();
-            const int ib = x.i * CG + rank;
-            for (int c = half; c < 4 * CG; c += 2) {
-                uint32_t acc[32];
-                tmem_load32(tmem + ((uint32_t)(quad * 32) << 16) + buf * 128 * CG + c * 32, acc);
-                tmem_wait_load();
-                const int jb = x.j * CG + (c >> 2);
-                if (ib >= g.mblk || jb >= g.nblk || (g.sym && ib > jb))
-                    continue;
-                epilogue_chunk<CG, EPI>(g, x, ib, jb, row, c & 3, acc, bounce, lane);
-            }
-            tmem_fence_before();
-            __syncwarp();
+        if (!ok) {
+            sh.abort = 1;
             if (lane == 0)
-                mbar_arrive_cluster(map_to_rank(smem_addr(&s_acc_empty[buf]), 0));
+                atomicOr(plan.status, kStatusWaitLimit);
+        }
+        // the matrix instructions in flight end before the CTA does: the
+        // commits of the last stages have arrived
+        for (uint32_t d = it > kStages ? it - kStages : 0; d < it; ++d)
+            mbar_wait(smem_addr(&sh.empty[d % kStages]), (d / kStages) & 1, nullptr);
+    } else {
+        const int w = warp - 2;
+        const int ew = (warp & 3) | ((w >> 2) << 2);  // a warp reads the 32 lanes of tensor memory of its number mod 4
+        const uint32_t mine = ring + kStages * kStageBytes + ew * kEpiBytes;
+        uint32_t n = 0, seq = 0;
+        bool ok = true;
+        for (int f = 0; f < plan.n_phases && ok; ++f) {
+            const OrthoGemm &g = plan.ph[f];
+            if (f > 0) {
+                ok = __all_sync(kFullMask, mbar_wait(smem_addr(&sh.phase), (f - 1) & 1, &sh.abort));
+                if (!ok)
+                    break;
+                fence_async();
+            }
+            switch (g.epi) {
+            case kEpiGram: ok = epilogue_tiles<CG, kEpiGram>(plan, g, sh, tmem, mine, ew, lane, rank, n, seq); break;
+            case kEpiPoly: ok = epilogue_tiles<CG, kEpiPoly>(plan, g, sh, tmem, mine, ew, lane, rank, n, seq); break;
+            case kEpiSym: ok = epilogue_tiles<CG, kEpiSym>(plan, g, sh, tmem, mine, ew, lane, rank, n, seq); break;
+            case kEpiApply: ok = epilogue_tiles<CG, kEpiApply>(plan, g, sh, tmem, mine, ew, lane, rank, n, seq); break;
+            case kEpiOut: ok = epilogue_tiles<CG, kEpiOut>(plan, g, sh, tmem, mine, ew, lane, rank, n, seq); break;
+            default: ok = epilogue_tiles<CG, kEpiMuon>(plan, g, sh, tmem, mine, ew, lane, rank, n, seq); break;
+            }
+            bulk_wait<0>();
+            __syncwarp();
+            if (ok && f + 1 < plan.n_phases && lane == 0) {  // the CTA's last warp counts it in
+                __threadfence();
+                if (atomicAdd(&sh.written, 1u) == (unsigned)((f + 1) * kEpiWarps - 1)) {
+                    __threadfence();
+                    atomicAdd(plan.status + f + 1, 1u);
+                }
+            }
+            __syncwarp();
+        }
+        if (!ok) {
+            sh.abort = 1;
+            if (lane == 0)
+                atomicOr(plan.status, kStatusWaitLimit);
+            if (seq > 0)  // a copy of C may be in flight
+                mbar_wait(smem_addr(&sh.c[ew]), (seq - 1) & 1, nullptr);
         }
     }
     __syncwarp();
@@ -426,56 +635,96 @@ __global__ void __launch_bounds__(kThreads, 1) k_ortho_gemm(const __grid_constan
 
 constexpr int kMaxDevices = 64;
 
-template <int CG, int EPI>
-cudaError_t launch(const OrthoGemm &g, int device, cudaStream_t stream)
+template <int CG>
+cudaError_t launch(const OrthoPlan &plan, int groups, cudaStream_t stream)
 {
-    static std::atomic<int> sms[kMaxDevices];
-    int n = sms[device].load(std::memory_order_acquire);
-    if (n == 0) {
-        cudaError_t e = cudaFuncSetAttribute(k_ortho_gemm<CG, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-        if (e == cudaSuccess)
-            e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device);
-        if (e != cudaSuccess)
-            return e;
-        sms[device].store(n, std::memory_order_release);
+    int most = 1;
+    for (int f = 0; f < plan.n_phases; ++f) {
+        const int t = tile_count<CG>(plan.ph[f], plan.batch);
+        most = t > most ? t : most;
     }
-    const int mt = (g.mblk + CG - 1) / CG, nt = (g.nblk + CG - 1) / CG;
-    const int64_t tiles = (int64_t)(g.sym ? mt * (mt + 1) / 2 : mt * nt) * g.batch * g.nprob;
-    const int groups = (int)(tiles < n / CG ? tiles : n / CG);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(groups * CG);
+    cfg.gridDim = dim3((most < groups ? most : groups) * CG);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;
+    cudaLaunchAttribute at[3];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = CG;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeCooperative;
+    at[1].val.cooperative = 1;
+    at[2].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[2].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 3;
+    return cudaLaunchKernelEx(&cfg, k_ortho_products<CG>, plan);
+}
+
+// How many groups of CG CTAs the device holds at once (once per device: *cache).
+template <int CG>
+cudaError_t resident_groups(std::atomic<int> &cache, int device, int *groups)
+{
+    *groups = cache.load(std::memory_order_acquire);
+    if (*groups > 0)
+        return cudaSuccess;
+    int sms = 0;
+    cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_ortho_products<CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(sms / CG * CG);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = CG;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_ortho_gemm<CG, EPI>, g);
+    if (e == cudaSuccess)
+        e = cudaOccupancyMaxActiveClusters(groups, k_ortho_products<CG>, &cfg);
+    if (e != cudaSuccess)
+        return e;
+    if (*groups < 1)
+        return cudaErrorLaunchOutOfResources;
+    *groups = *groups < sms / CG ? *groups : sms / CG;
+    cache.store(*groups, std::memory_order_release);
+    return cudaSuccess;
 }
 
+// Steps of the ring on the busiest CTA.
 template <int CG>
-cudaError_t launch_epi(const OrthoGemm &g, int epi, int device, cudaStream_t stream)
+int64_t steps(const OrthoPlan &plan, int groups)
 {
-    switch (epi) {
-    case kEpiGram: return launch<CG, kEpiGram>(g, device, stream);
-    case kEpiPoly: return launch<CG, kEpiPoly>(g, device, stream);
-    case kEpiSym: return launch<CG, kEpiSym>(g, device, stream);
-    case kEpiApply: return launch<CG, kEpiApply>(g, device, stream);
-    case kEpiOut: return launch<CG, kEpiOut>(g, device, stream);
-    default: return launch<CG, kEpiMuon>(g, device, stream);
+    int64_t sum = 0;
+    for (int f = 0; f < plan.n_phases; ++f) {
+        const int t = tile_count<CG>(plan.ph[f], plan.batch);
+        sum += (int64_t)((t + groups - 1) / groups) * plan.ph[f].k64;
     }
+    return sum;
 }
 
 }  // namespace
 
-cudaError_t launch_ortho_gemm(const OrthoGemm &g, int epi, int device, cudaStream_t stream)
+cudaError_t launch_ortho_products(const OrthoPlan &plan, int device, cudaStream_t stream)
 {
     if (device < 0 || device >= kMaxDevices)
         return cudaErrorInvalidDevice;
-    return launch_epi<1>(g, epi, device, stream);
+    static std::atomic<int> singles[kMaxDevices], pairs[kMaxDevices];
+    int n1 = 0, n2 = 0;
+    cudaError_t e = resident_groups<1>(singles[device], device, &n1);
+    if (e == cudaSuccess)
+        e = resident_groups<2>(pairs[device], device, &n2);
+    if (e != cudaSuccess)
+        return e;
+    // A pair of CTAs on a 256 x 256 tile takes 0.39 us a step, a single one on
+    // 128 x 128 0.33 us with every SM at it (both bound by what L2 delivers,
+    // 15 TB/s): pairs do 3.3 times the work per step, but a matrix has four
+    // times fewer tiles for them.
+    if (39 * steps<2>(plan, n2) <= 33 * steps<1>(plan, n1))
+        return launch<2>(plan, n2, stream);
+    return launch<1>(plan, n1, stream);
 }
 
 }  // namespace slide

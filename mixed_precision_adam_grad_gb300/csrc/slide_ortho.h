@@ -1,16 +1,17 @@
 // slide_ortho.h — internal interface of the Newton-Schulz products
 // (ortho_gemm.cu) and the code that plans them (ortho.cu).
 //
-// Tiled layouts of the workspace's matrices.  A matrix is cut into row blocks
-// of 128; a T16 matrix (FP16) keeps, row block by row block, tiles of 128 rows
-// x 64 columns of 16 KiB, a T32 matrix (FP32) tiles of 128 x 32, also 16 KiB.
-// Inside a tile each row's 128 bytes are eight 16-byte chunks, and chunk c of
-// row r lies at place c ^ (r & 7): the 128-byte swizzle the matrix unit reads,
-// so a tile goes to shared memory as one linear bulk copy.  The same bytes
-// serve as a K-major operand (rows along M or N) and as an MN-major one (rows
-// along K), so no matrix is ever transposed.  A symmetric matrix keeps only
-// its upper 128 x 128 blocks: block (i, j), i > j, is read as block (j, i)
-// with the other major-ness.
+// Every m x n matrix of the iteration is a pair of FP16 matrices, hi and lo,
+// for the value (hi + lo/2048) / s with s a power of two: 22 bits, and hi is
+// at the same time the operand of the next product.  A matrix lies in tiles of
+// 128 rows x 64 columns of 16 KiB, row block after row block.  Inside a tile
+// each row's 128 bytes are eight 16-byte chunks, and chunk c of row r lies at
+// place c ^ (r & 7): the 128-byte swizzle the matrix unit reads, so a tile
+// goes to shared memory as one linear bulk copy.  The same bytes serve as a
+// K-major operand (rows along M or N) and as an MN-major one (rows along K),
+// so no matrix is ever transposed.  A symmetric matrix keeps only its upper
+// 128 x 128 blocks: block (i, j), i > j, is read as block (j, i) with the
+// other major-ness.
 #pragma once
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -18,59 +19,72 @@
 
 namespace slide {
 
-constexpr int kTileElems16 = 128 * 64;  // halves of a T16 tile
-constexpr int kTileElems32 = 128 * 32;  // floats of a T32 tile
+constexpr int kTileElems = 128 * 64;   // values of a tile
+constexpr float kLoScale = 2048.0f;    // lo holds the rounding error of hi times this
 
 enum OperandKind { kOperandK = 0, kOperandMN = 1, kOperandSym = 2 };
 
+// What becomes of the product: value = alpha*acc, then
 enum EpilogueKind {
-    kEpiGram = 0,    // G = acc: out16, and out32 if given
-    kEpiPoly = 1,    // B = b*C16 + c*acc: out16 without the diagonal, dvec_out = a + diag; out32/out16b = aI + B if given
-    kEpiSym = 2,     // Y = d_i*C32 + acc: out16 (diag_out: without the diagonal, which goes to dvec_out) and out32 if given
-    kEpiApply = 3,   // X = d*C32 + acc: out32 and out16
+    kEpiGram = 0,    // G = value
+    kEpiPoly = 1,    // B = c_scale*C.hi + value: out (hi only) without its diagonal, dvec_out = coef_a + diagonal
+    kEpiSym = 2,     // Y = d_i*C + value.  With dvec2 (the product of two factors diag(d) + O that are kept as such):
+                     // Y = d_i*C.hi + dvec2_j*C.lo + value, and d_i*dvec2_i on the diagonal.  With diag_out only hi,
+                     // without the diagonal, which goes to dvec_out
+    kEpiApply = 3,   // X = d*C + value
     kEpiOut = 4,     // X as in kEpiApply, rounded to BF16 into the caller's array
     kEpiMuon = 5     // X as in kEpiApply, applied to the caller's master weights
 };
 
-struct OrthoOperands {
+struct OrthoPair {
+    __half *hi, *lo;
+};
+
+struct OrthoProduct {
     const __half *a, *b;
-    const float *c32;
-    const __half *c16;
-    const float *dvec;
-    float *out32;
-    __half *out16, *out16b;
+    OrthoPair c;          // read
+    OrthoPair out;        // written
+    const float *dvec, *dvec2;
     float *dvec_out;
+    float alpha;
+    float c_scale;        // of C (1/its scale; for kEpiPoly times b)
+    float c_scale2;       // of C.lo, with dvec2
+    float s_out;          // scale of out
+    int diag_out;
 };
 
 struct OrthoGemm {
-    OrthoOperands p[2];      // nprob products of one shape
-    int nprob, batch;
+    OrthoProduct p[2];       // nprob products of one shape and kind
+    int epi;                 // EpilogueKind
+    int nprob;
     int a_kind, b_kind;      // OperandKind
     int a_c64, b_c64;        // tiles of a row block of each operand
-    int64_t a_stride, b_stride;  // halves from one matrix of the batch to the next
+    int64_t a_stride, b_stride;  // values from one matrix of the batch to the next
     int k64;                 // steps of 64 along K
     int mblk, nblk;          // 128-blocks of the result
     int sym;                 // only the upper blocks of the result
-    int out_c64;             // T16 tiles of a row block of the result (T32: twice as many)
-    int64_t out_stride;      // elements from one matrix to the next
+    int out_c64;             // tiles of a row block of C and the results
+    int64_t out_stride;      // values from one matrix to the next
     int d_stride;            // floats of dvec per matrix
     int d_by_col;            // dvec scales columns
-    int diag_out;
-    float alpha;             // acc -> value
-    float c16_scale;         // b / scale of C16
     float coef_a;
-    float s16, s16b;         // scales of out16 and out16b
-    const float *c_inv;      // per matrix factor of C32, or NULL
+};
+
+constexpr int kMaxPhases = 32;  // products of one launch, one after the other
+
+struct OrthoPlan {
+    OrthoGemm ph[kMaxPhases];
+    int n_phases, batch;
+    unsigned *status;        // a word, and behind it an arrival counter per phase (zero at the start)
     // kEpiOut and kEpiMuon
     int rows, cols;
     uint16_t *w;
     int64_t w_row, w_batch;  // strides in elements
     float *theta;            // contiguous
     float decay, step;
-    unsigned *status;
     int test_stall;
 };
 
-cudaError_t launch_ortho_gemm(const OrthoGemm &g, int epi, int device, cudaStream_t stream);
+cudaError_t launch_ortho_products(const OrthoPlan &plan, int device, cudaStream_t stream);
 
 }  // namespace slide

@@ -26,7 +26,12 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
 // Arrive on a barrier of this or another CTA of the cluster (an address from map_to_rank).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity)
@@ -35,7 +40,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity)
     asm volatile(
         "{\n"
         " .reg .pred p;\n"
-        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
         " selp.u32 %0, 1, 0, p;\n"
         "}\n"
         : "=r"(done)
@@ -52,7 +57,8 @@ __device__ __forceinline__ unsigned long long global_ns()
 }
 
 // Wait for the phase of `bar` with the given parity; false if the limit passed
-// first or *abort (a flag of the CTA, set by a wait that ran out) was seen.
+// first or *abort (a flag of the CTA, set by a wait that ran out; may be NULL)
+// was seen.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort)
 {
     if (mbar_try_wait(bar, parity))
@@ -62,7 +68,32 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
         for (int i = 0; i < 32; ++i)
             if (mbar_try_wait(bar, parity))
                 return true;
-        if (*abort || global_ns() - t0 > kWaitLimitNs)
+        if ((abort && *abort) || global_ns() - t0 > kWaitLimitNs)
+            return false;
+    }
+    return false;
+}
+
+__device__ __forceinline__ unsigned load_acquire(const unsigned *p)
+{
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+// Wait until *counter has reached `target`; false if the limit passed first,
+// or bit `stop` of *status or *abort was seen.
+__device__ __forceinline__ bool counter_wait(const unsigned *counter, unsigned target, const unsigned *status,
+                                             unsigned stop, volatile int *abort)
+{
+    if (load_acquire(counter) >= target)
+        return true;
+    const unsigned long long t0 = global_ns();
+    for (uint32_t round = 0; round < kWaitLimitTries / 32; ++round) {
+        for (int i = 0; i < 32; ++i)
+            if (load_acquire(counter) >= target)
+                return true;
+        if (*abort || (load_acquire(status) & stop) || global_ns() - t0 > kWaitLimitNs)
             return false;
     }
     return false;
@@ -103,6 +134,28 @@ __device__ __forceinline__ void bulk_wait()
 // Order this thread's ordinary accesses before later ones of the copy and matrix engines.
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// One lane of a converged warp.  Code that a whole warp runs up to here keeps
+// its addresses and descriptors in uniform registers, which the copy and
+// matrix instructions take; under a test of the lane number they would be
+// moved there one by one (the products ran at half the rate).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t is;
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " elect.sync _|p, 0xffffffff;\n"
+        " selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(is));
+    return is != 0;
+}
+
+// Programmatic serialisation: let the next launch's blocks start, and wait for
+// the end of the launch before this one (its writes are then visible).
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---- clusters ---------------------------------------------------------------
 
