@@ -155,6 +155,7 @@ def _load():
 
 
 _LIB = None
+_FAST = None
 
 
 def _lib():
@@ -163,6 +164,23 @@ def _lib():
     if _LIB is None:
         _LIB = _load()
     return _LIB
+
+
+def _fast():
+    """The C module _fastcall, bound to the loaded library."""
+    global _FAST
+    if _FAST is None:
+        L = _lib()
+        try:
+            from . import _fastcall as F
+        except ImportError as e:
+            raise ImportError("the C module _fastcall is missing: build it first "
+                              "(python -m mixed_precision_adam_grad_gb300.build)") from e
+        for name in ("slide_route_experts", "slide_route_experts_backward", "slide_route_bias_step",
+                     "slide_orthogonalize", "slide_muon_step"):
+            F.bind(name, C.cast(getattr(L, name), C.c_void_p).value)
+        _FAST = F
+    return _FAST
 
 
 def __getattr__(name):
@@ -446,21 +464,21 @@ def slide_orthogonalize(batch: int, rows: int, cols: int, x, bf16_out, params: s
     ws, nbytes = _workspace(workspace, workspace_bytes)
     xr = cols if x_row_stride is None else x_row_stride
     orow = cols if out_row_stride is None else out_row_stride
-    _check(_lib().slide_orthogonalize(batch, rows, cols, _ptr(x), x_type, xr,
-                                      rows * xr if x_batch_stride is None else x_batch_stride, _ptr(bf16_out), orow,
-                                      rows * orow if out_batch_stride is None else out_batch_stride, C.byref(params),
-                                      ws, nbytes, _stream(stream)))
+    rc = _fast().orthogonalize(batch, rows, cols, x, x_type, xr, rows * xr if x_batch_stride is None else x_batch_stride,
+                               bf16_out, orow, rows * orow if out_batch_stride is None else out_batch_stride, params, ws,
+                               nbytes, stream)
+    if rc:
+        _check(rc)
 
 
 def slide_muon_step(batch: int, rows: int, cols: int, grad_replicas, master, momentum, bf16_out,
                     hp: slide_muon_hparams, workspace, grads_type=SLIDE_TYPE_BF16, workspace_bytes=None,
                     stream=None) -> None:
     """The Muon step of a batch of contiguous matrices (see include/slide.h)."""
-    ptrs = [_ptr(g) for g in grad_replicas]
-    arr = (C.c_void_p * max(1, len(ptrs)))(*ptrs)
     ws, nbytes = _workspace(workspace, workspace_bytes)
-    _check(_lib().slide_muon_step(batch, rows, cols, len(ptrs), arr, grads_type, _ptr(master), _ptr(momentum),
-                                  _ptr(bf16_out), C.byref(hp), ws, nbytes, _stream(stream)))
+    rc = _fast().muon_step(batch, rows, cols, grad_replicas, grads_type, master, momentum, bf16_out, hp, ws, nbytes, stream)
+    if rc:
+        _check(rc)
 
 
 def slide_ortho_status(workspace, stream=None) -> int:
@@ -493,24 +511,27 @@ def route_config(n_experts: int, top_k: int, score=SLIDE_SCORE_SIGMOID, n_groups
 def slide_route_experts(tokens: int, logits, weights, experts, cfg: slide_route_config, bias=None, token_mask=None,
                         load=None, logits_type=SLIDE_TYPE_FP32, logits_stride=None, stream=None) -> None:
     """Scores, choice and weights of each token's experts (see include/slide.h)."""
-    _check(_lib().slide_route_experts(tokens, _ptr(logits), logits_type,
-                                      cfg.n_experts if logits_stride is None else logits_stride, _ptr(bias),
-                                      _ptr(token_mask), C.byref(cfg), _ptr(weights), _ptr(experts), _ptr(load),
-                                      _stream(stream)))
+    rc = (_FAST or _fast()).route_experts(tokens, logits, logits_type,
+                                          cfg.n_experts if logits_stride is None else logits_stride, bias, token_mask,
+                                          cfg, weights, experts, load, stream)
+    if rc:
+        _check(rc)
 
 
 def slide_route_experts_backward(tokens: int, logits, experts, d_weights, d_logits, cfg: slide_route_config,
                                  token_mask=None, logits_type=SLIDE_TYPE_FP32, logits_stride=None,
                                  d_logits_stride=None, stream=None) -> None:
     """d_logits from d_weights, the choice held fixed."""
-    _check(_lib().slide_route_experts_backward(tokens, _ptr(logits), logits_type,
-                                               cfg.n_experts if logits_stride is None else logits_stride,
-                                               _ptr(experts), _ptr(d_weights), _ptr(token_mask), C.byref(cfg),
-                                               _ptr(d_logits),
-                                               cfg.n_experts if d_logits_stride is None else d_logits_stride,
-                                               _stream(stream)))
+    rc = (_FAST or _fast()).route_experts_backward(tokens, logits, logits_type,
+                                                   cfg.n_experts if logits_stride is None else logits_stride, experts,
+                                                   d_weights, token_mask, cfg, d_logits,
+                                                   cfg.n_experts if d_logits_stride is None else d_logits_stride, stream)
+    if rc:
+        _check(rc)
 
 
 def slide_route_bias_step(n_experts: int, load, bias, rate: float, stream=None) -> None:
     """bias += rate * sign(mean load - load); load = 0."""
-    _check(_lib().slide_route_bias_step(n_experts, _ptr(load), _ptr(bias), rate, _stream(stream)))
+    rc = (_FAST or _fast()).route_bias_step(n_experts, load, bias, rate, stream)
+    if rc:
+        _check(rc)

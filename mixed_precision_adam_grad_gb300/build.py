@@ -3,13 +3,16 @@
     python -m mixed_precision_adam_grad_gb300.build
 
 Each .cu under csrc/ compiles in parallel to _build/*.o, then one nvcc link
-makes libslide.so next to this file (CUDA runtime linked statically).
+makes libslide.so next to this file (CUDA runtime linked statically).  The C
+module _fastcall, through which the binding makes its hottest calls, is built
+beside it.
 """
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libslide.so")
+FASTCALL = os.path.join(PKG, "_fastcall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "-Xcompiler", "-fvisibility=hidden",
@@ -52,8 +56,22 @@ def _compile(src, extra):
     return obj
 
 
+def build_fastcall() -> str:
+    src = os.path.join(CSRC, "fastcall.c")
+    if _stale(FASTCALL, [src] + _deps()):
+        tmp = FASTCALL + f".tmp{os.getpid()}"
+        cmd = ["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], src,
+               "-o", tmp]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"gcc failed on {src}:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, FASTCALL)
+    return FASTCALL
+
+
 def build(verbose_ptxas: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
+    build_fastcall()
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
     srcs = sources()
     with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:

@@ -3,13 +3,25 @@
 // (slide_route_experts_backward) and the step of the balancing bias
 // (slide_route_bias_step).
 //
-// One warp per token; lane l holds the NV = 1, 2, 4, ... 32 consecutive
-// experts from l*NV on, in registers, so a row is read once.  Every choice is
+// A token has LPT = 8, 16 or 32 lanes of a warp (a warp 32/LPT tokens); its
+// lane l holds the NV = 2, 4, 8, 16 or 32 consecutive experts from l*NV on, in
+// registers, so a row is read once.  Every choice is
 // made on 32-bit keys whose unsigned order is the order of the FP32 values
-// (0 = not available), so a pick is the maximum of the lane's keys, one
-// warp-wide maximum and a ballot; the lowest lane holding it has the lowest
-// expert, which decides ties.  The scores that enter a choice are single FP32
-// operations, each rounded, with the accurate exponential: 1 / (1 + exp(-x)).
+// (0 = not available).  Each lane sorts its keys once, in runs of at most
+// eight, so that a pick is one maximum of the runs' heads over the token's lanes, a ballot
+// and a shift in the lane that held it; the lowest lane holding the maximum
+// has the lowest expert, which decides ties.  Which experts they were is
+// looked up at the end, all picks at once: lane p finds pick p's key among its
+// owner's, and of equal ones takes the next that no earlier pick took.  The
+// chosen experts' scores are formed again from their logits.
+// The scores that enter a choice are single FP32 operations, each rounded,
+// with the accurate exponential: 1 / (1 + exp(-x)).
+//
+// Bound by instructions: at 65536 tokens x 256 experts the rows take 11 us
+// from memory, the kernel 65 us: the FP32 sigmoids take two fifths of its
+// instructions, the picks a third.  Eight experts per lane are best: 16 lanes
+// of 16 there took 94 us (the sort and the pops of two runs), while 8 lanes of
+// 8 need less than half the instructions of 32 lanes of 2 for 60 experts.
 #include <cuda_runtime.h>
 #include <float.h>
 
@@ -25,7 +37,8 @@ namespace {
 
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;
-constexpr int kWarps = 8;
+constexpr int kWarps = 8;      // of a block
+constexpr int kAnyWarps = 4;   // where each needs shared memory
 constexpr float kTiny = 1e-20f;
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -41,8 +54,10 @@ struct RouteArgs {
     int E, K, groups, top_groups, group_size, group_max;
     int renorm;
     float scale;
-    int vec;
+    int vec, bias_vec;
 };
+
+constexpr uint32_t kKeyNone = 0x007fffffu, kKeyInf = 0xff800000u;  // keys of -inf and inf
 
 __device__ __forceinline__ uint32_t key_of(float x)
 {
@@ -94,7 +109,29 @@ __device__ __forceinline__ void load_row(const T *row, int lane, int E, bool vec
         x[i] = e0 + i < E ? widen(row[e0 + i]) : -INFINITY;
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-x))); }
+__device__ __forceinline__ float sigmoid(float x) { return __frcp_rn(__fadd_rn(1.0f, expf(-x))); }
+
+// The bias of the lane's experts (0 beyond the last), four at a time where
+// they are aligned.
+template <int NV>
+__device__ __forceinline__ void load_bias(const RouteArgs &a, int lane, float (&b)[NV])
+{
+    const int e0 = lane * NV;
+    if constexpr (NV >= 4) {
+        if (a.bias_vec && e0 + NV <= a.E) {
+#pragma unroll
+            for (int q = 0; q < NV / 4; ++q) {
+                const float4 w = __ldg(reinterpret_cast<const float4 *>(a.bias + e0) + q);
+                b[4 * q] = w.x, b[4 * q + 1] = w.y, b[4 * q + 2] = w.z, b[4 * q + 3] = w.w;
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (e0 + i < a.E)
+            b[i] = __ldg(a.bias + e0 + i);
+}
 
 __device__ __forceinline__ float warp_max(float x)
 {
@@ -112,14 +149,69 @@ __device__ __forceinline__ float warp_sum(float x)
     return x;
 }
 
+// Sorted keys: L = 1, 2 or 4 runs of R = min(NV, 8), largest first.
 template <int NV>
-__device__ __forceinline__ uint32_t lane_max(const uint32_t (&key)[NV])
+struct Runs {
+    static constexpr int R = NV < 8 ? NV : 8, L = NV / R;
+    uint32_t key[L][R];
+};
+
+template <int NV>
+__device__ __forceinline__ void sort_runs(const uint32_t (&key)[NV], Runs<NV> &r)
 {
-    uint32_t m = key[0];
+    constexpr int R = Runs<NV>::R, L = Runs<NV>::L;
 #pragma unroll
-    for (int i = 1; i < NV; ++i)
-        m = max(m, key[i]);
+    for (int l = 0; l < L; ++l) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            r.key[l][i] = key[l * R + i];
+        // odd-even merge sort
+#pragma unroll
+        for (int p = 1; p < R; p *= 2) {
+#pragma unroll
+            for (int k = p; k >= 1; k /= 2) {
+#pragma unroll
+                for (int j = k % p; j + k < R; j += 2 * k) {
+#pragma unroll
+                    for (int i = 0; i < k; ++i) {
+                        if (i + j + k < R && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                            const uint32_t x = r.key[l][i + j], y = r.key[l][i + j + k];
+                            r.key[l][i + j] = max(x, y);
+                            r.key[l][i + j + k] = min(x, y);
+                        }
+                    }
+                }
+            }
+        }
+    }
+}
+
+template <int NV>
+__device__ __forceinline__ uint32_t head(const Runs<NV> &r)
+{
+    uint32_t m = r.key[0][0];
+#pragma unroll
+    for (int l = 1; l < Runs<NV>::L; ++l)
+        m = max(m, r.key[l][0]);
     return m;
+}
+
+// Takes the head m off one run that has it.
+template <int NV>
+__device__ __forceinline__ void pop(Runs<NV> &r, uint32_t m)
+{
+    constexpr int R = Runs<NV>::R, L = Runs<NV>::L;
+    bool done = false;
+#pragma unroll
+    for (int l = 0; l < L; ++l) {
+        if (!done && (L == 1 || r.key[l][0] == m)) {
+            done = true;
+#pragma unroll
+            for (int i = 0; i + 1 < R; ++i)
+                r.key[l][i] = r.key[l][i + 1];
+            r.key[l][R - 1] = 0;
+        }
+    }
 }
 
 // Rank of a group from its best two keys (0 = none).
@@ -130,223 +222,255 @@ __device__ __forceinline__ uint32_t group_rank(uint32_t k1, uint32_t k2, bool on
     return key_of(__fadd_rn(value_of(k1), value_of(k2)));
 }
 
-// Drop the keys of all but the best groups.
-template <int NV>
-__device__ __forceinline__ void keep_groups(uint32_t (&key)[NV], const RouteArgs &a, int lane)
+// Maximum over the LPT lanes of a token.
+template <int LPT>
+__device__ __forceinline__ uint32_t token_max(uint32_t x)
 {
-    const int gs = a.group_size, lanes = gs / NV;
-    if (gs % NV == 0 && (lanes & (lanes - 1)) == 0 && lanes <= 32) {
-        // a group is a run of 1, 2, 4, ... lanes: its best two by exchanges
-        uint32_t k1 = 0, k2 = 0;
+    if constexpr (LPT == 32)
+        return __reduce_max_sync(kFull, x);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            k2 = max(k2, min(k1, key[i]));
-            k1 = max(k1, key[i]);
-        }
-        for (int o = 1; o < lanes; o <<= 1) {
-            const uint32_t o1 = __shfl_xor_sync(kFull, k1, o), o2 = __shfl_xor_sync(kFull, k2, o);
-            k2 = max(max(k2, o2), min(k1, o1));
-            k1 = max(k1, o1);
-        }
-        const uint32_t rank = group_rank(k1, k2, a.group_max);
-        uint32_t left = rank;  // of the lane's group, 0 once it is taken
-        for (int p = 0; p < a.top_groups; ++p) {
-            const uint32_t m = __reduce_max_sync(kFull, left);
-            if (m == 0)
-                break;
-            const int owner = __ffs(__ballot_sync(kFull, left == m)) - 1;
-            if (lane / lanes == owner / lanes)
-                left = 0;
-        }
-        const bool kept = left == 0;  // groups of rank 0 have nothing to drop
+    for (int o = LPT / 2; o > 0; o >>= 1)
+        x = max(x, __shfl_xor_sync(kFull, x, o));
+    return x;
+}
+
+template <int LPT>
+__device__ __forceinline__ float token_sum(float x)
+{
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            key[i] = kept ? key[i] : 0;
-        return;
+    for (int o = LPT / 2; o > 0; o >>= 1)
+        x += __shfl_xor_sync(kFull, x, o);
+    return x;
+}
+
+// The token's lanes for which `is` holds, as the lowest bits.
+template <int LPT>
+__device__ __forceinline__ uint32_t token_ballot(bool is, int lane)
+{
+    const uint32_t b = __ballot_sync(kFull, is);
+    if constexpr (LPT == 32)
+        return b;
+    return (b >> (lane & ~(LPT - 1))) & ((1u << (LPT & 31)) - 1);
+}
+
+// For groups of 1, 2, 4, ... whole lanes: whether the lane's is one of the best,
+// from the lane's sorted keys.
+template <int LPT, int NV>
+__device__ __forceinline__ bool lane_kept(const Runs<NV> &r, const RouteArgs &a, int lane)
+{
+    const int lanes = a.group_size / NV;
+    uint32_t k1 = 0, k2 = 0;
+#pragma unroll
+    for (int l = 0; l < Runs<NV>::L; ++l) {
+        k2 = max(max(k2, r.key[l][1]), min(k1, r.key[l][0]));
+        k1 = max(k1, r.key[l][0]);
     }
-    // any size: one group after the other; lane g holds the rank of groups g, g + 32, ...
-    uint32_t ranks[kMaxExperts / 32];
-    const int rounds = (a.groups + 31) / 32;
-#pragma unroll
-    for (int r = 0; r < kMaxExperts / 32; ++r)
-        ranks[r] = 0;
-    for (int g = 0; g < a.groups; ++g) {
-        uint32_t k1 = 0, k2 = 0;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = lane * NV + i;
-            const uint32_t k = e >= g * gs && e < (g + 1) * gs ? key[i] : 0;
-            k2 = max(k2, min(k1, k));
-            k1 = max(k1, k);
-        }
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t o1 = __shfl_xor_sync(kFull, k1, o), o2 = __shfl_xor_sync(kFull, k2, o);
-            k2 = max(max(k2, o2), min(k1, o1));
-            k1 = max(k1, o1);
-        }
-        const uint32_t rank = group_rank(k1, k2, a.group_max);
-#pragma unroll
-        for (int r = 0; r < kMaxExperts / 32; ++r)
-            if (g == r * 32 + lane)
-                ranks[r] = rank;
+    for (int o = 1; o < lanes; o <<= 1) {
+        const uint32_t o1 = __shfl_xor_sync(kFull, k1, o), o2 = __shfl_xor_sync(kFull, k2, o);
+        k2 = max(max(k2, o2), min(k1, o1));
+        k1 = max(k1, o1);
     }
-    uint32_t kept[kMaxExperts / 32];  // bit g of word g / 32, the same in every lane
-#pragma unroll
-    for (int r = 0; r < kMaxExperts / 32; ++r)
-        kept[r] = 0;
+    uint32_t left = group_rank(k1, k2, a.group_max);  // of the lane's group, 0 once it is taken
+    const int my = lane & (LPT - 1);
     for (int p = 0; p < a.top_groups; ++p) {
-        uint32_t mine = 0;
+        const uint32_t m = token_max<LPT>(left);
+        const int owner = __ffs(token_ballot<LPT>(left == m, lane)) - 1;
+        if (((my ^ owner) & ~(lanes - 1)) == 0)
+            left = 0;
+    }
+    return left == 0;  // groups of rank 0 have nothing to drop
+}
+
+// Groups of any size: drop the keys of all but the best.  keys and ranks: the
+// warp's shared memory, E and a.groups words.
+template <int NV>
+__device__ __forceinline__ void keep_groups(uint32_t (&key)[NV], const RouteArgs &a, int lane, uint32_t *keys,
+                                            uint32_t *ranks)
+{
+    const int gs = a.group_size;
+    __syncwarp();
 #pragma unroll
-        for (int r = 0; r < kMaxExperts / 32; ++r)
-            mine = max(mine, ranks[r]);
+    for (int i = 0; i < NV; ++i)
+        if (lane * NV + i < a.E)
+            keys[lane * NV + i] = key[i];
+    __syncwarp();
+    uint32_t mine = 0;  // best rank of the lane's groups lane, lane + 32, ...
+    for (int g = lane; g < a.groups; g += 32) {
+        uint32_t k1 = 0, k2 = 0;
+        for (int e = g * gs; e < (g + 1) * gs; ++e) {
+            k2 = max(k2, min(k1, keys[e]));
+            k1 = max(k1, keys[e]);
+        }
+        ranks[g] = group_rank(k1, k2, a.group_max);
+        mine = max(mine, ranks[g]);
+    }
+    for (int p = 0; p < a.top_groups; ++p) {
         const uint32_t m = __reduce_max_sync(kFull, mine);
         if (m == 0)
             break;
-        int best = kMaxExperts;
-#pragma unroll
-        for (int r = kMaxExperts / 32 - 1; r >= 0; --r)
-            if (r < rounds && ranks[r] == m)
-                best = r * 32 + lane;
+        int best = a.groups;
+        if (mine == m)
+            for (best = lane; ranks[best] != m; best += 32)
+                ;
         best = __reduce_min_sync(kFull, best);
-#pragma unroll
-        for (int r = 0; r < kMaxExperts / 32; ++r) {
-            if (best == r * 32 + lane)
-                ranks[r] = 0;
-            if (best >> 5 == r)
-                kept[r] |= 1u << (best & 31);
+        if (lane == (best & 31)) {
+            ranks[best] = 0;  // taken
+            mine = 0;
+            for (int g = lane; g < a.groups; g += 32)
+                mine = max(mine, ranks[g]);
         }
     }
+    __syncwarp();
+    // a group that had a rank and was not taken is dropped
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int g = (lane * NV + i) / gs;
-        uint32_t word = 0;
-#pragma unroll
-        for (int r = 0; r < kMaxExperts / 32; ++r)
-            if (g >> 5 == r)
-                word = kept[r];
-        key[i] = word >> (g & 31) & 1 ? key[i] : 0;
-    }
+    for (int i = 0; i < NV; ++i)
+        if (lane * NV + i < a.E && ranks[(lane * NV + i) / gs] != 0)
+            key[i] = 0;
 }
 
-template <typename T, int NV, bool SIGMOID>
-__global__ void __launch_bounds__(kWarps * 32) k_route(const RouteArgs a)
+// ANY: the groups are not runs of lanes; each warp (LPT is 32) then has E +
+// groups words of shared memory.
+template <typename T, int LPT, int NV, bool SIGMOID, bool ANY>
+__global__ void __launch_bounds__((ANY ? kAnyWarps : kWarps) * 32) k_route(const RouteArgs a)
 {
+    constexpr int kWarpsHere = ANY ? kAnyWarps : kWarps, kTokens = 32 / LPT;
     __shared__ unsigned hist[kMaxExperts];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    extern __shared__ uint32_t words[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, my = lane & (LPT - 1);
     if (a.load) {
-        for (int e = threadIdx.x; e < a.E; e += kWarps * 32)
+        for (int e = threadIdx.x; e < a.E; e += kWarpsHere * 32)
             hist[e] = 0;
         __syncthreads();
     }
-    float bias[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-        bias[i] = a.bias && lane * NV + i < a.E ? a.bias[lane * NV + i] : 0.0f;
     // a softmax keeps the order of the logits: the choice is made on them,
     // except where the scores' values matter (a bias, or sums of a group)
     const bool by_logit = !SIGMOID && !a.bias && (a.groups == 1 || a.group_max);
+    const bool by_lane = !ANY && a.groups > 1;
 
-    for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.tokens; t += (int64_t)gridDim.x * kWarps) {
-        int my_expert = -1;
-        float my_score = 0.0f;
+    for (int64_t t0 = ((int64_t)blockIdx.x * kWarpsHere + warp) * kTokens; t0 < a.tokens;
+         t0 += (int64_t)gridDim.x * kWarpsHere * kTokens) {
+        const int64_t t = t0 + lane / LPT;
+        const bool in = t < a.tokens, live = in && (!a.mask || a.mask[t]);
+        const T *row = static_cast<const T *>(a.logits) + t * a.row_stride;
+        float x[NV], top = 0.0f, sum = 1.0f;
+        uint32_t key[NV];
         bool nan = false;
-        if (!a.mask || a.mask[t]) {
-            float score[NV];
-            uint32_t key[NV];
-            load_row<T, NV>(static_cast<const T *>(a.logits) + t * a.row_stride, lane, a.E, a.vec, score);
-            if constexpr (SIGMOID) {
+        if (live) {
+            load_row<T, NV>(row, my, a.E, a.vec, x);
+        } else {
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const float x = score[i];
-                    score[i] = sigmoid(x);
-                    const float v = a.bias ? __fadd_rn(score[i], bias[i]) : score[i];
-                    nan |= v != v;
-                    key[i] = x == -INFINITY || v == -INFINITY ? 0 : key_of(v);
-                }
-            } else {
-                float top = -INFINITY;
+            for (int i = 0; i < NV; ++i)
+                x[i] = -INFINITY;
+        }
+        if constexpr (SIGMOID) {
+            float bias[NV];
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    nan |= score[i] != score[i];
-                    score[i] = fminf(score[i], FLT_MAX);
-                    top = fmaxf(top, score[i]);
-                }
-                top = warp_max(top);
-                float sum = 0.0f;
-                if (top > -INFINITY) {
+            for (int i = 0; i < NV; ++i)
+                bias[i] = 0.0f;
+            if (a.bias)
+                load_bias<NV>(a, my, bias);
 #pragma unroll
-                    for (int i = 0; i < NV; ++i) {
-                        key[i] = score[i] == -INFINITY ? 0 : key_of(score[i]);
-                        score[i] = expf(score[i] - top);
-                        sum += score[i];
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < NV; ++i) {
-                        key[i] = 0;
-                        score[i] = 0.0f;
-                    }
-                    sum = 1.0f;
-                }
-                sum = warp_sum(sum);
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    score[i] = __fdiv_rn(score[i], sum);
-                    if (!by_logit) {
-                        const float v = a.bias ? __fadd_rn(score[i], bias[i]) : score[i];
-                        nan |= v != v;
-                        key[i] = key[i] == 0 || v == -INFINITY ? 0 : key_of(v);
-                    }
-                }
+            for (int i = 0; i < NV; ++i) {
+                // neither a score nor its sum with a bias is -0
+                const uint32_t u = __float_as_uint(__fadd_rn(sigmoid(x[i]), bias[i]));
+                key[i] = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+                key[i] = x[i] == -INFINITY ? 0 : key[i];
             }
-            nan = __any_sync(kFull, nan);
-            if (!nan) {
-                if (a.groups > 1)
-                    keep_groups<NV>(key, a, lane);
-                uint32_t mine = lane_max<NV>(key);
-                for (int p = 0; p < a.K; ++p) {
-                    const uint32_t m = __reduce_max_sync(kFull, mine);
-                    if (m == 0)
-                        break;
-                    const int owner = __ffs(__ballot_sync(kFull, mine == m)) - 1;
-                    int at = 0;
-                    float s = 0.0f;
-                    if (lane == owner) {
+        } else {
+            top = -INFINITY;
 #pragma unroll
-                        for (int i = NV - 1; i >= 0; --i) {
-                            if (key[i] == m) {
-                                at = i;
-                                s = score[i];
-                            }
-                        }
+            for (int i = 0; i < NV; ++i) {
+                nan |= x[i] != x[i];
+                x[i] = fminf(x[i], FLT_MAX);
+                top = fmaxf(top, x[i]);
+                key[i] = key_of(x[i]);
+            }
 #pragma unroll
-                        for (int i = 0; i < NV; ++i)
-                            key[i] = i == at ? 0 : key[i];
-                        mine = lane_max<NV>(key);
-                    }
-                    at = __shfl_sync(kFull, at, owner);
-                    s = __shfl_sync(kFull, s, owner);
-                    if (lane == p) {
-                        my_expert = owner * NV + at;
-                        my_score = s;
-                    }
+            for (int o = LPT / 2; o > 0; o >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+            top = fmaxf(top, -FLT_MAX);  // where nothing is available
+            if (!(by_logit && a.renorm)) {
+                // scores are needed: for the keys, or for the weights' scale
+                sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    x[i] = expf(x[i] - top);
+                    sum += x[i];
                 }
-                if (a.renorm)
-                    my_score = __fdiv_rn(my_score, __fadd_rn(warp_sum(my_score), kTiny));
-                my_score *= a.scale;
+                sum = token_sum<LPT>(sum);
+                if (!by_logit) {
+                    float bias[NV];
+#pragma unroll
+                    for (int i = 0; i < NV; ++i)
+                        bias[i] = 0.0f;
+                    if (a.bias)
+                        load_bias<NV>(a, my, bias);
+#pragma unroll
+                    for (int i = 0; i < NV; ++i)
+                        key[i] = key[i] <= kKeyNone ? 0 : key_of(__fadd_rn(__fdiv_rn(x[i], sum), bias[i]));
+                }
             }
         }
-        if (lane < a.K) {
-            a.experts[t * a.K + lane] = my_expert;
-            a.weights[t * a.K + lane] = nan ? __int_as_float(0x7fffffff) : my_score;
-            if (a.load && my_expert >= 0)
-                atomicAdd(&hist[my_expert], 1u);
+        // keys up to that of -inf are none; a NaN's is above every number's
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            key[i] = key[i] <= kKeyNone ? 0 : key[i];
+        if constexpr (ANY) {
+            uint32_t *mine = words + warp * (a.E + a.groups);
+            keep_groups<NV>(key, a, lane, mine, mine + a.E);
+        }
+        Runs<NV> runs;
+        sort_runs<NV>(key, runs);
+        uint32_t mine = head<NV>(runs);
+        nan = token_ballot<LPT>(nan || mine > kKeyInf, lane) != 0;
+        const bool kept = !by_lane || lane_kept<LPT, NV>(runs, a, lane);
+        mine = kept ? mine : 0;
+        uint32_t my_key = 0;           // lane p: pick p's key, its owner and
+        int my_owner = 0, my_nth = 0;  // which of the owner's equal keys it is
+        uint32_t last = 0;
+        int last_owner = 0, nth = 0;
+        for (int p = 0; p < a.K; ++p) {
+            const uint32_t m = token_max<LPT>(mine);
+            const int owner = __ffs(token_ballot<LPT>(mine == m, lane)) - 1;
+            nth = m == last && owner == last_owner ? nth + 1 : 0;
+            last = m;
+            last_owner = owner;
+            if (my == p) {
+                my_key = m;
+                my_owner = owner;
+                my_nth = nth;
+            }
+            if (my == owner) {
+                pop<NV>(runs, m);
+                mine = kept ? head<NV>(runs) : 0;
+            }
+        }
+        int best = -1;  // lane p: the expert of pick p
+        const int from = (lane & ~(LPT - 1)) + my_owner;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const bool is = __shfl_sync(kFull, key[i], from) == my_key;
+            best = is && my_nth == 0 && best < 0 ? my_owner * NV + i : best;
+            my_nth -= is;
+        }
+        best = my_key == 0 || nan || !live ? -1 : best;
+        float score = 0.0f;
+        if (best >= 0) {
+            const float y = widen(row[best]);
+            score = SIGMOID ? sigmoid(y) : __fdiv_rn(expf(fminf(y, FLT_MAX) - top), sum);
+        }
+        if (a.renorm)
+            score = __fdiv_rn(score, __fadd_rn(token_sum<LPT>(score), kTiny));
+        if (in && my < a.K) {
+            a.experts[t * a.K + my] = best;
+            a.weights[t * a.K + my] = nan && live ? __int_as_float(0x7fffffff) : score * a.scale;
+            if (a.load && best >= 0)
+                atomicAdd(&hist[best], 1u);
         }
     }
     if (a.load) {
         __syncthreads();
-        for (int e = threadIdx.x; e < a.E; e += kWarps * 32)
+        for (int e = threadIdx.x; e < a.E; e += kWarpsHere * 32)
             if (hist[e])
                 atomicAdd(a.load + e, (unsigned long long)hist[e]);
     }
@@ -379,10 +503,75 @@ __device__ __forceinline__ T narrow(float x)
     }
 }
 
-// dlogits of one token per warp.  Only the chosen experts have a gradient,
-// except for a softmax that is not renormalised, whose row is dense (DENSE).
-template <typename T, int NV, bool SIGMOID, bool DENSE>
-__global__ void __launch_bounds__(kWarps * 32) k_route_back(const BackArgs a)
+// Gradient where only the chosen experts have one: W = 1, 2, 4, ... 32 lanes
+// (at least top_k) per token, 32/W tokens per warp at a time.  The rows are
+// filled with zeros, then the chosen experts' values go over them.
+template <typename T, bool SIGMOID>
+__global__ void __launch_bounds__(kWarps * 32) k_route_back_sparse(const BackArgs a, int W)
+{
+    const int lane = threadIdx.x & 31;
+    constexpr int kPer = 16 / sizeof(T);
+    const int at_once = 32 / W, place = lane & (W - 1);
+    const int64_t step = (int64_t)gridDim.x * kWarps * at_once;
+    for (int64_t t0 = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * at_once; t0 < a.tokens; t0 += step) {
+        const int64_t t = t0 + lane / W;
+        int e = -1;
+        float dw = 0.0f;
+        if (t < a.tokens && place < a.K && (!a.mask || a.mask[t])) {
+            e = a.experts[t * a.K + place];
+            dw = a.d_weights[t * a.K + place] * a.scale;
+            if (e < 0 || e >= a.E) {
+                e = -1;
+                dw = 0.0f;
+            }
+        }
+        const float x = e >= 0 ? fminf(widen(static_cast<const T *>(a.logits)[t * a.row_stride + e]), FLT_MAX) : -INFINITY;
+        // the rows of the warp's tokens, in whole vectors where they are aligned
+        const int rows = (int)(a.tokens - t0 < at_once ? a.tokens - t0 : at_once);
+        for (int r = 0; r < rows; ++r) {
+            T *out = static_cast<T *>(a.d_logits) + (t0 + r) * a.d_stride;
+            if (a.d_vec) {
+                for (int c = lane * kPer; c < a.E; c += 32 * kPer)
+                    *reinterpret_cast<uint4 *>(out + c) = make_uint4(0, 0, 0, 0);
+            } else {
+                for (int c = lane; c < a.E; c += 32)
+                    out[c] = T(0);
+            }
+        }
+        auto sum_of = [&](float v) {  // over the token's lanes
+            for (int o = 1; o < W; o <<= 1)
+                v += __shfl_xor_sync(kFull, v, o);
+            return v;
+        };
+        float dx;
+        if constexpr (SIGMOID) {
+            const float p = e >= 0 ? sigmoid(x) : 0.0f;
+            const float q = x > 0.0f ? expf(-x) * p : 1.0f - p;  // 1 - p without cancellation
+            float dp = dw;
+            if (a.renorm) {
+                const float total = sum_of(p) + kTiny;
+                dp = (dw - sum_of(dw * p) / total) / total;
+            }
+            dx = dp * p * q;
+        } else {
+            float top = x;
+            for (int o = 1; o < W; o <<= 1)
+                top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+            float p = e >= 0 ? expf(x - top) : 0.0f;
+            const float total = sum_of(p);
+            p = total > 0.0f ? p / total : 0.0f;
+            dx = p * (dw - sum_of(dw * p));
+        }
+        __syncwarp();
+        if (e >= 0)
+            static_cast<T *>(a.d_logits)[t * a.d_stride + e] = narrow<T>(dx);
+    }
+}
+
+// Gradient of a softmax that is not renormalised: the whole row, one token per
+// warp.
+template <typename T, int NV>
+__global__ void __launch_bounds__(kWarps * 32) k_route_back_dense(const BackArgs a)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kPer = 16 / sizeof(T);
@@ -398,10 +587,10 @@ __global__ void __launch_bounds__(kWarps * 32) k_route_back(const BackArgs a)
                 dw = a.d_weights[t * a.K + lane] * a.scale;
         }
         const bool any = __any_sync(kFull, e >= 0);
-        float x[NV], top = -INFINITY, sum = 0.0f;
-        const float xe = e >= 0 ? fminf(widen(row[e]), FLT_MAX) : -INFINITY;
-        float dx = 0.0f, base = 0.0f;
-        if (DENSE && any) {
+        float x[NV], dx = 0.0f, base = 0.0f;
+        if (any) {
+            const float xe = e >= 0 ? fminf(widen(row[e]), FLT_MAX) : -INFINITY;
+            float top = -INFINITY, sum = 0.0f;
             load_row<T, NV>(row, lane, a.E, a.vec, x);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -419,23 +608,11 @@ __global__ void __launch_bounds__(kWarps * 32) k_route_back(const BackArgs a)
             base = warp_sum(dw * p);
             dx = p * (dw - base);
             base = -base / sum;
-        } else if (any && SIGMOID) {
-            const float p = e >= 0 ? sigmoid(xe) : 0.0f;
-            float dp = dw;
-            if (a.renorm) {
-                const float total = warp_sum(p) + kTiny;
-                dp = (dw - warp_sum(dw * p) / total) / total;
-            }
-            dx = dp * p * (1.0f - p);
-        } else if (any) {
-            top = warp_max(xe);
-            float p = e >= 0 ? expf(xe - top) : 0.0f;
-            p /= warp_sum(p);
-            dx = p * (dw - warp_sum(dw * p));
         }
         // the row, then the chosen experts over it
-        if (a.d_vec) {
-            if constexpr (DENSE && NV >= kPer) {
+        bool done = false;
+        if constexpr (NV >= kPer) {
+            if (a.d_vec) {
 #pragma unroll
                 for (int q = 0; q < NV / kPer; ++q) {
                     const int at = lane * NV + q * kPer;
@@ -447,21 +624,14 @@ __global__ void __launch_bounds__(kWarps * 32) k_route_back(const BackArgs a)
                         *reinterpret_cast<uint4 *>(out + at) = *reinterpret_cast<uint4 *>(w);
                     }
                 }
-            } else if constexpr (!DENSE) {
-                for (int at = lane * kPer; at < a.E; at += 32 * kPer)
-                    *reinterpret_cast<uint4 *>(out + at) = make_uint4(0, 0, 0, 0);
+                done = true;
             }
         }
-        if (!a.d_vec || (DENSE && NV < kPer)) {
-            if constexpr (DENSE) {
+        if (!done) {
 #pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    if (lane * NV + i < a.E)
-                        out[lane * NV + i] = any ? narrow<T>(x[i] * base) : T(0);
-            } else {
-                for (int at = lane; at < a.E; at += 32)
-                    out[at] = T(0);
-            }
+            for (int i = 0; i < NV; ++i)
+                if (lane * NV + i < a.E)
+                    out[lane * NV + i] = any ? narrow<T>(x[i] * base) : T(0);
         }
         __syncwarp();
         if (e >= 0)
@@ -507,62 +677,107 @@ cudaError_t sm_count(int *n)
     return e;
 }
 
-template <typename T, int NV>
-cudaError_t launch_route(const RouteArgs &a, bool sig, int grid, cudaStream_t s)
+// Launches `kernel` with blocks of `warps` warps for `units` warps' worth of
+// work, but no more blocks than the device holds at once (*resident caches
+// that number per kernel).
+template <typename Kernel, typename... Args>
+cudaError_t launch_warps(Kernel kernel, std::atomic<int> &resident, int64_t units, int warps, size_t smem, int sms,
+                         cudaStream_t s, Args... args)
 {
-    if (sig)
-        k_route<T, NV, true><<<grid, kWarps * 32, 0, s>>>(a);
-    else
-        k_route<T, NV, false><<<grid, kWarps * 32, 0, s>>>(a);
+    int per_sm = resident.load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, warps * 32, smem);
+        if (e != cudaSuccess)
+            return e;
+        per_sm = per_sm > 0 ? per_sm : 1;
+        if (smem == 0)
+            resident.store(per_sm, std::memory_order_relaxed);
+    }
+    const int64_t blocks = (units + warps - 1) / warps, most = (int64_t)sms * per_sm;
+    kernel<<<(unsigned)(blocks < most ? blocks : most), warps * 32, smem, s>>>(args...);
     return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t launch_route(const RouteArgs &a, bool sig, int grid, cudaStream_t s)
+template <typename T, int LPT, int NV, bool ANY>
+cudaError_t launch_route(const RouteArgs &a, bool sig, int sms, cudaStream_t s)
 {
-    const int nv = (a.E + 31) / 32;
-    if (nv <= 1)
-        return launch_route<T, 1>(a, sig, grid, s);
-    if (nv <= 2)
-        return launch_route<T, 2>(a, sig, grid, s);
-    if (nv <= 4)
-        return launch_route<T, 4>(a, sig, grid, s);
-    if (nv <= 8)
-        return launch_route<T, 8>(a, sig, grid, s);
-    if (nv <= 16)
-        return launch_route<T, 16>(a, sig, grid, s);
-    return launch_route<T, 32>(a, sig, grid, s);
+    static std::atomic<int> resident[2];
+    const int warps = ANY ? kAnyWarps : kWarps;
+    const size_t smem = ANY ? sizeof(uint32_t) * kAnyWarps * (a.E + a.groups) : 0;  // at most 32 KiB
+    const int64_t units = (a.tokens + 32 / LPT - 1) / (32 / LPT);
+    return sig ? launch_warps(k_route<T, LPT, NV, true, ANY>, resident[0], units, warps, smem, sms, s, a)
+               : launch_warps(k_route<T, LPT, NV, false, ANY>, resident[1], units, warps, smem, sms, s, a);
+}
+
+// Whether groups of this size are runs of 1, 2, 4, ... lanes of nv experts.
+bool runs_of_lanes(const RouteArgs &a, int nv)
+{
+    const int lanes = a.group_size / nv;
+    return a.groups == 1 || (a.group_size % nv == 0 && (lanes & (lanes - 1)) == 0);
+}
+
+template <typename T>
+cudaError_t launch_route(const RouteArgs &a, bool sig, int sms, cudaStream_t s)
+{
+    // as few lanes per token as hold its picks, with eight experts each
+    if (a.K <= 8 && a.E <= 64) {
+        if (a.E <= 16 && runs_of_lanes(a, 2))
+            return launch_route<T, 8, 2, false>(a, sig, sms, s);
+        if (a.E <= 32 && runs_of_lanes(a, 4))
+            return launch_route<T, 8, 4, false>(a, sig, sms, s);
+        if (runs_of_lanes(a, 8))
+            return launch_route<T, 8, 8, false>(a, sig, sms, s);
+    }
+    if (a.K <= 16 && a.E <= 128) {
+        if (a.E <= 64 && runs_of_lanes(a, 4))
+            return launch_route<T, 16, 4, false>(a, sig, sms, s);
+        if (runs_of_lanes(a, 8))
+            return launch_route<T, 16, 8, false>(a, sig, sms, s);
+    }
+    if (a.E <= 64 && runs_of_lanes(a, 2))
+        return launch_route<T, 32, 2, false>(a, sig, sms, s);
+    if (a.E <= 256 && runs_of_lanes(a, 8))
+        return launch_route<T, 32, 8, false>(a, sig, sms, s);
+    if (a.E <= 512 && runs_of_lanes(a, 16))
+        return launch_route<T, 32, 16, false>(a, sig, sms, s);
+    if (runs_of_lanes(a, 32))
+        return launch_route<T, 32, 32, false>(a, sig, sms, s);
+    if (a.E <= 256)
+        return launch_route<T, 32, 8, true>(a, sig, sms, s);
+    return launch_route<T, 32, 32, true>(a, sig, sms, s);
 }
 
 template <typename T, int NV>
-cudaError_t launch_dense(const BackArgs &a, int grid, cudaStream_t s)
+cudaError_t launch_dense(const BackArgs &a, int sms, cudaStream_t s)
 {
-    k_route_back<T, NV, false, true><<<grid, kWarps * 32, 0, s>>>(a);
-    return cudaGetLastError();
+    static std::atomic<int> resident;
+    return launch_warps(k_route_back_dense<T, NV>, resident, a.tokens, kWarps, 0, sms, s, a);
 }
 
 template <typename T>
-cudaError_t launch_back(const BackArgs &a, bool sig, int grid, cudaStream_t s)
+cudaError_t launch_back(const BackArgs &a, bool sig, int sms, cudaStream_t s)
 {
     if (sig || a.renorm) {
-        if (sig)
-            k_route_back<T, 1, true, false><<<grid, kWarps * 32, 0, s>>>(a);
-        else
-            k_route_back<T, 1, false, false><<<grid, kWarps * 32, 0, s>>>(a);
-        return cudaGetLastError();
+        int W = 1;
+        while (W < a.K)
+            W *= 2;
+        static std::atomic<int> resident[2];
+        const int64_t units = (a.tokens + 32 / W - 1) / (32 / W);
+        return sig ? launch_warps(k_route_back_sparse<T, true>, resident[0], units, kWarps, 0, sms, s, a, W)
+                   : launch_warps(k_route_back_sparse<T, false>, resident[1], units, kWarps, 0, sms, s, a, W);
     }
     const int nv = (a.E + 31) / 32;
     if (nv <= 1)
-        return launch_dense<T, 1>(a, grid, s);
+        return launch_dense<T, 1>(a, sms, s);
     if (nv <= 2)
-        return launch_dense<T, 2>(a, grid, s);
+        return launch_dense<T, 2>(a, sms, s);
     if (nv <= 4)
-        return launch_dense<T, 4>(a, grid, s);
+        return launch_dense<T, 4>(a, sms, s);
     if (nv <= 8)
-        return launch_dense<T, 8>(a, grid, s);
+        return launch_dense<T, 8>(a, sms, s);
     if (nv <= 16)
-        return launch_dense<T, 16>(a, grid, s);
-    return launch_dense<T, 32>(a, grid, s);
+        return launch_dense<T, 16>(a, sms, s);
+    return launch_dense<T, 32>(a, sms, s);
 }
 
 bool misaligned(const void *p, size_t to) { return ((uintptr_t)p % to) != 0; }
@@ -591,13 +806,6 @@ slide_status check_route(int64_t tokens, const slide_route_config *c, int32_t ty
     if (!std::isfinite(c->scale))
         return fail(SLIDE_ERR_INVALID_ARG, "route config: non-finite scale");
     return SLIDE_OK;
-}
-
-int grid_for(int64_t tokens, int sms, int per_sm)
-{
-    const int64_t blocks = (tokens + kWarps - 1) / kWarps;
-    const int64_t most = (int64_t)sms * per_sm;
-    return (int)(blocks < most ? blocks : most);
 }
 
 }  // namespace
@@ -646,10 +854,10 @@ extern "C" slide_status slide_route_experts(int64_t tokens, const void *logits, 
     a.renorm = cfg->renormalize != 0;
     a.scale = cfg->scale;
     a.vec = !misaligned(logits, 16) && (logits_stride * size) % 16 == 0;
-    const int grid = grid_for(tokens, sms, 8);
+    a.bias_vec = !misaligned(bias, 16);
     const bool sig = cfg->score == SLIDE_SCORE_SIGMOID;
-    e = size == 4 ? launch_route<float>(a, sig, grid, (cudaStream_t)stream)
-                  : launch_route<uint16_t>(a, sig, grid, (cudaStream_t)stream);
+    e = size == 4 ? launch_route<float>(a, sig, sms, (cudaStream_t)stream)
+                  : launch_route<uint16_t>(a, sig, sms, (cudaStream_t)stream);
     if (e != cudaSuccess)
         return fail_cuda(e, "routing launch");
     clear_error();
@@ -698,10 +906,9 @@ extern "C" slide_status slide_route_experts_backward(int64_t tokens, const void 
     const size_t per = 16 / size;
     a.vec = !misaligned(logits, 16) && (logits_stride * size) % 16 == 0;
     a.d_vec = !misaligned(d_logits, 16) && (d_logits_stride * size) % 16 == 0 && cfg->n_experts % per == 0;
-    const int grid = grid_for(tokens, sms, 8);
     const bool sig = cfg->score == SLIDE_SCORE_SIGMOID;
-    e = size == 4 ? launch_back<float>(a, sig, grid, (cudaStream_t)stream)
-                  : launch_back<uint16_t>(a, sig, grid, (cudaStream_t)stream);
+    e = size == 4 ? launch_back<float>(a, sig, sms, (cudaStream_t)stream)
+                  : launch_back<uint16_t>(a, sig, sms, (cudaStream_t)stream);
     if (e != cudaSuccess)
         return fail_cuda(e, "routing gradient launch");
     clear_error();
