@@ -25,6 +25,7 @@
 
 #include "slide.h"
 #include "slide_ortho.h"
+#include "slide_ortho_small.h"
 #include "slide_state.h"
 #include "sm103_ptx.h"
 
@@ -275,6 +276,9 @@ struct Work {
     // grouped form
     OrthoPair t, q[2];
     float *dq;
+    // the kernels for a small side, in the same place
+    float *inv, *small_parts, *small_u;
+    __half *small_q;
     int64_t x_elems, m_elems;  // per matrix
     int64_t bytes;
 };
@@ -318,6 +322,14 @@ Work layout(const Shape &s, char *base)
                                                                                : 4 * (int64_t)s.batch * s.rows * s.cols);
     w.u = (float *)w.x_hi[1];
     w.bytes = off;
+    if (s.m <= kSmallSide) {  // status and counters, then the other kernels' arrays
+        off = (int64_t)align_up(4 * (1 + kMaxPhases));
+        w.inv = (float *)take(4 * (int64_t)s.batch);
+        w.small_parts = (float *)take(small_parts_bytes(s.batch));
+        w.small_q = (__half *)take(small_q_bytes(s.batch));
+        w.small_u = (float *)take(4 * (int64_t)s.batch * s.rows * s.cols);
+        w.bytes = off > w.bytes ? off : w.bytes;
+    }
     return w;
 }
 
@@ -330,6 +342,7 @@ struct Schedule {
     float a[kMaxSteps], b[kMaxSteps], c[kMaxSteps];
     float sx[kMaxSteps];  // scale of X entering step k
     float sg[kMaxSteps];  // scale of the m x m operands of step k
+    double norm[kMaxSteps], r_max[kMaxSteps], t_max[kMaxSteps];  // bounds of |X|, |R| and |R G|
 };
 
 float pow2_floor(double x) { return (float)std::exp2(std::floor(std::log2(x))); }
@@ -352,13 +365,17 @@ slide_status schedule_of(const slide_ortho_params *p, int m, Schedule *out)
             if (!std::isfinite(t[e]))
                 return fail(SLIDE_ERR_INVALID_ARG, "ortho params: non-finite coefficient");
         const double a = out->a[k] = t[0], b = out->b[k] = t[1], c = out->c[k] = t[2];
-        double next = 0.0, big = norm * norm, r_max = std::fabs(a);
+        double next = 0.0, big = norm * norm, r_max = std::fabs(a), t_max = 0.0;
         for (int i = 1; i <= 1024; ++i) {  // the polynomials on [0, norm]
             const double x = norm * i / 1024.0, x2 = x * x, r = a + b * x2 + c * x2 * x2;
             next = std::fmax(next, std::fabs(x * r));
             big = std::fmax(big, std::fmax(std::fabs(r - a), std::fabs(x2 * r)));
             r_max = std::fmax(r_max, std::fabs(r));
+            t_max = std::fmax(t_max, std::fabs(x2 * r));
         }
+        out->norm[k] = norm;
+        out->r_max[k] = r_max;
+        out->t_max[k] = t_max;
         next *= 1.01;
         q = (k % kGroupSteps == 0 ? 1.0 : q) * r_max;
         if (!(next <= 64.0) || !(q <= 16384.0) || !(big <= 16384.0))
@@ -572,6 +589,61 @@ cudaError_t launch_behind(Kernel k, dim3 grid, const Args &a, cudaStream_t strea
     return cudaLaunchKernelEx(&cfg, k, a);
 }
 
+// The kernels for a small side of at most 128, which run all steps on the Gram
+// matrix; more than kSmallMaxSteps steps would let its rounding errors grow
+// (times a^2 a step in directions that X does not have).
+bool is_small(const Shape &s, const Schedule &sc) { return s.m <= kSmallSide && sc.steps <= kSmallMaxSteps; }
+
+cudaError_t enqueue_small(const Shape &s, const Work &w, const Schedule &sc, const SourceArgs &a, const Finish &f,
+                          bool fp32, bool muon, float eps, int device, cudaStream_t stream)
+{
+    SmallOrtho o{};
+    o.g = a.g;
+    o.R = a.R;
+    o.row_stride = a.row_stride;
+    o.batch_stride = a.batch_stride;
+    o.batch = s.batch;
+    o.rows = s.rows;
+    o.cols = s.cols;
+    o.m = s.m;
+    o.tall = s.tall;
+    o.fp32 = fp32;
+    o.muon = muon;
+    o.vec = a.vec;
+    o.mom = a.mom;
+    o.u = w.small_u;
+    o.mu = a.mu;
+    o.one_minus_mu = a.one_minus_mu;
+    o.nesterov = a.nesterov;
+    o.steps = sc.steps;
+    double q = 1.0;
+    const auto scale = [](double bound) { return pow2_floor(16384.0 / std::fmax(bound, 1.0)); };
+    for (int k = 0; k < sc.steps; ++k) {
+        o.a[k] = sc.a[k];
+        o.b[k] = sc.b[k];
+        o.c[k] = sc.c[k];
+        o.s_g[k] = scale(sc.norm[k] * sc.norm[k]);
+        o.s_r[k] = scale(sc.r_max[k]);
+        o.s_t[k] = scale(sc.t_max[k]);
+        o.s_q[k] = scale(q *= sc.r_max[k]);
+    }
+    o.eps = eps;
+    o.parts = w.small_parts;
+    o.q = w.small_q;
+    o.inv = w.inv;
+    o.status = w.status;
+    o.w = f.w;
+    o.w_row = f.w_row;
+    o.w_batch = f.w_batch;
+    o.theta = f.theta;
+    o.decay = f.decay;
+    o.step = f.step;
+    o.w_vec = muon ? s.cols % 4 == 0
+                   : (uintptr_t)f.w % 8 == 0 && f.w_row % 4 == 0 && (s.batch == 1 || f.w_batch % 4 == 0);
+    o.test_stall = test_stall();
+    return launch_ortho_small(o, device, stream);
+}
+
 // The norms (and a Muon step's update), then the normalised operands.
 cudaError_t enqueue_source(const Shape &s, const Work &w, const Schedule &sc, SourceArgs a, bool fp32, bool muon,
                            float eps, cudaStream_t stream)
@@ -621,6 +693,15 @@ cudaError_t enqueue_source(const Shape &s, const Work &w, const Schedule &sc, So
     const dim3 grid2((unsigned)(blocks < per ? blocks : per), s.batch);
     return muon || fp32 ? launch_behind(k_ortho_scale<float>, grid2, c, stream)
                         : launch_behind(k_ortho_scale<uint16_t>, grid2, c, stream);
+}
+
+cudaError_t enqueue(const Shape &s, const Work &w, const Schedule &sc, const SourceArgs &a, const Finish &f, bool fp32,
+                    bool muon, float eps, int device, cudaStream_t stream)
+{
+    if (is_small(s, sc))
+        return enqueue_small(s, w, sc, a, f, fp32, muon, eps, device, stream);
+    const cudaError_t e = enqueue_source(s, w, sc, a, fp32, muon, eps, stream);
+    return e == cudaSuccess ? enqueue_products(s, w, sc, f, device, stream) : e;
 }
 
 slide_status check_shape(int32_t batch, int32_t rows, int32_t cols)
@@ -726,17 +807,14 @@ extern "C" slide_status slide_orthogonalize(int32_t batch, int32_t rows, int32_t
     a.batch_stride = x_batch_stride;
     const int64_t per16 = x_type == SLIDE_TYPE_FP32 ? 4 : 8;  // elements of 16 bytes
     a.vec = !misaligned(x, 16) && x_row_stride % per16 == 0 && (batch == 1 || x_batch_stride % per16 == 0);
-    e = enqueue_source(s, w, sc, a, x_type == SLIDE_TYPE_FP32, false, params->eps, (cudaStream_t)stream);
-    if (e != cudaSuccess)
-        return fail_cuda(e, "orthogonalisation: preparation launch");
     Finish f{};
     f.epi = kEpiOut;
     f.w = (uint16_t *)bf16_out;
     f.w_row = out_row_stride;
     f.w_batch = out_batch_stride;
-    e = enqueue_products(s, w, sc, f, device, (cudaStream_t)stream);
+    e = enqueue(s, w, sc, a, f, x_type == SLIDE_TYPE_FP32, false, params->eps, device, (cudaStream_t)stream);
     if (e != cudaSuccess)
-        return fail_cuda(e, "orthogonalisation: product launch");
+        return fail_cuda(e, "orthogonalisation launch");
     clear_error();
     return SLIDE_OK;
 }
@@ -790,9 +868,6 @@ extern "C" slide_status slide_muon_step(int32_t batch, int32_t rows, int32_t col
     a.one_minus_mu = (float)(1.0 - (double)hp->momentum);
     a.nesterov = hp->nesterov != 0;
     a.vec = cols % (grads_type == SLIDE_TYPE_FP32 ? 4 : 8) == 0;
-    e = enqueue_source(s, w, sc, a, grads_type == SLIDE_TYPE_FP32, true, hp->ortho.eps, (cudaStream_t)stream);
-    if (e != cudaSuccess)
-        return fail_cuda(e, "muon step: preparation launch");
     Finish f{};
     f.epi = kEpiMuon;
     f.w = (uint16_t *)bf16_out;
@@ -800,9 +875,9 @@ extern "C" slide_status slide_muon_step(int32_t batch, int32_t rows, int32_t col
     f.decay = (float)(1.0 - (double)hp->lr * (double)hp->weight_decay);
     const double scale = hp->scale > 0.0f ? (double)hp->scale : 0.2 * std::sqrt((double)(rows > cols ? rows : cols));
     f.step = (float)((double)hp->lr * scale);
-    e = enqueue_products(s, w, sc, f, device, (cudaStream_t)stream);
+    e = enqueue(s, w, sc, a, f, grads_type == SLIDE_TYPE_FP32, true, hp->ortho.eps, device, (cudaStream_t)stream);
     if (e != cudaSuccess)
-        return fail_cuda(e, "muon step: product launch");
+        return fail_cuda(e, "muon step launch");
     clear_error();
     return SLIDE_OK;
 }

@@ -1,0 +1,802 @@
+// ortho_small.cu — the Newton-Schulz polynomial for matrices whose smaller side
+// m is at most 128: the iteration runs on the m x m Gram matrix inside one
+// CTA, and the matrix itself is read twice and written once.
+//
+//   1. k_small_gram: raw = X X^T (X^T X if tall), each CTA a stretch of the
+//      long side, eight of them (a cluster) added up through distributed
+//      shared memory; a Muon step's update is formed on the way.  FP32 values
+//      enter as pairs of BF16, which need no scale, so no norm has to be known
+//      before: |X|_F^2 is the trace of the result.
+//   2. k_small_poly: one CTA per matrix: G = raw / (|X|_F + eps)^2, then per
+//      step R = aI + bG + cG^2, G <- R G R, Q <- R Q.
+//   3. k_small_apply: out = Q X / (|X|_F + eps).
+//
+// Operands of 2 and 3 are FP16 pairs (hi + lo, 22 bits), each product three
+// tensor-core products (hi*hi + hi*lo + lo*hi) into one FP32 accumulator, so
+// all steps can run on G without going back to X.  For a 64 x 2560 matrix the
+// products themselves take a fifth of the time: what counts is the number of
+// dependent steps, about 1 us each inside a CTA, where a product that goes
+// through global memory and a barrier of all CTAs takes 4.5 us.
+#include <cuda_bf16.h>
+
+#include <atomic>
+
+#include "slide_ortho_small.h"
+#include "sm103_ptx.h"
+
+namespace slide {
+namespace {
+
+using namespace ptx;
+
+constexpr int kThreads = 256;
+constexpr int kCluster = 8;
+constexpr unsigned kStatusWaitLimit = 2u;
+constexpr int kTile = 16384;           // 128 rows x 64 columns of 16-bit values
+constexpr int kGramStages = 3;
+constexpr float kApplyScale = 1024.0f; // of X / |X| in k_small_apply: entries are at most 1
+
+__device__ __forceinline__ uint32_t idesc_of(uint32_t n, bool a_mn, bool b_mn, bool bf16)
+{
+    return f16_idesc(128, n, a_mn, b_mn) | (bf16 ? (1u << 7) | (1u << 10) : 0u);
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float widen(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+__device__ __forceinline__ float widen(float x) { return x; }
+
+// Values at .. at+7 of a row, of which n lie inside it (zero beyond).
+template <typename T>
+__device__ __forceinline__ void load8(const void *base, int64_t at, int n, bool vec, float (&v)[8])
+{
+    const T *p = static_cast<const T *>(base) + at;
+    if (vec && n >= 8) {
+        if constexpr (sizeof(T) == 2) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(p);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[2 * e] = __uint_as_float(u[e] << 16);
+                v[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+            }
+        } else {
+            const float4 w = *reinterpret_cast<const float4 *>(p), x = *reinterpret_cast<const float4 *>(p + 4);
+            v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w, v[4] = x.x, v[5] = x.y, v[6] = x.z, v[7] = x.w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = e < n ? widen(p[e]) : 0.0f;
+    }
+}
+
+__device__ __forceinline__ void store8(float *p, int n, bool vec, const float (&v)[8])
+{
+    if (vec && n >= 8) {
+        reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n)
+                p[e] = v[e];
+    }
+}
+
+// Eight values as a 16-byte chunk of FP16 (or BF16) and the chunk of what the
+// rounding left.
+template <bool BF>
+__device__ __forceinline__ void split8(const float (&v)[8], uint4 &hi, uint4 &lo)
+{
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float x = v[2 * e], y = v[2 * e + 1];
+        if constexpr (BF) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(x, y);
+            const float2 f = __bfloat1622float2(p);
+            const __nv_bfloat162 q = __floats2bfloat162_rn(x - f.x, y - f.y);
+            h[e] = *reinterpret_cast<const uint32_t *>(&p);
+            l[e] = *reinterpret_cast<const uint32_t *>(&q);
+        } else {
+            const __half2 p = __floats2half2_rn(x, y);
+            const float2 f = __half22float2(p);
+            const __half2 q = __floats2half2_rn(x - f.x, y - f.y);
+            h[e] = *reinterpret_cast<const uint32_t *>(&p);
+            l[e] = *reinterpret_cast<const uint32_t *>(&q);
+        }
+    }
+    hi = make_uint4(h[0], h[1], h[2], h[3]);
+    lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// Set-up shared by the three kernels: mbarriers, tensor memory of `cols` columns.
+struct Base {
+    uint64_t bar[kGramStages + 1];
+    uint32_t tmem;
+    volatile int abort;
+};
+
+__device__ __forceinline__ uint32_t set_up(Base &b, uint32_t cols)
+{
+    if (threadIdx.x == 0) {
+        for (int i = 0; i <= kGramStages; ++i)
+            mbar_init(smem_addr(&b.bar[i]), 1);
+        b.abort = 0;
+        fence_async_shared();
+    }
+    if (threadIdx.x < 32)
+        tmem_alloc<1>(smem_addr(&b.tmem), cols);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    return b.tmem;
+}
+
+// Wait for a barrier that tensor-core products arrive on; on a wait that runs
+// out the call is marked.
+__device__ __forceinline__ void wait_products(Base &b, int i, uint32_t parity, unsigned *status)
+{
+    if (!mbar_wait(smem_addr(&b.bar[i]), parity, &b.abort)) {
+        b.abort = 1;
+        atomicOr(status, kStatusWaitLimit);
+    }
+    tmem_fence_after();
+}
+
+// ---- 1: the Gram matrix ---------------------------------------------------------
+
+// Chunk (row, eight columns) of the matrix; a Muon step forms the update there
+// and writes it and the momentum.
+template <typename T, bool MUON>
+__device__ __forceinline__ void load_chunk(const SmallOrtho &a, int b, int row, int col, float (&v)[8])
+{
+    const int n = a.cols - col;
+    if (row >= a.rows || n <= 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = 0.0f;
+        return;
+    }
+    const int64_t at = (int64_t)b * a.batch_stride + (int64_t)row * a.row_stride + col;
+    load8<T>(a.g.p[0], at, n, a.vec, v);
+    if constexpr (MUON) {
+        float m[8];
+        load8<float>(a.mom, at, n, a.vec, m);
+        for (int k = 1; k < a.R; ++k) {
+            float w[8];
+            load8<T>(a.g.p[k], at, n, a.vec, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = __fadd_rn(v[e], w[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float g = __fmul_rn(a.one_minus_mu, __fdiv_rn(v[e], (float)a.R));
+            m[e] = __fadd_rn(__fmul_rn(m[e], a.mu), g);
+            v[e] = a.nesterov ? __fadd_rn(__fmul_rn(m[e], a.mu), g) : m[e];
+        }
+        store8(a.mom + at, n, a.vec, m);
+        store8(a.u + at, n, a.vec, v);
+    }
+}
+
+// Grid: (8 * n_parts, batch), clusters of 8 along x.  A step takes 64 of the
+// long side.  PAIR: the values need a second BF16.
+template <typename T, bool MUON>
+__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
+    k_small_gram(const __grid_constant__ SmallOrtho a)
+{
+    constexpr bool kPair = sizeof(T) == 4 || MUON;
+    constexpr int kStage = (kPair ? 2 : 1) * kTile;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Base sh;
+    const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const uint32_t tmem = set_up(sh, 128);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.y;
+    launch_dependents();
+    if (blockIdx.x == 0 && b == 0 && tid == 0)
+        *a.status = 0;
+    const int n_side = a.tall ? a.rows : a.cols;
+    const int steps = (n_side + 63) / 64, per = (steps + gridDim.x - 1) / gridDim.x;
+    const int k0 = min(steps, (int)blockIdx.x * per), k1 = min(steps, k0 + per);
+    const uint32_t n16 = (uint32_t)((a.m + 15) & ~15);
+    const uint32_t idesc = idesc_of(n16, a.tall, a.tall, true);
+    const int mchunks = (a.m + 7) / 8;  // chunks along the short side (tall)
+
+    for (int k = k0; k < k1; ++k) {
+        const int it = k - k0, s = it % kGramStages;
+        // chunk i of the step: wide: row i >> 3, columns 8*(i & 7); tall: row i >> 4, columns 8*(i & 15)
+        float v[4][8];
+        int place[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = tid + j * kThreads;
+            if (a.tall) {
+                const int r = i >> 4, c = i & 15;
+                place[j] = c < ((mchunks + 7) & ~7) ? (c >> 3) * (kTile / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4) : -1;
+                if (place[j] >= 0)
+                    load_chunk<T, MUON>(a, b, k * 64 + r, c * 8, v[j]);
+            } else {
+                const int r = i >> 3, c = i & 7;
+                place[j] = r * 128 + ((c ^ (r & 7)) << 4);
+                load_chunk<T, MUON>(a, b, r, k * 64 + c * 8, v[j]);
+            }
+        }
+        if (it >= kGramStages)
+            wait_products(sh, s, (it / kGramStages - 1) & 1, a.status);
+        const uint32_t stage = ring + s * kStage;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (place[j] < 0)
+                continue;
+            uint4 hi, lo;
+            split8<true>(v[j], hi, lo);
+            sts128(stage + place[j], hi);
+            if constexpr (kPair)
+                sts128(stage + kTile + place[j], lo);
+        }
+        fence_async_shared();
+        __syncthreads();
+        if (warp == 0 && elect_one() && !a.test_stall) {
+            const uint32_t step = a.tall ? 2048u : 32u;
+#pragma unroll
+            for (int term = 0; term < (kPair ? 3 : 1); ++term) {
+                const uint64_t da = operand_desc(stage + (term == 2 ? kTile : 0), kTile / 2);
+                const uint64_t db = operand_desc(stage + (term == 1 ? kTile : 0), kTile / 2);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    mma_f16<1>(tmem, da + j * (step >> 4), db + j * (step >> 4), idesc, it > 0 || term > 0 || j > 0);
+            }
+            mma_commit<1>(smem_addr(&sh.bar[s]));
+        }
+        __syncwarp();
+    }
+    // the last products of each stage
+    for (int it = max(0, k1 - k0 - kGramStages); it < k1 - k0; ++it)
+        wait_products(sh, it % kGramStages, (it / kGramStages) & 1, a.status);
+    __syncthreads();
+
+    // The cluster's sum: each CTA puts its part into shared memory (chunk c of
+    // row r at c ^ (r & 31)), then adds up 16 rows of all of them.
+    const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
+    if (half * 64 < (int)n16) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t acc[32];
+            if (k1 > k0) {
+                tmem_load32(tmem + ((uint32_t)(quad * 32) << 16) + half * 64 + h * 32, acc);
+                tmem_wait_load();
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const int c = half * 16 + h * 8 + q;
+                const bool in = k1 > k0 && 4 * c < (int)n16;
+                sts128(ring + row * 512 + ((c ^ (row & 31)) << 4),
+                       in ? make_uint4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]) : make_uint4(0, 0, 0, 0));
+            }
+        }
+    }
+    tmem_fence_before();
+    cluster_sync();
+    const int part = blockIdx.x / kCluster;
+    const uint32_t rank = cluster_rank();
+    float4 *out = reinterpret_cast<float4 *>(a.parts) + ((int64_t)b * a.n_parts + part) * 4096;
+    for (int i = tid; i < 16 * 32; i += kThreads) {
+        const int r = rank * 16 + (i & 15), c = i >> 4;
+        if (r >= a.m || 4 * c >= (int)n16)
+            continue;
+        const uint32_t at = ring + r * 512 + ((c ^ (r & 31)) << 4);
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (uint32_t p = 0; p < kCluster; ++p) {
+            float4 x;
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                         : "r"(map_to_rank(at, p))
+                         : "memory");
+            sum.x += x.x;
+            sum.y += x.y;
+            sum.z += x.z;
+            sum.w += x.w;
+        }
+        out[c * 128 + r] = sum;  // chunk after chunk, so that a thread per row reads along the rows
+    }
+    cluster_sync();
+    tmem_fence_after();
+    if (warp == 0)
+        tmem_free<1>(tmem, 128);
+}
+
+// ---- 2: the polynomial ------------------------------------------------------------
+
+// acc (+)= A * B over three terms of pairs (hi, lo 32 KiB apart), all K-major
+// tiles of 128 x 64 (the factors are symmetric).
+__device__ __forceinline__ void issue_pair(uint32_t tmem, uint32_t a, uint32_t b, uint32_t k16, uint32_t idesc)
+{
+#pragma unroll
+    for (int term = 0; term < 3; ++term) {
+        const uint64_t da = operand_desc(a + (term == 2 ? 2 * kTile : 0), 16);
+        const uint64_t db = operand_desc(b + (term == 1 ? 2 * kTile : 0), 16);
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) {
+            constexpr uint32_t kStep = 32;
+            const uint32_t off = ((j >> 2) * kTile + (j & 3) * kStep) >> 4;
+            if (j < k16)
+                mma_f16<1>(tmem, da + off, db + off, idesc, term > 0 || j > 0);
+        }
+    }
+}
+
+// Row `row`, columns 32*block.. of a pair, from 32 values.
+__device__ __forceinline__ void put_pair(uint32_t m, int row, int block, const float (&v)[32])
+{
+    const uint32_t tile = m + (block >> 1) * kTile + row * 128;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const float x[8] = {v[8 * q], v[8 * q + 1], v[8 * q + 2], v[8 * q + 3],
+                            v[8 * q + 4], v[8 * q + 5], v[8 * q + 6], v[8 * q + 7]};
+        uint4 hi, lo;
+        split8<false>(x, hi, lo);
+        const uint32_t at = tile + (((4 * (block & 1) + q) ^ (row & 7)) << 4);
+        sts128(at, hi);
+        sts128(at + 2 * kTile, lo);
+    }
+}
+
+__device__ __forceinline__ void get_pair(uint32_t m, int row, int block, float (&v)[32])
+{
+    const uint32_t tile = m + (block >> 1) * kTile + row * 128;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t at = tile + (((4 * (block & 1) + q) ^ (row & 7)) << 4);
+        const uint4 hi = lds128(at), lo = lds128(at + 2 * kTile);
+        const uint32_t u[4] = {hi.x, hi.y, hi.z, hi.w}, w[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u[e]));
+            const float2 l = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
+            v[8 * q + 2 * e] = f.x + l.x;
+            v[8 * q + 2 * e + 1] = f.y + l.y;
+        }
+    }
+}
+
+constexpr int kPairBytes = 4 * kTile;                 // hi and lo of a 128 x 128 matrix
+constexpr int kPolySmem = 1024 + 3 * kPairBytes;
+
+// 128 threads per 32 columns.  Warp (quad, block) has rows 32*quad.. and columns
+// 32*block.. of every matrix; warps whose rows all lie beyond m rest.  Rows and columns beyond m
+// inside a used block are zero, those of unused blocks hold anything: they only
+// meet rows of results that nobody reads.
+__global__ void __launch_bounds__(512) k_small_poly(const __grid_constant__ SmallOrtho a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Base sh;
+    __shared__ double s_trace[4];
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const uint32_t G = base, R = base + kPairBytes, Q = base + 2 * kPairBytes;
+    const uint32_t tmem = set_up(sh, 256);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.x;
+    const int quad = warp & 3, block = warp >> 2, row = quad * 32 + lane;
+    const uint32_t n16 = (uint32_t)((a.m + 15) & ~15), k16 = n16 / 16, idesc = idesc_of(n16, false, false, false);
+    const uint32_t acc_at = tmem + ((uint32_t)(quad * 32) << 16) + block * 32;
+    const bool mine = quad * 32 < a.m;
+    const bool diag = mine && quad == block;  // the lane's diagonal element is its number `lane`
+    launch_dependents();
+    wait_for_previous_grid();
+    if (tid == 0 && (*(volatile unsigned *)a.status & kStatusWaitLimit))
+        sh.abort = 1;  // the launch before gave up: no waits of the full length
+
+    // the raw Gram matrix, zero beyond m; its trace is |X|_F^2
+    float v[32];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        const int chunk = block * 8 + c;
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (row < a.m && 4 * chunk < (int)n16) {
+            const float4 *p = reinterpret_cast<const float4 *>(a.parts) + (int64_t)b * a.n_parts * 4096 + chunk * 128 + row;
+            for (int k = 0; k < a.n_parts; ++k) {
+                const float4 x = p[(int64_t)k * 4096];
+                sum.x += x.x;
+                sum.y += x.y;
+                sum.z += x.z;
+                sum.w += x.w;
+            }
+        }
+        v[4 * c] = sum.x, v[4 * c + 1] = sum.y, v[4 * c + 2] = sum.z, v[4 * c + 3] = sum.w;
+    }
+    if (diag) {
+        double trace = 0.0;
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (e == lane)
+                trace = v[e];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            trace += __shfl_xor_sync(0xffffffffu, trace, o);
+        if (lane == 0)
+            s_trace[quad] = trace;
+    }
+    __syncthreads();
+    double trace = 0.0;
+    for (int i = 0; i < (int)blockDim.x / 128; ++i)
+        trace += s_trace[i];
+    // a matrix of zeros stays one, whatever eps
+    const float inv = trace == 0.0 && a.eps == 0.0f ? 0.0f : (float)(1.0 / (sqrt(trace) + (double)a.eps));
+    if (tid == 0)
+        a.inv[b] = inv;
+    if (mine) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            v[e] = v[e] * inv * (inv * a.s_g[0]);
+        put_pair(G, row, block, v);
+    }
+    fence_async_shared();
+    __syncthreads();
+
+    uint32_t phase = 0;
+    // one product (or two), waited for by every thread
+    auto products = [&](uint32_t a0, uint32_t b0, uint32_t a1, uint32_t b1) {
+        if (warp == 0 && !a.test_stall) {
+            tmem_fence_after();
+            if (elect_one()) {
+                issue_pair(tmem, a0, b0, k16, idesc);
+                if (a1)
+                    issue_pair(tmem + 128, a1, b1, k16, idesc);
+                mma_commit<1>(smem_addr(&sh.bar[0]));
+            }
+            __syncwarp();
+        }
+        wait_products(sh, 0, phase & 1, a.status);
+        ++phase;
+    };
+    // this thread's values of an accumulator, times f, into a pair
+    auto keep = [&](uint32_t acc, float f, uint32_t to) {
+        if (!mine)
+            return;
+        uint32_t x[32];
+        tmem_load32(acc, x);
+        tmem_wait_load();
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            v[e] = __uint_as_float(x[e]) * f;
+        put_pair(to, row, block, v);
+    };
+    auto settle = [&] {
+        tmem_fence_before();
+        fence_async_shared();
+        __syncthreads();
+    };
+
+    for (int k = 0; k < a.steps && !sh.abort; ++k) {
+        const float sg = a.s_g[k], sr = a.s_r[k];
+        const bool more = k + 1 < a.steps;
+        products(G, G, 0, 0);
+        if (mine) {  // R = aI + bG + cG^2; the first R is also Q
+            const float cc = a.c[k] / (sg * sg) * sr, bb = a.b[k] / sg * sr;
+            uint32_t x[32];
+            tmem_load32(acc_at, x);
+            get_pair(G, row, block, v);
+            tmem_wait_load();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                v[e] = fmaf(cc, __uint_as_float(x[e]), bb * v[e]);
+            if (diag && row < a.m) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (e == lane)
+                        v[e] = fmaf(a.a[k], sr, v[e]);
+            }
+            put_pair(R, row, block, v);
+            if (k == 0) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    v[e] *= a.s_q[0] / sr;
+                put_pair(Q, row, block, v);
+            }
+        }
+        settle();
+        // T = R G and Q <- R Q
+        if (more || k > 0) {
+            if (more && k > 0)
+                products(R, G, R, Q);
+            else if (more)
+                products(R, G, 0, 0);
+            else
+                products(R, Q, 0, 0);
+            if (more)
+                keep(acc_at, a.s_t[k] / (sr * sg), G);
+            if (k > 0)
+                keep(acc_at + (more ? 128 : 0), a.s_q[k] / (sr * a.s_q[k - 1]), Q);
+            settle();
+        }
+        if (more) {  // G <- R T
+            products(R, G, 0, 0);
+            keep(acc_at, a.s_g[k + 1] / (sr * a.s_t[k]), G);
+            settle();
+        }
+    }
+    // Q, as it lies: rows beyond m are not read, columns beyond m of a used tile are zero or meet zeros
+    uint4 *out = reinterpret_cast<uint4 *>(a.q) + (int64_t)b * (kPairBytes / 16);
+    for (int i = tid; i < kPairBytes / 16; i += blockDim.x)
+        if ((i & 1023) < (int)n16 * 8)
+            out[i] = lds128(Q + i * 16);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == 0)
+        tmem_free<1>(tmem, 256);
+}
+
+// ---- 3: the result ------------------------------------------------------------------
+
+// A CTA takes stretches of 128 of the long side in turn.  Shared memory: Q
+// (pair), X (pair), both only as many 64-column tiles (Q) and rows or tiles (X)
+// as m needs; the result goes through X's place as FP32.
+template <typename T, bool MUON>
+__global__ void __launch_bounds__(kThreads) k_small_apply(const __grid_constant__ SmallOrtho a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Base sh;
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const uint32_t tmem = set_up(sh, 128);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.y;
+    const uint32_t n16 = (uint32_t)((a.m + 15) & ~15), k16 = n16 / 16;
+    const int tiles = n16 > 64 ? 2 : 1;        // 64-column tiles along the short side
+    const uint32_t q_lo = tiles * kTile;       // Q: tiles of hi, then tiles of lo
+    // X: tall: 128 rows x m, tiles along m; wide: m rows x 128, two tiles of 64*tiles rows
+    const uint32_t X = base + 2 * q_lo, x_lo = tiles * kTile, x_tile = a.tall ? kTile : tiles * (kTile / 2);
+    const uint32_t idesc = a.tall ? idesc_of(n16, false, false, false) : idesc_of(128, false, true, false);
+    const int quad = warp & 3, half = warp >> 2;
+    launch_dependents();
+    wait_for_previous_grid();
+    if (tid == 0 && (*(volatile unsigned *)a.status & kStatusWaitLimit))
+        sh.abort = 1;
+    __syncthreads();
+    const float inv = a.inv[b] * kApplyScale;
+    const float back = 1.0f / (a.s_q[a.steps - 1] * kApplyScale);
+    {
+        const uint4 *q = reinterpret_cast<const uint4 *>(a.q) + (int64_t)b * (kPairBytes / 16);
+        for (int i = tid; i < tiles * (kTile / 16); i += kThreads) {
+            sts128(base + i * 16, q[i]);
+            sts128(base + q_lo + i * 16, q[2 * (kTile / 16) + i]);
+        }
+    }
+    const int n_side = a.tall ? a.rows : a.cols;
+    uint32_t phase = 0;
+    for (int s0 = blockIdx.x * 128; s0 < n_side && !sh.abort; s0 += gridDim.x * 128, ++phase) {
+        // tall: 128 rows of 8*tiles chunks; wide: 64*tiles rows of 16 chunks
+        for (int i = tid; i < tiles * 1024; i += kThreads) {
+            float v[8];
+            uint32_t place;
+            int row, col;
+            if (a.tall) {
+                const int r = tiles == 2 ? i >> 4 : i >> 3, c = i & (8 * tiles - 1);
+                row = s0 + r;
+                col = c * 8;
+                place = (c >> 3) * kTile + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+            } else {
+                const int r = i >> 4, c = i & 15;
+                row = r;
+                col = s0 + c * 8;
+                place = (c >> 3) * x_tile + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+            }
+            const int n = a.cols - col;
+            if (row < a.rows && n > 0) {
+                const int64_t at = (int64_t)b * a.batch_stride + (int64_t)row * a.row_stride + col;
+                if constexpr (MUON)
+                    load8<float>(a.u, at, n, a.vec, v);
+                else
+                    load8<T>(a.g.p[0], at, n, a.vec, v);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = 0.0f;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] *= inv;
+            uint4 hi, lo;
+            split8<false>(v, hi, lo);
+            sts128(X + place, hi);
+            sts128(X + x_lo + place, lo);
+        }
+        fence_async_shared();
+        __syncthreads();
+        if (warp == 0 && elect_one() && !a.test_stall) {
+            tmem_fence_after();
+            for (int term = 0; term < 3; ++term) {
+                const uint32_t q = base + (term == 1 ? q_lo : 0), x = X + (term == 2 ? x_lo : 0);
+                const uint64_t dq = operand_desc(q, 16), dx = operand_desc(x, x_tile);
+                for (uint32_t j = 0; j < k16; ++j) {
+                    const uint32_t kq = ((j >> 2) * kTile + (j & 3) * 32) >> 4;
+                    if (a.tall)
+                        mma_f16<1>(tmem, dx + kq, dq + kq, idesc, term > 0 || j > 0);
+                    else
+                        mma_f16<1>(tmem, dq + kq, dx + ((j * 2048) >> 4), idesc, term > 0 || j > 0);
+                }
+            }
+            mma_commit<1>(smem_addr(&sh.bar[0]));
+        }
+        __syncwarp();
+        wait_products(sh, 0, phase & 1, a.status);
+        // rows x cols of the result: tall 128 x m, wide m x 128; FP32 in X's
+        // place, chunk c of row r at c ^ (r & (chunks of a row - 1))
+        const int d_cols = a.tall ? 64 * tiles : 128, d_rows = a.tall ? 128 : 64 * tiles, chunks = d_cols / 4;
+        const int row = quad * 32 + lane;
+        if (row < d_rows && half * 64 < d_cols) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t x[32];
+                tmem_load32(tmem + ((uint32_t)(quad * 32) << 16) + half * 64 + h * 32, x);
+                tmem_wait_load();
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int c = half * 16 + h * 8 + q;
+                    sts128(X + row * d_cols * 4 + ((c ^ (row & (chunks - 1) & 31)) << 4),
+                           make_uint4(__float_as_uint(__uint_as_float(x[4 * q]) * back),
+                                      __float_as_uint(__uint_as_float(x[4 * q + 1]) * back),
+                                      __float_as_uint(__uint_as_float(x[4 * q + 2]) * back),
+                                      __float_as_uint(__uint_as_float(x[4 * q + 3]) * back)));
+                }
+            }
+        }
+        tmem_fence_before();
+        __syncthreads();
+        const int top = a.tall ? s0 : 0, left = a.tall ? 0 : s0;
+        const int r_end = min(d_rows, a.rows - top), c_end = min(d_cols, a.cols - left);
+        // four columns of a row at a time: 16 or 32 threads per row
+        const int per_row = d_cols / 4, at_once = kThreads / per_row;
+        const int c = (tid % per_row) * 4;
+        constexpr int kAhead = 4;
+        for (int r0 = tid / per_row; r0 < r_end; r0 += at_once * kAhead) {
+            float th[kAhead][4];
+            if constexpr (MUON) {
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    const int r = r0 + j * at_once;
+                    if (r < r_end && c < c_end) {
+                        const float *p = a.theta + ((int64_t)b * a.rows + top + r) * a.cols + left + c;
+                        if (a.w_vec && c + 4 <= c_end) {
+                            const float4 w = *reinterpret_cast<const float4 *>(p);
+                            th[j][0] = w.x, th[j][1] = w.y, th[j][2] = w.z, th[j][3] = w.w;
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                th[j][e] = c + e < c_end ? p[e] : 0.0f;
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int r = r0 + j * at_once;
+                if (r >= r_end || c >= c_end)
+                    continue;
+                const uint4 u = lds128(X + r * d_cols * 4 + (((c / 4) ^ (r & (chunks - 1) & 31)) << 4));
+                float o[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
+                int64_t at;
+                if constexpr (MUON) {
+                    at = ((int64_t)b * a.rows + top + r) * a.cols + left + c;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[e] = __fsub_rn(__fmul_rn(th[j][e], a.decay), __fmul_rn(a.step, o[e]));
+                } else {
+                    at = (int64_t)b * a.w_batch + (int64_t)(top + r) * a.w_row + left + c;
+                }
+                uint16_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = __bfloat16_as_ushort(__float2bfloat16_rn(o[e]));
+                if (a.w_vec && c + 4 <= c_end) {
+                    if constexpr (MUON)
+                        *reinterpret_cast<float4 *>(a.theta + at) = make_float4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint2 *>(a.w + at) =
+                        make_uint2((uint32_t)w[0] | (uint32_t)w[1] << 16, (uint32_t)w[2] | (uint32_t)w[3] << 16);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (c + e < c_end) {
+                            if constexpr (MUON)
+                                a.theta[at + e] = o[e];
+                            a.w[at + e] = w[e];
+                        }
+                    }
+                }
+            }
+        }
+        fence_async_shared();
+        __syncthreads();  // the next stretch takes X's place
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == 0)
+        tmem_free<1>(tmem, 128);
+}
+
+constexpr int kMaxDevices = 64;
+
+template <typename Kernel>
+cudaError_t launch_kernel(Kernel k, dim3 grid, int threads, int smem, bool behind, const SmallOrtho &a, cudaStream_t stream,
+                          std::atomic<int> &ready)
+{
+    if (!ready.load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kPolySmem);
+        if (e != cudaSuccess)
+            return e;
+        ready.store(1, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = behind ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k, a);
+}
+
+template <typename T, bool MUON>
+cudaError_t launch_all(SmallOrtho &a, int device, int sms, cudaStream_t stream)
+{
+    static std::atomic<int> ready[kMaxDevices][3];
+    const int n_side = a.tall ? a.rows : a.cols;
+    // a cluster of eight CTAs per 8 x 4 steps of 64, while that leaves no SM idle
+    const int steps = (n_side + 63) / 64;
+    const int fit = sms / (kCluster * a.batch);
+    int parts = (steps + 4 * kCluster - 1) / (4 * kCluster);
+    parts = parts < fit ? parts : fit;
+    parts = parts < 1 ? 1 : parts > kSmallMaxParts ? kSmallMaxParts : parts;
+    a.n_parts = parts;
+    const int pair = sizeof(T) == 4 || MUON ? 2 : 1;
+    const int gram = 1024 + (kGramStages * pair * kTile > 65536 ? kGramStages * pair * kTile : 65536);
+    cudaError_t e = launch_kernel(k_small_gram<T, MUON>, dim3(kCluster * parts, a.batch), kThreads, gram, false, a, stream,
+                                  ready[device][0]);
+    if (e == cudaSuccess)
+        e = launch_kernel(k_small_poly, dim3(a.batch), (a.m + 31) / 32 * 128, kPolySmem, true, a, stream, ready[device][1]);
+    if (e != cudaSuccess)
+        return e;
+    const int tiles = a.m > 64 ? 2 : 1;
+    const int64_t stretches = (n_side + 127) / 128;
+    const int64_t room = (int64_t)sms * (tiles == 2 ? 1 : 3);
+    const int64_t per = (room + a.batch - 1) / a.batch;
+    return launch_kernel(k_small_apply<T, MUON>, dim3((unsigned)(stretches < per ? stretches : per), a.batch),
+                         kThreads, 1024 + 4 * tiles * kTile, true, a, stream, ready[device][2]);
+}
+
+}  // namespace
+
+cudaError_t launch_ortho_small(SmallOrtho a, int device, cudaStream_t stream)
+{
+    if (device < 0 || device >= kMaxDevices)
+        return cudaErrorInvalidDevice;
+    static std::atomic<int> count[kMaxDevices];
+    int sms = count[device].load(std::memory_order_acquire);
+    if (sms == 0) {
+        const cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+        if (e != cudaSuccess)
+            return e;
+        count[device].store(sms, std::memory_order_release);
+    }
+    if (a.muon)
+        return a.fp32 ? launch_all<float, true>(a, device, sms, stream) : launch_all<uint16_t, true>(a, device, sms, stream);
+    return a.fp32 ? launch_all<float, false>(a, device, sms, stream) : launch_all<uint16_t, false>(a, device, sms, stream);
+}
+
+}  // namespace slide

@@ -1,0 +1,59 @@
+// slide_ortho_small.h — internal interface of the Newton-Schulz kernels for
+// matrices with a side of at most 128 (ortho_small.cu).
+#pragma once
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "slide_kernels.h"
+
+namespace slide {
+
+constexpr int kSmallSide = 128;
+constexpr int kSmallMaxSteps = 6;
+constexpr int kSmallMaxParts = 4;  // clusters along the long side, one partial Gram matrix each
+
+struct SmallOrtho {
+    // the matrices, or the R replicas of a Muon step
+    ReplicaPtrs g;
+    int R;
+    int64_t row_stride, batch_stride;
+    int batch, rows, cols;
+    int m;                      // the smaller side
+    int tall;
+    int fp32;                   // type of the matrices or replicas
+    int muon;
+    int vec;                    // rows can be read eight values at a time
+    // Muon: contiguous
+    float *mom, *u;
+    float mu, one_minus_mu;
+    int nesterov;
+    // the polynomial: per step its coefficients and the scales (powers of two)
+    // of the FP16 pairs that hold G, R = aI + bG + cG^2, R G and the product
+    // of the R
+    int steps;
+    float a[kSmallMaxSteps], b[kSmallMaxSteps], c[kSmallMaxSteps];
+    float s_g[kSmallMaxSteps], s_r[kSmallMaxSteps], s_t[kSmallMaxSteps], s_q[kSmallMaxSteps];
+    float eps;
+    // scratch
+    float *parts;               // [batch][n_parts][128 x 128]
+    __half *q;                  // [batch][hi, lo][128 x 128], tiles as in slide_ortho.h
+    float *inv;                 // [batch]
+    unsigned *status;
+    int n_parts;                // set by the launch
+    // results
+    uint16_t *w;
+    int64_t w_row, w_batch;
+    int w_vec;
+    float *theta;
+    float decay, step;
+    int test_stall;
+};
+
+// Bytes of the scratch's three arrays for `batch` matrices.
+inline int64_t small_parts_bytes(int batch) { return (int64_t)batch * kSmallMaxParts * 128 * 128 * 4; }
+inline int64_t small_q_bytes(int batch) { return (int64_t)batch * 2 * 128 * 128 * 2; }
+
+cudaError_t launch_ortho_small(SmallOrtho s, int device, cudaStream_t stream);
+
+}  // namespace slide
