@@ -616,17 +616,23 @@ cudaError_t enqueue_small(const Shape &s, const Work &w, const Schedule &sc, con
     o.one_minus_mu = a.one_minus_mu;
     o.nesterov = a.nesterov;
     o.steps = sc.steps;
-    double q = 1.0;
-    const auto scale = [](double bound) { return pow2_floor(16384.0 / std::fmax(bound, 1.0)); };
+    const auto scale = [](double bound) { return (double)pow2_floor(16384.0 / std::fmax(bound, 1.0)); };
+    double q = 1.0, sq = 1.0;
     for (int k = 0; k < sc.steps; ++k) {
-        o.a[k] = sc.a[k];
-        o.b[k] = sc.b[k];
-        o.c[k] = sc.c[k];
-        o.s_g[k] = scale(sc.norm[k] * sc.norm[k]);
-        o.s_r[k] = scale(sc.r_max[k]);
-        o.s_t[k] = scale(sc.t_max[k]);
-        o.s_q[k] = scale(q *= sc.r_max[k]);
+        const double sg = scale(sc.norm[k] * sc.norm[k]), sr = scale(sc.r_max[k]), st = scale(sc.t_max[k]);
+        const double next_q = scale(q *= sc.r_max[k]);
+        if (k == 0)
+            o.g_first = (float)sg;
+        o.r_eye[k] = (float)(sc.a[k] * sr);
+        o.r_g[k] = (float)(sc.b[k] * sr / sg);
+        o.r_g2[k] = (float)(sc.c[k] * sr / (sg * sg));
+        o.t_of[k] = (float)(st / (sr * sg));
+        if (k + 1 < sc.steps)
+            o.g_of[k] = (float)(scale(sc.norm[k + 1] * sc.norm[k + 1]) / (sr * st));
+        o.q_of[k] = (float)(k == 0 ? next_q / sr : next_q / (sr * sq));
+        sq = next_q;
     }
+    o.q_last = (float)(1.0 / sq);
     o.eps = eps;
     o.parts = w.small_parts;
     o.q = w.small_q;

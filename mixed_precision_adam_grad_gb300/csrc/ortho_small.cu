@@ -141,8 +141,13 @@ __device__ __forceinline__ uint32_t set_up(Base &b, uint32_t cols)
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    return b.tmem;
+    return __shfl_sync(0xffffffffu, b.tmem, 0);
 }
+
+// The warp's number, in a form the compiler knows to be the same in all lanes:
+// what is computed from it and the kernel's arguments stays in uniform
+// registers, which the matrix instructions take (80 cycles each otherwise).
+__device__ __forceinline__ int warp_number() { return __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0); }
 
 // Wait for a barrier that tensor-core products arrive on; on a wait that runs
 // out the call is marked.
@@ -204,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
     __shared__ Base sh;
     const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const uint32_t tmem = set_up(sh, 128);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.y;
+    const int tid = threadIdx.x, warp = warp_number(), lane = tid & 31, b = blockIdx.y;
     launch_dependents();
     if (blockIdx.x == 0 && b == 0 && tid == 0)
         *a.status = 0;
@@ -388,12 +393,13 @@ __global__ void __launch_bounds__(512) k_small_poly(const __grid_constant__ Smal
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const uint32_t G = base, R = base + kPairBytes, Q = base + 2 * kPairBytes;
     const uint32_t tmem = set_up(sh, 256);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.x;
+    const int tid = threadIdx.x, warp = warp_number(), lane = tid & 31, b = blockIdx.x;
     const int quad = warp & 3, block = warp >> 2, row = quad * 32 + lane;
     const uint32_t n16 = (uint32_t)((a.m + 15) & ~15), k16 = n16 / 16, idesc = idesc_of(n16, false, false, false);
     const uint32_t acc_at = tmem + ((uint32_t)(quad * 32) << 16) + block * 32;
     const bool mine = quad * 32 < a.m;
     const bool diag = mine && quad == block;  // the lane's diagonal element is its number `lane`
+    const int eye_at = diag && row < a.m ? lane : -1;
     launch_dependents();
     wait_for_previous_grid();
     if (tid == 0 && (*(volatile unsigned *)a.status & kStatusWaitLimit))
@@ -440,15 +446,15 @@ __global__ void __launch_bounds__(512) k_small_poly(const __grid_constant__ Smal
     if (mine) {
 #pragma unroll
         for (int e = 0; e < 32; ++e)
-            v[e] = v[e] * inv * (inv * a.s_g[0]);
+            v[e] = v[e] * inv * (inv * a.g_first);
         put_pair(G, row, block, v);
     }
     fence_async_shared();
     __syncthreads();
 
     uint32_t phase = 0;
-    // one product (or two), waited for by every thread
-    auto products = [&](uint32_t a0, uint32_t b0, uint32_t a1, uint32_t b1) {
+    // one product (or two), which every thread then waits for
+    auto issue = [&](uint32_t a0, uint32_t b0, uint32_t a1, uint32_t b1) {
         if (warp == 0 && !a.test_stall) {
             tmem_fence_after();
             if (elect_one()) {
@@ -459,6 +465,8 @@ __global__ void __launch_bounds__(512) k_small_poly(const __grid_constant__ Smal
             }
             __syncwarp();
         }
+    };
+    auto wait = [&] {
         wait_products(sh, 0, phase & 1, a.status);
         ++phase;
     };
@@ -481,50 +489,49 @@ __global__ void __launch_bounds__(512) k_small_poly(const __grid_constant__ Smal
     };
 
     for (int k = 0; k < a.steps && !sh.abort; ++k) {
-        const float sg = a.s_g[k], sr = a.s_r[k];
         const bool more = k + 1 < a.steps;
-        products(G, G, 0, 0);
+        const float eye = a.r_eye[k], bb = a.r_g[k], cc = a.r_g2[k], t_of = a.t_of[k], g_of = a.g_of[k], q_of = a.q_of[k];
+        issue(G, G, 0, 0);
+        if (mine) {  // bG + aI, while the product runs
+            get_pair(G, row, block, v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                v[e] = fmaf(bb, v[e], e == eye_at ? eye : 0.0f);
+        }
+        wait();
         if (mine) {  // R = aI + bG + cG^2; the first R is also Q
-            const float cc = a.c[k] / (sg * sg) * sr, bb = a.b[k] / sg * sr;
             uint32_t x[32];
             tmem_load32(acc_at, x);
-            get_pair(G, row, block, v);
             tmem_wait_load();
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-                v[e] = fmaf(cc, __uint_as_float(x[e]), bb * v[e]);
-            if (diag && row < a.m) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (e == lane)
-                        v[e] = fmaf(a.a[k], sr, v[e]);
-            }
+                v[e] = fmaf(cc, __uint_as_float(x[e]), v[e]);
             put_pair(R, row, block, v);
             if (k == 0) {
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
-                    v[e] *= a.s_q[0] / sr;
+                    v[e] *= q_of;
                 put_pair(Q, row, block, v);
             }
         }
         settle();
         // T = R G and Q <- R Q
         if (more || k > 0) {
-            if (more && k > 0)
-                products(R, G, R, Q);
-            else if (more)
-                products(R, G, 0, 0);
-            else
-                products(R, Q, 0, 0);
             if (more)
-                keep(acc_at, a.s_t[k] / (sr * sg), G);
+                issue(R, G, k > 0 ? R : 0, Q);
+            else
+                issue(R, Q, 0, 0);
+            wait();
+            if (more)
+                keep(acc_at, t_of, G);
             if (k > 0)
-                keep(acc_at + (more ? 128 : 0), a.s_q[k] / (sr * a.s_q[k - 1]), Q);
+                keep(acc_at + (more ? 128 : 0), q_of, Q);
             settle();
         }
         if (more) {  // G <- R T
-            products(R, G, 0, 0);
-            keep(acc_at, a.s_g[k + 1] / (sr * a.s_t[k]), G);
+            issue(R, G, 0, 0);
+            wait();
+            keep(acc_at, g_of, G);
             settle();
         }
     }
@@ -552,7 +559,7 @@ __global__ void __launch_bounds__(kThreads) k_small_apply(const __grid_constant_
     __shared__ Base sh;
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const uint32_t tmem = set_up(sh, 128);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.y;
+    const int tid = threadIdx.x, warp = warp_number(), lane = tid & 31, b = blockIdx.y;
     const uint32_t n16 = (uint32_t)((a.m + 15) & ~15), k16 = n16 / 16;
     const int tiles = n16 > 64 ? 2 : 1;        // 64-column tiles along the short side
     const uint32_t q_lo = tiles * kTile;       // Q: tiles of hi, then tiles of lo
@@ -566,7 +573,7 @@ __global__ void __launch_bounds__(kThreads) k_small_apply(const __grid_constant_
         sh.abort = 1;
     __syncthreads();
     const float inv = a.inv[b] * kApplyScale;
-    const float back = 1.0f / (a.s_q[a.steps - 1] * kApplyScale);
+    const float back = a.q_last / kApplyScale;
     {
         const uint4 *q = reinterpret_cast<const uint4 *>(a.q) + (int64_t)b * (kPairBytes / 16);
         for (int i = tid; i < tiles * (kTile / 16); i += kThreads) {

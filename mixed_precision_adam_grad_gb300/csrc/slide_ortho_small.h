@@ -28,12 +28,18 @@ struct SmallOrtho {
     float *mom, *u;
     float mu, one_minus_mu;
     int nesterov;
-    // the polynomial: per step its coefficients and the scales (powers of two)
-    // of the FP16 pairs that hold G, R = aI + bG + cG^2, R G and the product
-    // of the R
+    // the polynomial: G, R = aI + bG + cG^2, T = R G and Q, the product of the
+    // R, are FP16 pairs times powers of two; per step the factors that take an
+    // accumulator (of scaled factors) or G to the next scaled pair
     int steps;
-    float a[kSmallMaxSteps], b[kSmallMaxSteps], c[kSmallMaxSteps];
-    float s_g[kSmallMaxSteps], s_r[kSmallMaxSteps], s_t[kSmallMaxSteps], s_q[kSmallMaxSteps];
+    float g_first;                   // scale of the first G
+    float r_eye[kSmallMaxSteps];     // a
+    float r_g[kSmallMaxSteps];       // b
+    float r_g2[kSmallMaxSteps];      // c
+    float t_of[kSmallMaxSteps];      // R G -> T
+    float g_of[kSmallMaxSteps];      // R T -> the next G
+    float q_of[kSmallMaxSteps];      // R Q -> Q; for the first step R -> Q
+    float q_last;                    // 1 / scale of the last Q
     float eps;
     // scratch
     float *parts;               // [batch][n_parts][128 x 128]
