@@ -85,19 +85,6 @@ __device__ __forceinline__ void load8(const void *base, int64_t at, int n, bool 
     }
 }
 
-__device__ __forceinline__ void store8(float *p, int n, bool vec, const float (&v)[8])
-{
-    if (vec && n >= 8) {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < n)
-                p[e] = v[e];
-    }
-}
-
 // Sum of a block's values in a fixed order; thread 0 has it.
 __device__ __forceinline__ double block_sum(double x)
 {
@@ -116,53 +103,162 @@ __device__ __forceinline__ double block_sum(double x)
     return t;
 }
 
-// A block of threads passes over 128 x 128 blocks of a matrix; a thread has
-// eight columns of every 16th row.
-constexpr int kRowsAtOnce = kPrepThreads / 16;
+constexpr int kRowsAtOnce = kPrepThreads / 16;  // rows of 128 columns, eight a thread
 
-// A partial sum of the matrix's squares per block of threads; for a Muon step
-// the squares are those of the update, which is formed from the replicas and
-// the momentum on the way and kept in u.
+// V values from an address that is aligned to V of them.
+template <int V>
+__device__ __forceinline__ void load_vec(const uint16_t *p, float (&v)[V])
+{
+    uint32_t u[V / 2];
+    if constexpr (V == 8) {
+        const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p));
+        u[0] = w.x, u[1] = w.y, u[2] = w.z, u[3] = w.w;
+    } else {
+        const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(p));
+        u[0] = w.x, u[1] = w.y;
+    }
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) {
+        v[2 * e] = __uint_as_float(u[e] << 16);
+        v[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void load_vec(const float *p, float (&v)[V])
+{
+    static_assert(V == 4, "16 bytes");
+    const float4 w = __ldcs(reinterpret_cast<const float4 *>(p));
+    v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+}
+
+// One value of a Muon step: the replicas' mean into the momentum, the update.
+__device__ __forceinline__ float muon_value(const SourceArgs &a, float sum, float &m)
+{
+    const float g = __fmul_rn(a.one_minus_mu, __fdiv_rn(sum, (float)a.R));
+    m = __fadd_rn(__fmul_rn(m, a.mu), g);
+    return a.nesterov ? __fadd_rn(__fmul_rn(m, a.mu), g) : m;
+}
+
+__device__ __forceinline__ void begin_source(const SourceArgs &a)
+{
+    ptx::launch_dependents();
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x <= kMaxPhases)
+        a.status[threadIdx.x] = 0;
+}
+
+// A partial sum of a matrix's squares per block of threads, the matrices lying
+// one after another without gaps: whole aligned vectors whatever the length of
+// a row.  For a Muon step the squares are those of the update, which is formed
+// on the way and kept in u.
 template <typename T, bool MUON>
 __global__ void __launch_bounds__(kPrepThreads) k_ortho_source(const __grid_constant__ SourceArgs a)
 {
+    begin_source(a);
+    // vectors a thread reads whole: 16 bytes of each array it reads most from
+    constexpr int V = !MUON && sizeof(T) == 2 ? 8 : 4, kAhead = MUON ? 2 : 4;
+    const int b = blockIdx.y;
+    const int64_t size = (int64_t)a.rows * a.cols, from = b * size, to = from + size;
+    const T *x = static_cast<const T *>(a.g.p[0]);
+    const int64_t v0 = (from + V - 1) / V, v1 = to / V;  // aligned vectors inside the matrix
+    double sum = 0.0;
+    auto square = [](const float(&v)[V]) {
+        float s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            s = fmaf(v[e], v[e], s);
+        return s;
+    };
+    for (int64_t k = v0 + (int64_t)blockIdx.x * (kPrepThreads * kAhead) + threadIdx.x; k < v1;
+         k += (int64_t)gridDim.x * (kPrepThreads * kAhead)) {
+        float v[kAhead][V], m[MUON ? kAhead : 1][V];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int64_t at = (k + j * kPrepThreads) * V;
+            if (at + V <= to) {
+                load_vec<V>(x + at, v[j]);
+                if constexpr (MUON)
+                    load_vec<V>(a.mom + at, m[j]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    v[j][e] = 0.0f;
+            }
+        }
+        if constexpr (MUON) {
+            for (int r = 1; r < a.R; ++r) {
+                float w[kAhead][V];
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    const int64_t at = (k + j * kPrepThreads) * V;
+                    if (at + V <= to)
+                        load_vec<V>(static_cast<const T *>(a.g.p[r]) + at, w[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j)
+                    if ((k + j * kPrepThreads) * V + V <= to)
+#pragma unroll
+                        for (int e = 0; e < V; ++e)
+                            v[j][e] = __fadd_rn(v[j][e], w[j][e]);
+            }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int64_t at = (k + j * kPrepThreads) * V;
+                if (at + V <= to) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        v[j][e] = muon_value(a, v[j][e], m[j][e]);
+                    __stcs(reinterpret_cast<float4 *>(a.mom + at), make_float4(m[j][0], m[j][1], m[j][2], m[j][3]));
+                    *reinterpret_cast<float4 *>(a.u + at) = make_float4(v[j][0], v[j][1], v[j][2], v[j][3]);
+                }
+            }
+        }
+        float part = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            part += square(v[j]);
+        sum += (double)part;
+    }
+    // the matrix's first and last values outside whole vectors
+    const int head = (int)((v0 * V < to ? v0 * V : to) - from), tail = v1 >= v0 ? (int)(to - v1 * V) : 0;
+    if (blockIdx.x == 0 && (int)threadIdx.x < head + tail) {
+        const int i = threadIdx.x;
+        const int64_t at = i < head ? from + i : v1 * V + (i - head);
+        float u = widen(x[at]);
+        if constexpr (MUON) {
+            for (int r = 1; r < a.R; ++r)
+                u = __fadd_rn(u, widen(static_cast<const T *>(a.g.p[r])[at]));
+            float m = a.mom[at];
+            u = muon_value(a, u, m);
+            a.mom[at] = m;
+            a.u[at] = u;
+        }
+        sum += (double)(u * u);
+    }
+    sum = block_sum(sum);
+    if (threadIdx.x == 0)
+        a.parts[(int64_t)b * kNormParts + blockIdx.x] = sum;
+}
+
+// The same of matrices with strides.  A block of threads passes over 128 x 128
+// blocks of a matrix; a thread has eight columns of every 16th row.
+template <typename T>
+__global__ void __launch_bounds__(kPrepThreads) k_ortho_source_strided(const __grid_constant__ SourceArgs a)
+{
+    begin_source(a);
     const int b = blockIdx.y, r0 = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * 8;
-    ptx::launch_dependents();
-    if (blockIdx.x == 0 && b == 0 && threadIdx.x <= kMaxPhases)
-        a.status[threadIdx.x] = 0;
     double sum = 0.0;
     for (int blk = blockIdx.x; blk < a.rblk * a.cblk; blk += gridDim.x) {
         const int rb = blk / a.cblk, cb = blk - rb * a.cblk;
         const int col = cb * 128 + c0, n = a.cols - col;
         float part = 0.0f;
         if (n > 0) {
-#pragma unroll MUON ? 1 : 4
+#pragma unroll 4
             for (int r = r0; r < 128; r += kRowsAtOnce) {
                 const int row = rb * 128 + r;
-                if (row >= a.rows)
-                    break;
-                const int64_t at = (int64_t)b * a.batch_stride + (int64_t)row * a.row_stride + col;
-                float v[8];
-                load8<T>(a.g.p[0], at, n, a.vec, v);
-                if constexpr (MUON) {
-                    float m[8];
-                    load8<float>(a.mom, at, n, a.vec, m);
-                    for (int k = 1; k < a.R; ++k) {
-                        float w[8];
-                        load8<T>(a.g.p[k], at, n, a.vec, w);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            v[e] = __fadd_rn(v[e], w[e]);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float g = __fmul_rn(a.one_minus_mu, __fdiv_rn(v[e], (float)a.R));
-                        m[e] = __fadd_rn(__fmul_rn(m[e], a.mu), g);
-                        v[e] = a.nesterov ? __fadd_rn(__fmul_rn(m[e], a.mu), g) : m[e];
-                    }
-                    store8(a.mom + at, n, a.vec, m);
-                    store8(a.u + at, n, a.vec, v);
-                }
+                float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+                if (row < a.rows)
+                    load8<T>(a.g.p[0], (int64_t)b * a.batch_stride + (int64_t)row * a.row_stride + col, n, a.vec, v);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     part = fmaf(v[e], v[e], part);
@@ -187,9 +283,74 @@ struct ScaleArgs {
     float eps, scale;
 };
 
-// X = G / (|G|_F + eps) as a pair of FP16 matrices in tiles, zero beyond the
-// matrix's edges.
+// The 16 aligned bytes at p; what lies outside [lo, hi), the caller's array,
+// is not read.
+__device__ __forceinline__ uint4 load_granule(uintptr_t p, uintptr_t lo, uintptr_t hi)
+{
+    if (p >= lo && p + 16 <= hi)
+        return *reinterpret_cast<const uint4 *>(p);
+    uint32_t w[4] = {0, 0, 0, 0};
+    for (int i = 0; i < 8; ++i)  // two bytes at a time: the elements are aligned to that
+        if (p + 2 * i >= lo && p + 2 * i < hi)
+            w[i >> 1] |= (uint32_t) * reinterpret_cast<const uint16_t *>(p + 2 * i) << (16 * (i & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Eight values from element c8*8 of the 128 of a row that begins anywhere: the
+// row's 16 lanes read aligned vectors, take the next lane's first one too and
+// shift.  `row`: address of the row's first of the 128 (in any case aligned to
+// the type), n: how many there are; all 16 lanes call it with the same two.
 template <typename T>
+__device__ __forceinline__ void load8_shifted(uintptr_t row, int n, int c8, uintptr_t lo, uintptr_t hi, float (&v)[8])
+{
+    constexpr int kVecs = sizeof(T) / 2;  // 16-byte vectors of eight values
+    const uint32_t off = (uint32_t)(row & 15);
+    const uintptr_t base = row - off, end = row + (uintptr_t)n * sizeof(T);
+    uint32_t w[4 * kVecs + 4];
+#pragma unroll
+    for (int i = 0; i <= kVecs; ++i) {
+        // the last vector is the next lane's first; the last lane reads it itself
+        const uintptr_t p = base + (uintptr_t)(c8 * kVecs + i) * 16;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (i < kVecs || c8 == 15)
+            if (n > 0 && p < end)
+                x = load_granule(p, lo, hi);
+        w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t next = __shfl_down_sync(0xffffffffu, w[j], 1);
+        if (c8 != 15)
+            w[4 * kVecs + j] = next;
+    }
+    const bool two = off & 8, one = off & 4;
+#pragma unroll
+    for (int j = 0; j < 4 * kVecs + 2; ++j)
+        w[j] = two ? w[j + 2] : w[j];
+#pragma unroll
+    for (int j = 0; j < 4 * kVecs + 1; ++j)
+        w[j] = one ? w[j + 1] : w[j];
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t s = (off & 2) * 8;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t x = __funnelshift_r(w[j], w[j + 1], s);
+            v[2 * j] = __uint_as_float(x << 16);
+            v[2 * j + 1] = __uint_as_float(x & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = __uint_as_float(w[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = c8 * 8 + j < n ? v[j] : 0.0f;
+}
+
+// X = G / (|G|_F + eps) as a pair of FP16 matrices in tiles, zero beyond the
+// matrix's edges.  SHIFTED: the rows do not begin at 16-byte boundaries.
+template <typename T, bool SHIFTED>
 __global__ void __launch_bounds__(kPrepThreads) k_ortho_scale(const __grid_constant__ ScaleArgs a)
 {
     __shared__ float s_inv;
@@ -204,16 +365,23 @@ __global__ void __launch_bounds__(kPrepThreads) k_ortho_scale(const __grid_const
         s_inv = x == 0.0 && a.eps == 0.0f ? 0.0f : (float)(1.0 / (sqrt(x) + (double)a.eps));
     __syncthreads();
     const float inv = s_inv, scale = a.scale;
+    const uintptr_t lo_at = (uintptr_t)a.x;
+    const uintptr_t hi_at = (uintptr_t)(static_cast<const T *>(a.x) + (int64_t)(gridDim.y - 1) * a.batch_stride +
+                                        (int64_t)(a.rows - 1) * a.row_stride + a.cols);
     for (int blk = blockIdx.x; blk < a.rblk * a.cblk; blk += gridDim.x) {
         const int rb = blk / a.cblk, cb = blk - rb * a.cblk;
         const int col = cb * 128 + c8 * 8, n = a.cols - col;
         const int64_t tile = (int64_t)b * a.out_stride + ((int64_t)rb * a.c64 + 2 * cb + (c8 >> 3)) * kTileElems;
-#pragma unroll 4
+#pragma unroll SHIFTED ? 2 : 4
         for (int r = r0; r < 128; r += kRowsAtOnce) {
             const int row = rb * 128 + r;
+            const int64_t at_row = (int64_t)b * a.batch_stride + (int64_t)row * a.row_stride;
             float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-            if (row < a.rows && n > 0)
-                load8<T>(a.x, (int64_t)b * a.batch_stride + (int64_t)row * a.row_stride + col, n, a.vec, v);
+            if constexpr (SHIFTED)
+                load8_shifted<T>((uintptr_t)(static_cast<const T *>(a.x) + at_row + cb * 128),
+                                 row < a.rows ? min(128, a.cols - cb * 128) : 0, c8, lo_at, hi_at, v);
+            else if (row < a.rows && n > 0)
+                load8<T>(a.x, at_row + col, n, true, v);
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -662,9 +830,18 @@ cudaError_t enqueue_source(const Shape &s, const Work &w, const Schedule &sc, So
     a.parts = w.parts;
     a.status = w.status;
     const int64_t blocks = (int64_t)s.rblk * s.cblk;
-    const int parts = (int)(blocks < kNormParts ? blocks : kNormParts);
+    const int64_t per = (1216 + s.batch - 1) / s.batch;  // eight blocks of threads per SM
+    const int64_t most = per < kNormParts ? per : kNormParts;
+    const int parts = (int)(blocks < most ? blocks : most);
     const dim3 grid(parts, s.batch);
-    if (muon) {
+    const bool flat = a.row_stride == s.cols && (s.batch == 1 || a.batch_stride == (int64_t)s.rows * s.cols) &&
+                      (uintptr_t)a.g.p[0] % 16 == 0;
+    if (!muon && !flat) {
+        if (fp32)
+            k_ortho_source_strided<float><<<grid, kPrepThreads, 0, stream>>>(a);
+        else
+            k_ortho_source_strided<uint16_t><<<grid, kPrepThreads, 0, stream>>>(a);
+    } else if (muon) {
         if (fp32)
             k_ortho_source<float, true><<<grid, kPrepThreads, 0, stream>>>(a);
         else
@@ -686,7 +863,7 @@ cudaError_t enqueue_source(const Shape &s, const Work &w, const Schedule &sc, So
     c.cols = s.cols;
     c.rblk = s.rblk;
     c.cblk = s.cblk;
-    c.vec = a.vec;
+    c.vec = muon ? s.cols % 4 == 0 : a.vec;
     c.out.hi = w.x_hi[0];
     c.out.lo = w.x_lo;
     c.c64 = 2 * s.cpad;
@@ -695,10 +872,12 @@ cudaError_t enqueue_source(const Shape &s, const Work &w, const Schedule &sc, So
     c.parts = w.parts;
     c.eps = eps;
     c.scale = sc.sx[0];
-    const int64_t per = (1216 + s.batch - 1) / s.batch;
     const dim3 grid2((unsigned)(blocks < per ? blocks : per), s.batch);
-    return muon || fp32 ? launch_behind(k_ortho_scale<float>, grid2, c, stream)
-                        : launch_behind(k_ortho_scale<uint16_t>, grid2, c, stream);
+    if (muon || fp32)
+        return c.vec ? launch_behind(k_ortho_scale<float, false>, grid2, c, stream)
+                     : launch_behind(k_ortho_scale<float, true>, grid2, c, stream);
+    return c.vec ? launch_behind(k_ortho_scale<uint16_t, false>, grid2, c, stream)
+                 : launch_behind(k_ortho_scale<uint16_t, true>, grid2, c, stream);
 }
 
 cudaError_t enqueue(const Shape &s, const Work &w, const Schedule &sc, const SourceArgs &a, const Finish &f, bool fp32,
