@@ -12,8 +12,9 @@
 // read finished accumulators from tensor memory, which holds two output tiles,
 // so an epilogue overlaps the next tile's products.  An epilogue warp takes 32
 // rows x 64 columns at a time: it copies their C into its own buffer (for the
-// first chunk of a tile before the product is ready), replaces it by the
-// result and writes that from there, all with bulk copies of 4 KiB.
+// first chunk of a tile before the product is ready, for both of its chunks
+// where only the high half is kept), replaces it by the result and writes that
+// from there, all with bulk copies of 4 KiB.
 //
 // One launch runs all the products of an iteration, one phase after the other:
 // a CTA whose tiles of a phase are written counts itself in, and the producers
@@ -48,7 +49,7 @@ constexpr int kStageBytes = 2 * kSlot;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (2 + kEpiWarps) * 32;
 constexpr int kPiece = 4096;                      // 32 rows of a tile
-constexpr int kEpiBytes = 2 * kPiece;             // an epilogue warp's buffer: hi and lo
+constexpr int kEpiBytes = 2 * kPiece;             // an epilogue warp's buffer: hi and lo of a chunk, or hi of two
 constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiWarps * kEpiBytes;
 constexpr unsigned kStatusWaitLimit = 2u;
 constexpr unsigned kFullMask = 0xffffffffu;
@@ -185,7 +186,7 @@ __device__ __forceinline__ void read_half(uint32_t piece, int lane, int h, uint3
 // replaced by the result.
 template <int CG, int EPI>
 __device__ __forceinline__ void epilogue_chunk(const OrthoPlan &plan, const OrthoGemm &g, const Tile &x, int ib, int c, int row, int lane,
-                                               uint32_t acc_addr, uint32_t buf)
+                                               uint32_t acc_addr, uint32_t buf, float d_row)
 {
     constexpr bool kFinal = EPI == kEpiOut || EPI == kEpiMuon;
     const OrthoProduct &p = g.p[x.prob];
@@ -202,19 +203,22 @@ __device__ __forceinline__ void epilogue_chunk(const OrthoPlan &plan, const Orth
         read_half(buf + kPiece, lane, 1, clo + 16);
         __syncwarp();
     }
-    float d_row = 0.0f;
     const float *d = p.dvec + (int64_t)x.b * g.d_stride;
-    if constexpr (kReadsOf<EPI> > 1)
-        if (!g.d_by_col)
-            d_row = d[gi] * p.c_scale;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         uint32_t acc[32];
         tmem_load32(acc_addr + h * 32, acc);
         if constexpr (kReadsOf<EPI> > 0 && !kFinal)
             read_half(buf, lane, h, chi);
-        if constexpr (kReadsOf<EPI> > 1 && !kFinal)
-            read_half(buf + kPiece, lane, h, clo);
+        if constexpr (kReadsOf<EPI> > 1 && !kFinal) {
+            if (p.c.lo) {
+                read_half(buf + kPiece, lane, h, clo);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    clo[e] = 0;
+            }
+        }
         tmem_wait_load();
         constexpr int kAt = kFinal ? 16 : 0;
         float v[32];
@@ -370,64 +374,80 @@ __device__ __forceinline__ void prefetch_chunk(const OrthoGemm &g, const Tile &x
     const int jb = x.j * CG + (c >> 1);
     const int64_t piece = (int64_t)x.b * g.out_stride + ((int64_t)ib * g.out_c64 + 2 * jb + (c & 1)) * kTileElems +
                           quad * 32 * 64;
-    mbar_expect_tx(bar, kReadsOf<EPI> * kPiece);
+    const bool lo = kReadsOf<EPI> > 1 && p.c.lo;
+    mbar_expect_tx(bar, lo ? 2 * kPiece : kPiece);
     bulk_load(buf, p.c.hi + piece, kPiece, bar);
-    if constexpr (kReadsOf<EPI> > 1)
+    if (lo)
         bulk_load(buf + kPiece, p.c.lo + piece, kPiece, bar);
 }
 
 // Shared state of a CTA, besides the operand ring and the epilogue's buffers.
 struct Shared {
-    uint64_t full[kStages], empty[kStages], peer[kStages], acc_full[2], acc_empty[2], c[kEpiWarps], phase;
+    uint64_t full[kStages], empty[kStages], peer[kStages], acc_full[2], acc_empty[2], c[kEpiWarps][2], phase;
     uint32_t tmem;
     unsigned written;        // epilogue warps whose tiles of the phase are written
     volatile int abort;
 };
 
 // The tiles of one phase, by one epilogue warp.  n: tiles so far (of all
-// phases); seq: chunks of C asked for so far.
+// phases); asked: copies of C asked for so far on each of the two barriers.
 template <int CG, int EPI>
 __device__ __forceinline__ bool epilogue_tiles(const OrthoPlan &plan, const OrthoGemm &g, Shared &sh, uint32_t tmem,
                                                uint32_t mine, int warp, int lane, uint32_t rank, uint32_t &n,
-                                               uint32_t &seq)
+                                               uint32_t (&asked)[2])
 {
     // warp (quad, half): rows 32*quad.., every second chunk of 64 columns
     const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
-    const uint32_t bar = smem_addr(&sh.c[warp]);
     const int n_tiles = tile_count<CG>(g, plan.batch);
     for (int t = blockIdx.x / CG; t < n_tiles; t += gridDim.x / CG, ++n) {
         const Tile x = decode<CG>(g, plan.batch, t);
+        const OrthoProduct &p = g.p[x.prob];
         const uint32_t buf = n & 1, use = n >> 1;
         const int ib = x.i * CG + rank;
-        // the chunks of the tile that exist (and, of a symmetric result, are kept)
+        // the chunks of the tile that exist (and, of a symmetric result, are
+        // kept): c0 and c0 + 2
         const int c0 = (g.sym ? max(0, 2 * (ib - x.j * CG)) : 0) + half;
         const int c1 = ib < g.mblk ? min(2 * CG, 2 * (g.nblk - x.j * CG)) : 0;
-        auto fetch = [&](int c) {
+        // both chunks fit side by side if they have no low halves
+        const bool both = EPI == kEpiPoly || (EPI == kEpiSym && !p.c.lo && !p.out.lo);
+        auto fetch = [&](int c, int i) {  // into buffer i
             if (elect_one()) {
-                bulk_wait_read<0>();  // of the store out of the buffer
+                bulk_wait_read<0>();  // of the stores out of it
                 if constexpr (kReadsOf<EPI> > 0)
-                    prefetch_chunk<CG, EPI>(g, x, ib, c, quad, mine, bar);
+                    prefetch_chunk<CG, EPI>(g, x, ib, c, quad, mine + i * kPiece, smem_addr(&sh.c[warp][i]));
             }
             __syncwarp();
             if constexpr (kReadsOf<EPI> > 0)
-                ++seq;
+                ++asked[i];
         };
         if (c0 < c1)
-            fetch(c0);
+            fetch(c0, 0);
+        if (both && c0 + 2 < c1)
+            fetch(c0 + 2, 1);
+        float d_row = 0.0f;
+        if constexpr (kReadsOf<EPI> > 1) {
+            const float *d = p.dvec + (int64_t)x.b * g.d_stride, *cols = p.dvec2 ? p.dvec2 + (int64_t)x.b * g.d_stride : d;
+            if (!g.d_by_col && c0 < c1)
+                d_row = d[ib * 128 + row] * p.c_scale;
+            if ((g.d_by_col || p.dvec2) && lane < 2)  // the factors of the columns, on their way
+                for (int c = c0; c < c1; c += 2)
+                    asm volatile("prefetch.global.L1 [%0];" ::"l"(cols + (x.j * CG + (c >> 1)) * 128 + (c & 1) * 64 + lane * 32));
+        }
         if constexpr (EPI == kEpiMuon)
             for (int c = c0; c < c1; c += 2)
                 prefetch_theta(plan, x, ib * 128 + quad * 32, (x.j * CG + (c >> 1)) * 128 + (c & 1) * 64, lane);
         bool ok = __all_sync(kFullMask, mbar_wait(smem_addr(&sh.acc_full[buf]), use & 1, &sh.abort));
         tmem_fence_after();
         for (int c = c0; c < c1 && ok; c += 2) {
+            const int i = both && c != c0;
             if constexpr (kReadsOf<EPI> > 0)
-                ok = __all_sync(kFullMask, mbar_wait(bar, (seq - 1) & 1, &sh.abort));
+                ok = __all_sync(kFullMask, mbar_wait(smem_addr(&sh.c[warp][i]), (asked[i] - 1) & 1, &sh.abort));
             if (!ok)
                 break;
             epilogue_chunk<CG, EPI>(plan, g, x, ib, c, row, lane,
-                                    tmem + ((uint32_t)(quad * 32) << 16) + buf * 128 * CG + c * 64, mine);
-            if (c + 2 < c1)
-                fetch(c + 2);
+                                    tmem + ((uint32_t)(quad * 32) << 16) + buf * 128 * CG + c * 64, mine + i * kPiece, d_row);
+            if (!both && c + 2 < c1)
+                fetch(c + 2, 0);
         }
         if (!ok)
             return false;
@@ -463,7 +483,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_ortho_products(const __grid_con
             mbar_init(smem_addr(&sh.acc_empty[a]), CG * kEpiWarps);
         }
         for (int w = 0; w < kEpiWarps; ++w)
-            mbar_init(smem_addr(&sh.c[w]), 1);
+            for (int i = 0; i < 2; ++i)
+                mbar_init(smem_addr(&sh.c[w][i]), 1);
         mbar_init(smem_addr(&sh.phase), 1);
         sh.abort = 0;
         sh.written = 0;
@@ -585,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ortho_products(const __grid_con
         const int w = warp - 2;
         const int ew = (warp & 3) | ((w >> 2) << 2);  // a warp reads the 32 lanes of tensor memory of its number mod 4
         const uint32_t mine = ring + kStages * kStageBytes + ew * kEpiBytes;
-        uint32_t n = 0, seq = 0;
+        uint32_t n = 0, asked[2] = {0, 0};
         bool ok = true;
         for (int f = 0; f < plan.n_phases && ok; ++f) {
             const OrthoGemm &g = plan.ph[f];
@@ -596,30 +617,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_ortho_products(const __grid_con
                 fence_async();
             }
             switch (g.epi) {
-            case kEpiGram: ok = epilogue_tiles<CG, kEpiGram>(plan, g, sh, tmem, mine, ew, lane, rank, n, seq); break;
-            case kEpiPoly: ok = epilogue_tiles<CG, kEpiPoly>(plan, g, sh, tmem, mine, ew, lane, rank, n, seq); break;
-            case kEpiSym: ok = epilogue_tiles<CG, kEpiSym>(plan, g, sh, tmem, mine, ew, lane, rank, n, seq); break;
-            case kEpiApply: ok = epilogue_tiles<CG, kEpiApply>(plan, g, sh, tmem, mine, ew, lane, rank, n, seq); break;
-            case kEpiOut: ok = epilogue_tiles<CG, kEpiOut>(plan, g, sh, tmem, mine, ew, lane, rank, n, seq); break;
-            default: ok = epilogue_tiles<CG, kEpiMuon>(plan, g, sh, tmem, mine, ew, lane, rank, n, seq); break;
+            case kEpiGram: ok = epilogue_tiles<CG, kEpiGram>(plan, g, sh, tmem, mine, ew, lane, rank, n, asked); break;
+            case kEpiPoly: ok = epilogue_tiles<CG, kEpiPoly>(plan, g, sh, tmem, mine, ew, lane, rank, n, asked); break;
+            case kEpiSym: ok = epilogue_tiles<CG, kEpiSym>(plan, g, sh, tmem, mine, ew, lane, rank, n, asked); break;
+            case kEpiApply: ok = epilogue_tiles<CG, kEpiApply>(plan, g, sh, tmem, mine, ew, lane, rank, n, asked); break;
+            case kEpiOut: ok = epilogue_tiles<CG, kEpiOut>(plan, g, sh, tmem, mine, ew, lane, rank, n, asked); break;
+            default: ok = epilogue_tiles<CG, kEpiMuon>(plan, g, sh, tmem, mine, ew, lane, rank, n, asked); break;
             }
             bulk_wait<0>();
             __syncwarp();
-            if (ok && f + 1 < plan.n_phases && lane == 0) {  // the CTA's last warp counts it in
-                __threadfence();
-                if (atomicAdd(&sh.written, 1u) == (unsigned)((f + 1) * kEpiWarps - 1)) {
-                    __threadfence();
-                    atomicAdd(plan.status + f + 1, 1u);
-                }
-            }
+            if (ok && f + 1 < plan.n_phases && lane == 0)  // the CTA's last warp counts it in
+                if (add_shared(smem_addr(&sh.written), 1u) == (unsigned)((f + 1) * kEpiWarps - 1))
+                    add_release(plan.status + f + 1, 1u);
             __syncwarp();
         }
         if (!ok) {
             sh.abort = 1;
             if (lane == 0)
                 atomicOr(plan.status, kStatusWaitLimit);
-            if (seq > 0)  // a copy of C may be in flight
-                mbar_wait(smem_addr(&sh.c[ew]), (seq - 1) & 1, nullptr);
+            for (int i = 0; i < 2; ++i)  // copies of C may be in flight
+                if (asked[i] > 0)
+                    mbar_wait(smem_addr(&sh.c[ew][i]), (asked[i] - 1) & 1, nullptr);
         }
     }
     __syncwarp();

@@ -74,29 +74,45 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     return false;
 }
 
-__device__ __forceinline__ unsigned load_acquire(const unsigned *p)
+__device__ __forceinline__ unsigned load_relaxed(const unsigned *p)
 {
     unsigned v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
 
-// Wait until *counter has reached `target`; false if the limit passed first,
-// or bit `stop` of *status or *abort was seen.
+__device__ __forceinline__ void add_release(unsigned *p, unsigned v)
+{
+    asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+// Add to a word of shared memory; the old value.  Orders like a barrier between
+// the threads of the CTA that meet in the word.
+__device__ __forceinline__ unsigned add_shared(uint32_t addr, unsigned v)
+{
+    unsigned old;
+    asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(addr), "r"(v) : "memory");
+    return old;
+}
+
+// Wait until *counter has reached `target` and acquire what was released with
+// it; false if the limit passed first, or bit `stop` of *status or *abort was
+// seen.
 __device__ __forceinline__ bool counter_wait(const unsigned *counter, unsigned target, const unsigned *status,
                                              unsigned stop, volatile int *abort)
 {
-    if (load_acquire(counter) >= target)
-        return true;
-    const unsigned long long t0 = global_ns();
-    for (uint32_t round = 0; round < kWaitLimitTries / 32; ++round) {
-        for (int i = 0; i < 32; ++i)
-            if (load_acquire(counter) >= target)
-                return true;
-        if (*abort || (load_acquire(status) & stop) || global_ns() - t0 > kWaitLimitNs)
-            return false;
+    bool ok = load_relaxed(counter) >= target;
+    if (!ok) {
+        const unsigned long long t0 = global_ns();
+        for (uint32_t round = 0; round < kWaitLimitTries / 32 && !ok; ++round) {
+            for (int i = 0; i < 32 && !ok; ++i)
+                ok = load_relaxed(counter) >= target;
+            if (!ok && (*abort || (load_relaxed(status) & stop) || global_ns() - t0 > kWaitLimitNs))
+                return false;
+        }
     }
-    return false;
+    asm volatile("fence.acq_rel.gpu;" ::: "memory");
+    return ok;
 }
 
 // 1-D bulk copies: global -> shared (completes `bytes` on the mbarrier) and
