@@ -586,6 +586,8 @@ cudaError_t enqueue_products(const Shape &s, const Work &w, const Schedule &sc, 
     plan.w = f.w;
     plan.w_row = f.w_row;
     plan.w_batch = f.w_batch;
+    plan.vec = (uintptr_t)f.w % 16 == 0 && (f.epi == kEpiMuon ? s.cols % 8 == 0 && (uintptr_t)f.theta % 32 == 0
+                                                              : f.w_row % 8 == 0 && (s.batch == 1 || f.w_batch % 8 == 0));
     plan.theta = f.theta;
     plan.decay = f.decay;
     plan.step = f.step;

@@ -14,7 +14,9 @@
 // rows x 64 columns at a time: it copies their C into its own buffer (for the
 // first chunk of a tile before the product is ready, for both of its chunks
 // where only the high half is kept), replaces it by the result and writes that
-// from there, all with bulk copies of 4 KiB.
+// from there, all with bulk copies of 4 KiB.  (Low halves through registers
+// instead, in 32-byte sectors, made room for a sixth stage, but the phases that
+// have them took 15 to 50 % longer.)
 //
 // One launch runs all the products of an iteration, one phase after the other:
 // a CTA whose tiles of a phase are written counts itself in, and the producers
@@ -123,10 +125,10 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr)
     return v;
 }
 
-__device__ __forceinline__ float lds32(uint32_t addr)
+__device__ __forceinline__ uint16_t lds16(uint32_t addr)
 {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
     return v;
 }
 
@@ -135,7 +137,7 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// Columns 32h..32h+31 of the lane's row of a 64-column piece, as hi (and lo).
+// Columns 32h..32h+31 of the lane's row of a 64-column piece: the high halves.
 __device__ __forceinline__ void put_hi(uint32_t piece, int lane, int h, const float (&v)[32], float s)
 {
     const uint32_t row = piece + lane * 128;
@@ -149,29 +151,164 @@ __device__ __forceinline__ void put_hi(uint32_t piece, int lane, int h, const fl
     }
 }
 
-__device__ __forceinline__ void put_pair(uint32_t hi, uint32_t lo, int lane, int h, const float (&v)[32], float s)
+// High and low halves, into the piece and the one behind it.
+__device__ __forceinline__ void put_pair(uint32_t piece, int lane, int h, const float (&v)[32], float s)
 {
-    const uint32_t at = lane * 128;
+    const uint32_t row = piece + lane * 128;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         uint32_t u[4], w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float x = v[8 * q + 2 * e] * s, y = v[8 * q + 2 * e + 1] * s;
-            const __half2 p = __floats2half2_rn(x, y);
-            const float2 f = __half22float2(p);
-            u[e] = pack_half2(p);
+            const __half2 k = __floats2half2_rn(x, y);
+            const float2 f = __half22float2(k);
+            u[e] = pack_half2(k);
             w[e] = pack_half2(__floats2half2_rn((x - f.x) * kLoScale, (y - f.y) * kLoScale));
         }
-        const uint32_t c = ((4 * h + q) ^ (lane & 7)) << 4;
-        sts128(hi + at + c, make_uint4(u[0], u[1], u[2], u[3]));
-        sts128(lo + at + c, make_uint4(w[0], w[1], w[2], w[3]));
+        const uint32_t c = row + (((4 * h + q) ^ (lane & 7)) << 4);
+        sts128(c, make_uint4(u[0], u[1], u[2], u[3]));
+        sts128(c + kPiece, make_uint4(w[0], w[1], w[2], w[3]));
     }
 }
 
-// What an epilogue reads of C.
+// Four floats, loaded where they are used (all of a chunk's at once would not
+// fit into the registers).
+__device__ __forceinline__ float4 load_here(const float *p)
+{
+    float4 v;
+    asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+    return v;
+}
+
+// Whether an epilogue has a C.
 template <int EPI>
-constexpr int kReadsOf = EPI == kEpiGram ? 0 : EPI == kEpiPoly ? 1 : 2;
+constexpr bool kHasC = EPI != kEpiGram;
+
+// How C enters: hi times one factor; hi and lo times the row's factor; hi times
+// the row's and lo times the column's (EpilogueKind: dvec2); hi and lo times
+// the column's factor.
+enum CMode { kCHigh = 0, kCRow = 1, kCTwo = 2, kCCol = 3 };
+
+// What a warp needs of a product's arguments, in registers.
+struct Local {
+    float alpha, s_out, d_row, c_scale, col_scale, eye;
+    const float *d_col;   // of the matrix; kCTwo, kCCol
+    float *d_out;         // of the matrix; NULL: the diagonal stays
+    __half *out_hi, *out_lo;  // out_lo NULL: only the high half is kept
+};
+
+__device__ __forceinline__ void put_bf16(uint32_t piece, int lane, int h, const float (&v)[32])
+{
+    const uint32_t row = piece + lane * 128;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        uint32_t u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(v[8 * q + 2 * e], v[8 * q + 2 * e + 1]);
+            u[e] = *reinterpret_cast<const uint32_t *>(&x);
+        }
+        sts128(row + (((4 * h + q) ^ (lane & 7)) << 4), make_uint4(u[0], u[1], u[2], u[3]));
+    }
+}
+
+// The orthogonal factor goes to the weights' update through 16-bit shared
+// memory: FP16 times this, 2^-12 of the value off, a tenth of the factor's own
+// error, and the weights stay in FP32.
+constexpr float kMuonScale = 256.0f;
+
+__device__ __forceinline__ float muon_weight(const OrthoPlan &plan, float th, float o)
+{
+    return __fsub_rn(__fmul_rn(th, plan.decay), __fmul_rn(plan.step, o * (1.0f / kMuonScale)));
+}
+
+// Writes a piece (32 rows from row0, 64 columns from gj) to the caller's
+// array, along the rows: eight lanes a row where vectors fit, else one row at a
+// time, 32 neighbouring columns together.
+template <int EPI>
+__device__ __forceinline__ void write_rows(const OrthoPlan &plan, int b, int row0, int gj, int lane, uint32_t buf)
+{
+    const int64_t next = EPI == kEpiMuon ? plan.cols : plan.w_row;
+    const int64_t at0 = EPI == kEpiMuon ? ((int64_t)b * plan.rows + row0) * plan.cols + gj
+                                        : (int64_t)b * plan.w_batch + (int64_t)row0 * plan.w_row + gj;
+    const int lim = min(32, plan.rows - row0), n = plan.cols - gj;
+    if (plan.vec && n >= 64) {
+        const int c = lane & 7;
+        constexpr int kAtOnce = 4;
+#pragma unroll 1
+        for (int r0 = lane >> 3; r0 < 32; r0 += 4 * kAtOnce) {
+            uint32_t th[kAtOnce][8];
+            if constexpr (EPI == kEpiMuon) {
+#pragma unroll
+                for (int j = 0; j < kAtOnce; ++j)
+                    if (r0 + 4 * j < lim)
+                        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                                     : "=r"(th[j][0]), "=r"(th[j][1]), "=r"(th[j][2]), "=r"(th[j][3]), "=r"(th[j][4]),
+                                       "=r"(th[j][5]), "=r"(th[j][6]), "=r"(th[j][7])
+                                     : "l"(plan.theta + at0 + (r0 + 4 * j) * next + c * 8));
+            }
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                const int r = r0 + 4 * j;
+                if (r >= lim)
+                    continue;
+                uint4 w = lds128(buf + r * 128 + ((c ^ (r & 7)) << 4));
+                const int64_t at = at0 + r * next + c * 8;
+                if constexpr (EPI == kEpiMuon) {
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t y[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 o = unpack_half2(u[e]);
+                        const float p = muon_weight(plan, __uint_as_float(th[j][2 * e]), o.x);
+                        const float q = muon_weight(plan, __uint_as_float(th[j][2 * e + 1]), o.y);
+                        th[j][2 * e] = __float_as_uint(p);
+                        th[j][2 * e + 1] = __float_as_uint(q);
+                        const __nv_bfloat162 z = __floats2bfloat162_rn(p, q);
+                        y[e] = *reinterpret_cast<const uint32_t *>(&z);
+                    }
+                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(plan.theta + at),
+                                 "r"(th[j][0]), "r"(th[j][1]), "r"(th[j][2]), "r"(th[j][3]), "r"(th[j][4]), "r"(th[j][5]),
+                                 "r"(th[j][6]), "r"(th[j][7])
+                                 : "memory");
+                    w = make_uint4(y[0], y[1], y[2], y[3]);
+                }
+                *reinterpret_cast<uint4 *>(plan.w + at) = w;
+            }
+        }
+        return;
+    }
+    constexpr int kAtOnce = 16;  // rows whose loads are in flight together
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        const int col = lane + 32 * (i & 1), r0 = (i >> 1) * kAtOnce;
+        if (col >= n)
+            continue;
+        float *th = EPI == kEpiMuon ? plan.theta + at0 + r0 * next + col : nullptr;
+        uint16_t *w = plan.w + at0 + r0 * next + col;
+        const uint32_t at = buf + r0 * 128 + (lane & 7) * 2;
+        const int c = col >> 3;
+        float old[kAtOnce];
+        if constexpr (EPI == kEpiMuon) {
+#pragma unroll
+            for (int r = 0; r < kAtOnce; ++r)
+                old[r] = r0 + r < lim ? __ldcs(th + r * next) : 0.0f;
+        }
+#pragma unroll
+        for (int r = 0; r < kAtOnce; ++r) {
+            uint16_t u = lds16(at + r * 128 + ((c ^ (r & 7)) << 4));
+            if constexpr (EPI == kEpiMuon) {
+                const float p = muon_weight(plan, old[r], __half2float(__ushort_as_half(u)));
+                u = __bfloat16_as_ushort(__float2bfloat16_rn(p));
+                if (r0 + r < lim)
+                    __stcs(th + r * next, p);
+            }
+            if (r0 + r < lim)
+                w[r * next] = u;
+        }
+    }
+}
 
 __device__ __forceinline__ void read_half(uint32_t piece, int lane, int h, uint32_t *w)
 {
@@ -182,168 +319,93 @@ __device__ __forceinline__ void read_half(uint32_t piece, int lane, int h, uint3
     }
 }
 
-// One 64-column chunk (c of the tile's) of this warp's 32 rows.  buf: its C,
-// replaced by the result.
-template <int CG, int EPI>
-__device__ __forceinline__ void epilogue_chunk(const OrthoPlan &plan, const OrthoGemm &g, const Tile &x, int ib, int c, int row, int lane,
-                                               uint32_t acc_addr, uint32_t buf, float d_row)
+// One chunk: this warp's 32 rows (the lane's is gi) x 64 columns from gj on.
+// buf holds C (hi, and lo behind it) and is where results leave from; at: the
+// chunk's place in the operands, in values.
+template <int EPI, int MODE>
+__device__ __forceinline__ void epilogue_chunk(const OrthoPlan &plan, const Local &k, int b, int gi, int gj, int lane,
+                                               uint32_t acc_addr, uint32_t buf, int64_t at)
 {
-    constexpr bool kFinal = EPI == kEpiOut || EPI == kEpiMuon;
-    const OrthoProduct &p = g.p[x.prob];
-    const int jb = x.j * CG + (c >> 1);
-    const int gi = ib * 128 + row, gj = jb * 128 + (c & 1) * 64;
-    // the caller's arrays are written from FP32 in the buffer: all of C is
-    // read first; otherwise each half's result takes the place of its C
-    constexpr int kHeld = kReadsOf<EPI> == 0 ? 1 : kFinal ? 32 : 16;
-    uint32_t chi[kHeld], clo[kHeld];
-    if constexpr (kFinal) {
-        read_half(buf, lane, 0, chi);
-        read_half(buf, lane, 1, chi + 16);
-        read_half(buf + kPiece, lane, 0, clo);
-        read_half(buf + kPiece, lane, 1, clo + 16);
-        __syncwarp();
-    }
-    const float *d = p.dvec + (int64_t)x.b * g.d_stride;
+    uint32_t chi[kHasC<EPI> ? 16 : 1], clo[MODE == kCHigh ? 1 : 16];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         uint32_t acc[32];
         tmem_load32(acc_addr + h * 32, acc);
-        if constexpr (kReadsOf<EPI> > 0 && !kFinal)
+        if constexpr (kHasC<EPI>)
             read_half(buf, lane, h, chi);
-        if constexpr (kReadsOf<EPI> > 1 && !kFinal) {
-            if (p.c.lo) {
-                read_half(buf + kPiece, lane, h, clo);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    clo[e] = 0;
-            }
-        }
+        if constexpr (MODE != kCHigh)
+            read_half(buf + kPiece, lane, h, clo);
         tmem_wait_load();
-        constexpr int kAt = kFinal ? 16 : 0;
         float v[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e)
-            v[e] = __uint_as_float(acc[e]) * p.alpha;
-        // the lane's diagonal element, if it lies among these columns
-        const int on_diag = gi - gj - 32 * h;
-        const bool has_diag = (EPI == kEpiPoly || EPI == kEpiSym) && (unsigned)on_diag < 32u;
-
-        if constexpr (EPI == kEpiPoly) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float2 f = unpack_half2(chi[e]);
-                v[2 * e] = fmaf(p.c_scale, f.x, v[2 * e]);
-                v[2 * e + 1] = fmaf(p.c_scale, f.y, v[2 * e + 1]);
-            }
-        }
-        if constexpr (kReadsOf<EPI> > 1) {
-            const bool two = EPI == kEpiSym && p.dvec2 != nullptr;
-            const float *by_col = two ? p.dvec2 + (int64_t)x.b * g.d_stride : d;
-            const float col_scale = two ? p.c_scale2 : p.c_scale;
+            v[e] = __uint_as_float(acc[e]) * k.alpha;
+        if constexpr (kHasC<EPI>) {
 #pragma unroll
             for (int e4 = 0; e4 < 8; ++e4) {
-                float kh[4] = {d_row, d_row, d_row, d_row}, kl[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    kl[e] = d_row * (1.0f / kLoScale);
-                if (two || g.d_by_col) {
-                    const float4 w = *reinterpret_cast<const float4 *>(by_col + gj + 32 * h + 4 * e4);
-                    kl[0] = w.x * col_scale, kl[1] = w.y * col_scale, kl[2] = w.z * col_scale, kl[3] = w.w * col_scale;
-                    if (!two) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            kh[e] = kl[e];
-                            kl[e] *= 1.0f / kLoScale;
-                        }
-                    }
+                float col[4];
+                if constexpr (MODE == kCTwo || MODE == kCCol) {
+                    const float4 w = load_here(k.d_col + gj + 32 * h + 4 * e4);
+                    col[0] = w.x * k.col_scale, col[1] = w.y * k.col_scale, col[2] = w.z * k.col_scale, col[3] = w.w * k.col_scale;
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float2 f = unpack_half2(chi[h * kAt + 2 * e4 + e]), l = unpack_half2(clo[h * kAt + 2 * e4 + e]);
+                    const float2 f = unpack_half2(chi[2 * e4 + e]);
                     float *y = v + 4 * e4 + 2 * e;
-                    y[0] = fmaf(kh[2 * e], f.x, fmaf(kl[2 * e], l.x, y[0]));
-                    y[1] = fmaf(kh[2 * e + 1], f.y, fmaf(kl[2 * e + 1], l.y, y[1]));
+                    if constexpr (MODE == kCHigh) {
+                        y[0] = fmaf(k.d_row, f.x, y[0]);
+                        y[1] = fmaf(k.d_row, f.y, y[1]);
+                    } else {
+                        const float2 l = unpack_half2(clo[2 * e4 + e]);
+                        if constexpr (MODE == kCTwo) {
+                            y[0] = fmaf(k.d_row, f.x, fmaf(col[2 * e], l.x, y[0]));
+                            y[1] = fmaf(k.d_row, f.y, fmaf(col[2 * e + 1], l.y, y[1]));
+                        } else {
+                            const float d0 = MODE == kCCol ? col[2 * e] : k.d_row, d1 = MODE == kCCol ? col[2 * e + 1] : k.d_row;
+                            y[0] = fmaf(d0, fmaf(l.x, 1.0f / kLoScale, f.x), y[0]);
+                            y[1] = fmaf(d1, fmaf(l.y, 1.0f / kLoScale, f.y), y[1]);
+                        }
+                    }
                 }
             }
-            if (two && has_diag) {
-                const float dd = d[gi] * by_col[gi];
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (e == on_diag)
-                        v[e] += dd;
-            }
         }
-
         if constexpr (EPI == kEpiPoly || EPI == kEpiSym) {
-            if (has_diag && (EPI == kEpiPoly || p.diag_out)) {
+            // the lane's diagonal element, if it lies among these columns
+            const int on_diag = gi - gj - 32 * h;
+            if ((MODE == kCTwo || k.d_out) && (unsigned)on_diag < 32u) {
                 float dd = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
                     if (e == on_diag) {
-                        dd = v[e];
-                        v[e] = 0.0f;
+                        dd = v[e] + k.eye;
+                        v[e] = k.d_out ? 0.0f : dd;
                     }
                 }
-                p.dvec_out[(int64_t)x.b * g.d_stride + gi] = EPI == kEpiPoly ? dd + g.coef_a : dd;
+                if (k.d_out)
+                    k.d_out[gi] = dd;
             }
         }
-        if constexpr (!kFinal) {
-            if (EPI == kEpiPoly || p.out.lo == nullptr)
-                put_hi(buf, lane, h, v, p.s_out);
-            else
-                put_pair(buf, buf + kPiece, lane, h, v, p.s_out);
-        } else {
-            // FP32 through the buffer, so that the warp writes along the rows
-            const uint32_t half = buf + h * kPiece;
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                sts128(half + lane * 128 + ((q ^ (lane & 7)) << 4),
-                       make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
-                                  __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3])));
-            __syncwarp();
-            const int col = gj + 32 * h + lane;
-            const int row0 = ib * 128 + (row & ~31);
-            const int lim = min(32, plan.rows - row0);
-            constexpr int kAtOnce = 16;  // rows whose loads are in flight together
-            if (col < plan.cols) {
-                const int64_t next = EPI == kEpiMuon ? plan.cols : plan.w_row;
-                const int64_t at0 = EPI == kEpiMuon ? ((int64_t)x.b * plan.rows + row0) * plan.cols + col
-                                                    : (int64_t)x.b * plan.w_batch + (int64_t)row0 * plan.w_row + col;
-                float *th = EPI == kEpiMuon ? plan.theta + at0 : nullptr;
-                uint16_t *w = plan.w + at0;
-#pragma unroll
-                for (int r0 = 0; r0 < 32; r0 += kAtOnce) {
-                    float old[kAtOnce];
-                    if constexpr (EPI == kEpiMuon) {
-#pragma unroll
-                        for (int r = 0; r < kAtOnce; ++r)
-                            old[r] = r0 + r < lim ? __ldcs(th + (r0 + r) * next) : 0.0f;
-                    }
-#pragma unroll
-                    for (int r = 0; r < kAtOnce; ++r) {
-                        float o = lds32(half + (r0 + r) * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
-                        if (r0 + r < lim) {
-                            if constexpr (EPI == kEpiMuon) {
-                                o = __fsub_rn(__fmul_rn(old[r], plan.decay), __fmul_rn(plan.step, o));
-                                __stcs(th + (r0 + r) * next, o);
-                            }
-                            w[(r0 + r) * next] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
-                        }
-                    }
-                }
-            }
-        }
+        // each half's result takes the place of its C
+        if constexpr (EPI == kEpiOut)
+            put_bf16(buf, lane, h, v);
+        else if constexpr (EPI == kEpiMuon)
+            put_hi(buf, lane, h, v, kMuonScale);
+        else if (k.out_lo)
+            put_pair(buf, lane, h, v, k.s_out);
+        else
+            put_hi(buf, lane, h, v, k.s_out);
+    }
+    if constexpr (EPI == kEpiOut || EPI == kEpiMuon) {
+        __syncwarp();
+        write_rows<EPI>(plan, b, gi & ~31, gj, lane, buf);
     }
     fence_async_shared();  // results leave the buffer, or the next C comes into it, by the copy engine
     __syncwarp();
-    if constexpr (!kFinal) {
-        const int64_t piece = (int64_t)x.b * g.out_stride + ((int64_t)ib * g.out_c64 + 2 * jb + (c & 1)) * kTileElems +
-                              (row & ~31) * 64;
+    if constexpr (EPI != kEpiOut && EPI != kEpiMuon) {
         if (elect_one()) {
-            bulk_store(p.out.hi + piece, buf, kPiece);
-            if (EPI != kEpiPoly && p.out.lo)
-                bulk_store(p.out.lo + piece, buf + kPiece, kPiece);
+            bulk_store(k.out_hi + at, buf, kPiece);
+            if (k.out_lo)
+                bulk_store(k.out_lo + at, buf + kPiece, kPiece);
             bulk_commit();
         }
         __syncwarp();
@@ -363,22 +425,6 @@ __device__ __forceinline__ void prefetch_theta(const OrthoPlan &plan, const Tile
     if (n > 32)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(p + 32));
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p + n - 1));
-}
-
-// Copy the C of chunk c into a buffer.
-template <int CG, int EPI>
-__device__ __forceinline__ void prefetch_chunk(const OrthoGemm &g, const Tile &x, int ib, int c, int quad, uint32_t buf,
-                                               uint32_t bar)
-{
-    const OrthoProduct &p = g.p[x.prob];
-    const int jb = x.j * CG + (c >> 1);
-    const int64_t piece = (int64_t)x.b * g.out_stride + ((int64_t)ib * g.out_c64 + 2 * jb + (c & 1)) * kTileElems +
-                          quad * 32 * 64;
-    const bool lo = kReadsOf<EPI> > 1 && p.c.lo;
-    mbar_expect_tx(bar, lo ? 2 * kPiece : kPiece);
-    bulk_load(buf, p.c.hi + piece, kPiece, bar);
-    if (lo)
-        bulk_load(buf + kPiece, p.c.lo + piece, kPiece, bar);
 }
 
 // Shared state of a CTA, besides the operand ring and the epilogue's buffers.
@@ -403,49 +449,95 @@ __device__ __forceinline__ bool epilogue_tiles(const OrthoPlan &plan, const Orth
         const Tile x = decode<CG>(g, plan.batch, t);
         const OrthoProduct &p = g.p[x.prob];
         const uint32_t buf = n & 1, use = n >> 1;
-        const int ib = x.i * CG + rank;
+        const int ib = x.i * CG + rank, gi = ib * 128 + row;
         // the chunks of the tile that exist (and, of a symmetric result, are
         // kept): c0 and c0 + 2
         const int c0 = (g.sym ? max(0, 2 * (ib - x.j * CG)) : 0) + half;
         const int c1 = ib < g.mblk ? min(2 * CG, 2 * (g.nblk - x.j * CG)) : 0;
+        const bool has_lo = kHasC<EPI> && EPI != kEpiPoly && p.c.lo != nullptr;
         // both chunks fit side by side if they have no low halves
-        const bool both = EPI == kEpiPoly || (EPI == kEpiSym && !p.c.lo && !p.out.lo);
+        const bool both = EPI == kEpiPoly || (EPI == kEpiSym && !has_lo && !p.out.lo);
+        auto place = [&](int c) {  // of this warp's piece of chunk c
+            return (int64_t)x.b * g.out_stride + ((int64_t)ib * g.out_c64 + 2 * x.j * CG + c) * kTileElems + quad * 32 * 64;
+        };
         auto fetch = [&](int c, int i) {  // into buffer i
             if (elect_one()) {
                 bulk_wait_read<0>();  // of the stores out of it
-                if constexpr (kReadsOf<EPI> > 0)
-                    prefetch_chunk<CG, EPI>(g, x, ib, c, quad, mine + i * kPiece, smem_addr(&sh.c[warp][i]));
+                if constexpr (kHasC<EPI>) {
+                    const uint32_t bar = smem_addr(&sh.c[warp][i]);
+                    mbar_expect_tx(bar, has_lo ? 2 * kPiece : kPiece);
+                    bulk_load(mine + i * kPiece, p.c.hi + place(c), kPiece, bar);
+                    if (has_lo)
+                        bulk_load(mine + kPiece, p.c.lo + place(c), kPiece, bar);
+                }
             }
             __syncwarp();
-            if constexpr (kReadsOf<EPI> > 0)
+            if constexpr (kHasC<EPI>)
                 ++asked[i];
         };
         if (c0 < c1)
             fetch(c0, 0);
         if (both && c0 + 2 < c1)
             fetch(c0 + 2, 1);
-        float d_row = 0.0f;
-        if constexpr (kReadsOf<EPI> > 1) {
-            const float *d = p.dvec + (int64_t)x.b * g.d_stride, *cols = p.dvec2 ? p.dvec2 + (int64_t)x.b * g.d_stride : d;
-            if (!g.d_by_col && c0 < c1)
-                d_row = d[ib * 128 + row] * p.c_scale;
-            if ((g.d_by_col || p.dvec2) && lane < 2)  // the factors of the columns, on their way
-                for (int c = c0; c < c1; c += 2)
-                    asm volatile("prefetch.global.L1 [%0];" ::"l"(cols + (x.j * CG + (c >> 1)) * 128 + (c & 1) * 64 + lane * 32));
+        Local k;
+        k.alpha = p.alpha;
+        k.s_out = p.s_out;
+        k.out_hi = p.out.hi;
+        k.out_lo = p.out.lo;
+        k.c_scale = p.c_scale;
+        k.d_row = p.c_scale;
+        k.eye = EPI == kEpiPoly ? g.coef_a : 0.0f;
+        k.col_scale = p.c_scale;
+        k.d_col = nullptr;
+        const bool two = EPI == kEpiSym && p.dvec2 != nullptr;
+        const int64_t d_at = (int64_t)x.b * g.d_stride;
+        k.d_out = (EPI == kEpiPoly || (EPI == kEpiSym && p.diag_out)) ? p.dvec_out + d_at : nullptr;
+        if constexpr (kHasC<EPI> && EPI != kEpiPoly) {
+            if (c0 < c1) {
+                if (g.d_by_col) {
+                    k.d_col = p.dvec + d_at;
+                } else {
+                    const float d = p.dvec[d_at + gi];
+                    k.d_row = d * p.c_scale;
+                    if (two) {
+                        k.d_col = p.dvec2 + d_at;
+                        k.col_scale = p.c_scale2;
+                        k.eye = d * k.d_col[gi];
+                    }
+                }
+                if (k.d_col && lane < 2)  // the factors of the columns, on their way
+                    for (int c = c0; c < c1; c += 2)
+                        asm volatile("prefetch.global.L1 [%0];" ::"l"(k.d_col + x.j * CG * 128 + c * 64 + lane * 32));
+            }
         }
         if constexpr (EPI == kEpiMuon)
             for (int c = c0; c < c1; c += 2)
-                prefetch_theta(plan, x, ib * 128 + quad * 32, (x.j * CG + (c >> 1)) * 128 + (c & 1) * 64, lane);
+                prefetch_theta(plan, x, ib * 128 + quad * 32, x.j * CG * 128 + c * 64, lane);
         bool ok = __all_sync(kFullMask, mbar_wait(smem_addr(&sh.acc_full[buf]), use & 1, &sh.abort));
         tmem_fence_after();
         for (int c = c0; c < c1 && ok; c += 2) {
             const int i = both && c != c0;
-            if constexpr (kReadsOf<EPI> > 0)
+            if constexpr (kHasC<EPI>)
                 ok = __all_sync(kFullMask, mbar_wait(smem_addr(&sh.c[warp][i]), (asked[i] - 1) & 1, &sh.abort));
             if (!ok)
                 break;
-            epilogue_chunk<CG, EPI>(plan, g, x, ib, c, row, lane,
-                                    tmem + ((uint32_t)(quad * 32) << 16) + buf * 128 * CG + c * 64, mine + i * kPiece, d_row);
+            const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + buf * 128 * CG + c * 64;
+            const int gj = x.j * CG * 128 + c * 64;
+            if constexpr (EPI == kEpiGram || EPI == kEpiPoly) {
+                epilogue_chunk<EPI, kCHigh>(plan, k, x.b, gi, gj, lane, acc, mine + i * kPiece, place(c));
+            } else if constexpr (EPI == kEpiSym) {
+                if (two)
+                    epilogue_chunk<EPI, kCTwo>(plan, k, x.b, gi, gj, lane, acc, mine + i * kPiece, place(c));
+                else if (has_lo)
+                    epilogue_chunk<EPI, kCRow>(plan, k, x.b, gi, gj, lane, acc, mine + i * kPiece, place(c));
+                else
+                    epilogue_chunk<EPI, kCHigh>(plan, k, x.b, gi, gj, lane, acc, mine + i * kPiece, place(c));
+            } else {
+                if (g.d_by_col)
+                    epilogue_chunk<EPI, kCCol>(plan, k, x.b, gi, gj, lane, acc, mine + i * kPiece, place(c));
+                else
+                    epilogue_chunk<EPI, kCRow>(plan, k, x.b, gi, gj, lane, acc, mine + i * kPiece, place(c));
+            }
             if (!both && c + 2 < c1)
                 fetch(c + 2, 0);
         }

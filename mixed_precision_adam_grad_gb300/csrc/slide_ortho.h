@@ -80,6 +80,7 @@ struct OrthoPlan {
     int rows, cols;
     uint16_t *w;
     int64_t w_row, w_batch;  // strides in elements
+    int vec;                 // rows of w (and theta) can be written eight values at a time
     float *theta;            // contiguous
     float decay, step;
     int test_stall;
