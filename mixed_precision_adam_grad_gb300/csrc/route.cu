@@ -7,7 +7,7 @@
 // lane l holds the NV = 2, 4, 8, 16 or 32 consecutive experts from l*NV on, in
 // registers, so a row is read once.  Every choice is
 // made on 32-bit keys whose unsigned order is the order of the FP32 values
-// (0 = not available).  Each lane sorts its keys once, in runs of at most
+// (those up to the key of -inf: not available).  Each lane sorts its keys once, in runs of at most
 // eight, so that a pick is one maximum of the runs' heads over the token's lanes, a ballot
 // and a shift in the lane that held it; the lowest lane holding the maximum
 // has the lowest expert, which decides ties.  Which experts they were is
@@ -196,28 +196,28 @@ __device__ __forceinline__ uint32_t head(const Runs<NV> &r)
     return m;
 }
 
-// Takes the head m off one run that has it.
+// If `here`, takes the head m off one run that has it.
 template <int NV>
-__device__ __forceinline__ void pop(Runs<NV> &r, uint32_t m)
+__device__ __forceinline__ void pop(Runs<NV> &r, uint32_t m, bool here)
 {
     constexpr int R = Runs<NV>::R, L = Runs<NV>::L;
-    bool done = false;
 #pragma unroll
     for (int l = 0; l < L; ++l) {
-        if (!done && (L == 1 || r.key[l][0] == m)) {
-            done = true;
+        const bool this_one = here && (L == 1 || r.key[l][0] == m);
+        here = here && !this_one;
 #pragma unroll
-            for (int i = 0; i + 1 < R; ++i)
-                r.key[l][i] = r.key[l][i + 1];
-            r.key[l][R - 1] = 0;
-        }
+        for (int i = 0; i + 1 < R; ++i)
+            r.key[l][i] = this_one ? r.key[l][i + 1] : r.key[l][i];
+        r.key[l][R - 1] = this_one ? 0 : r.key[l][R - 1];
     }
 }
 
-// Rank of a group from its best two keys (0 = none).
+// Rank of a group from its best two keys; 0: it has none.
 __device__ __forceinline__ uint32_t group_rank(uint32_t k1, uint32_t k2, bool only_max)
 {
-    if (k1 == 0 || k2 == 0 || only_max)
+    if (k1 <= kKeyNone)
+        return 0;
+    if (k2 <= kKeyNone || only_max)
         return k1;
     return key_of(__fadd_rn(value_of(k1), value_of(k2)));
 }
@@ -411,10 +411,6 @@ __global__ void __launch_bounds__((ANY ? kAnyWarps : kWarps) * 32) k_route(const
                 }
             }
         }
-        // keys up to that of -inf are none; a NaN's is above every number's
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            key[i] = key[i] <= kKeyNone ? 0 : key[i];
         if constexpr (ANY) {
             uint32_t *mine = words + warp * (a.E + a.groups);
             keep_groups<NV>(key, a, lane, mine, mine + a.E);
@@ -425,35 +421,41 @@ __global__ void __launch_bounds__((ANY ? kAnyWarps : kWarps) * 32) k_route(const
         nan = token_ballot<LPT>(nan || mine > kKeyInf, lane) != 0;
         const bool kept = !by_lane || lane_kept<LPT, NV>(runs, a, lane);
         mine = kept ? mine : 0;
-        uint32_t my_key = 0;           // lane p: pick p's key, its owner and
-        int my_owner = 0, my_nth = 0;  // which of the owner's equal keys it is
-        uint32_t last = 0;
-        int last_owner = 0, nth = 0;
+        uint32_t my_key = 0;  // lane p: pick p's key and its owner
+        int my_owner = 0;
         for (int p = 0; p < a.K; ++p) {
             const uint32_t m = token_max<LPT>(mine);
             const int owner = __ffs(token_ballot<LPT>(mine == m, lane)) - 1;
-            nth = m == last && owner == last_owner ? nth + 1 : 0;
-            last = m;
-            last_owner = owner;
-            if (my == p) {
-                my_key = m;
-                my_owner = owner;
-                my_nth = nth;
-            }
-            if (my == owner) {
-                pop<NV>(runs, m);
-                mine = kept ? head<NV>(runs) : 0;
-            }
+            my_key = my == p ? m : my_key;
+            my_owner = my == p ? owner : my_owner;
+            pop<NV>(runs, m, my == owner);
+            mine = kept ? head<NV>(runs) : 0;
         }
         int best = -1;  // lane p: the expert of pick p
         const int from = (lane & ~(LPT - 1)) + my_owner;
+        // equal keys of one lane are picked one after the other
+        const bool same_key = __shfl_up_sync(kFull, my_key, 1) == my_key;
+        const bool same_owner = __shfl_up_sync(kFull, my_owner, 1) == my_owner;
+        const bool again = my > 0 && my < a.K && same_key && same_owner;
+        if (!__any_sync(kFull, again)) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const bool is = __shfl_sync(kFull, key[i], from) == my_key;
-            best = is && my_nth == 0 && best < 0 ? my_owner * NV + i : best;
-            my_nth -= is;
+            for (int i = NV - 1; i >= 0; --i)
+                best = __shfl_sync(kFull, key[i], from) == my_key ? i : best;
+        } else {
+            int nth = 0;  // which of the owner's equal keys it is
+            for (int p = 1; p < a.K; ++p) {
+                const int before = __shfl_up_sync(kFull, nth, 1);
+                nth = my == p ? (again ? before + 1 : 0) : nth;
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const bool is = __shfl_sync(kFull, key[i], from) == my_key;
+                best = is && nth == 0 ? i : best;
+                nth -= is;
+            }
         }
-        best = my_key == 0 || nan || !live ? -1 : best;
+        best += my_owner * NV;
+        best = my_key <= kKeyNone || nan || !live ? -1 : best;
         float score = 0.0f;
         if (best >= 0) {
             const float y = widen(row[best]);
