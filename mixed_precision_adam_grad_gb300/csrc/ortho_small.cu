@@ -220,25 +220,33 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
     const uint32_t idesc = idesc_of(n16, a.tall, a.tall, true);
     const int mchunks = (a.m + 7) / 8;  // chunks along the short side (tall)
 
-    for (int k = k0; k < k1; ++k) {
-        const int it = k - k0, s = it % kGramStages;
-        // chunk i of the step: wide: row i >> 3, columns 8*(i & 7); tall: row i >> 4, columns 8*(i & 15)
-        float v[4][8];
-        int place[4];
+    // chunk i of a step: wide: row i >> 3, columns 8*(i & 7); tall: row i >> 4, columns 8*(i & 15)
+    float v[4][8];
+    int place[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int i = tid + j * kThreads;
+        if (a.tall) {
+            const int r = i >> 4, c = i & 15;
+            place[j] = c < ((mchunks + 7) & ~7) ? (c >> 3) * (kTile / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4) : -1;
+        } else {
+            const int r = i >> 3, c = i & 7;
+            place[j] = r * 128 + ((c ^ (r & 7)) << 4);
+        }
+    }
+    auto load_step = [&](int k) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int i = tid + j * kThreads;
-            if (a.tall) {
-                const int r = i >> 4, c = i & 15;
-                place[j] = c < ((mchunks + 7) & ~7) ? (c >> 3) * (kTile / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4) : -1;
-                if (place[j] >= 0)
-                    load_chunk<T, MUON>(a, b, k * 64 + r, c * 8, v[j]);
-            } else {
-                const int r = i >> 3, c = i & 7;
-                place[j] = r * 128 + ((c ^ (r & 7)) << 4);
-                load_chunk<T, MUON>(a, b, r, k * 64 + c * 8, v[j]);
-            }
+            if (place[j] >= 0)
+                load_chunk<T, MUON>(a, b, a.tall ? k * 64 + (i >> 4) : i >> 3, a.tall ? (i & 15) * 8 : k * 64 + (i & 7) * 8,
+                                    v[j]);
         }
+    };
+    if (k0 < k1)
+        load_step(k0);
+    for (int k = k0; k < k1; ++k) {
+        const int it = k - k0, s = it % kGramStages;
         if (it >= kGramStages)
             wait_products(sh, s, (it / kGramStages - 1) & 1, a.status);
         const uint32_t stage = ring + s * kStage;
@@ -252,6 +260,8 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
             if constexpr (kPair)
                 sts128(stage + kTile + place[j], lo);
         }
+        if (k + 1 < k1)
+            load_step(k + 1);
         fence_async_shared();
         __syncthreads();
         if (warp == 0 && elect_one() && !a.test_stall) {
@@ -552,8 +562,8 @@ __global__ void __launch_bounds__(512) k_small_poly(const __grid_constant__ Smal
 // A CTA takes stretches of 128 of the long side in turn.  Shared memory: Q
 // (pair), X (pair), both only as many 64-column tiles (Q) and rows or tiles (X)
 // as m needs; the result goes through X's place as FP32.
-template <typename T, bool MUON>
-__global__ void __launch_bounds__(kThreads) k_small_apply(const __grid_constant__ SmallOrtho a)
+template <typename T, bool MUON, int TILES>
+__global__ void __launch_bounds__(kThreads, TILES == 1 ? 3 : 1) k_small_apply(const __grid_constant__ SmallOrtho a)
 {
     extern __shared__ uint8_t smem_raw[];
     __shared__ Base sh;
@@ -561,7 +571,7 @@ __global__ void __launch_bounds__(kThreads) k_small_apply(const __grid_constant_
     const uint32_t tmem = set_up(sh, 128);
     const int tid = threadIdx.x, warp = warp_number(), lane = tid & 31, b = blockIdx.y;
     const uint32_t n16 = (uint32_t)((a.m + 15) & ~15), k16 = n16 / 16;
-    const int tiles = n16 > 64 ? 2 : 1;        // 64-column tiles along the short side
+    constexpr int tiles = TILES;               // 64-column tiles along the short side
     const uint32_t q_lo = tiles * kTile;       // Q: tiles of hi, then tiles of lo
     // X: tall: 128 rows x m, tiles along m; wide: m rows x 128, two tiles of 64*tiles rows
     const uint32_t X = base + 2 * q_lo, x_lo = tiles * kTile, x_tile = a.tall ? kTile : tiles * (kTile / 2);
@@ -583,43 +593,46 @@ __global__ void __launch_bounds__(kThreads) k_small_apply(const __grid_constant_
     }
     const int n_side = a.tall ? a.rows : a.cols;
     uint32_t phase = 0;
-    for (int s0 = blockIdx.x * 128; s0 < n_side && !sh.abort; s0 += gridDim.x * 128, ++phase) {
-        // tall: 128 rows of 8*tiles chunks; wide: 64*tiles rows of 16 chunks
-        for (int i = tid; i < tiles * 1024; i += kThreads) {
-            float v[8];
-            uint32_t place;
-            int row, col;
-            if (a.tall) {
-                const int r = tiles == 2 ? i >> 4 : i >> 3, c = i & (8 * tiles - 1);
-                row = s0 + r;
-                col = c * 8;
-                place = (c >> 3) * kTile + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-            } else {
-                const int r = i >> 4, c = i & 15;
-                row = r;
-                col = s0 + c * 8;
-                place = (c >> 3) * x_tile + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-            }
+    // tall: 128 rows of 8*tiles chunks; wide: 64*tiles rows of 16 chunks
+    float v[4 * tiles][8];
+    auto load_stretch = [&](int s0) {
+#pragma unroll
+        for (int j = 0; j < 4 * tiles; ++j) {
+            const int i = tid + j * kThreads;
+            const int row = a.tall ? s0 + (tiles == 2 ? i >> 4 : i >> 3) : i >> 4;
+            const int col = a.tall ? (i & (8 * tiles - 1)) * 8 : s0 + (i & 15) * 8;
             const int n = a.cols - col;
             if (row < a.rows && n > 0) {
                 const int64_t at = (int64_t)b * a.batch_stride + (int64_t)row * a.row_stride + col;
                 if constexpr (MUON)
-                    load8<float>(a.u, at, n, a.vec, v);
+                    load8<float>(a.u, at, n, a.vec, v[j]);
                 else
-                    load8<T>(a.g.p[0], at, n, a.vec, v);
+                    load8<T>(a.g.p[0], at, n, a.vec, v[j]);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    v[e] = 0.0f;
+                    v[j][e] = 0.0f;
             }
+        }
+    };
+    load_stretch(blockIdx.x * 128);
+    for (int s0 = blockIdx.x * 128; s0 < n_side && !sh.abort; s0 += gridDim.x * 128, ++phase) {
+#pragma unroll
+        for (int j = 0; j < 4 * tiles; ++j) {
+            const int i = tid + j * kThreads;
+            const int r = a.tall ? (tiles == 2 ? i >> 4 : i >> 3) : i >> 4, c = a.tall ? i & (8 * tiles - 1) : i & 15;
+            const uint32_t place = (c >> 3) * x_tile + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+            float x[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                v[e] *= inv;
+                x[e] = v[j][e] * inv;
             uint4 hi, lo;
-            split8<false>(v, hi, lo);
+            split8<false>(x, hi, lo);
             sts128(X + place, hi);
             sts128(X + x_lo + place, lo);
         }
+        if (s0 + (int)gridDim.x * 128 < n_side)
+            load_stretch(s0 + gridDim.x * 128);
         fence_async_shared();
         __syncthreads();
         if (warp == 0 && elect_one() && !a.test_stall) {
@@ -762,11 +775,11 @@ cudaError_t launch_kernel(Kernel k, dim3 grid, int threads, int smem, bool behin
 template <typename T, bool MUON>
 cudaError_t launch_all(SmallOrtho &a, int device, int sms, cudaStream_t stream)
 {
-    static std::atomic<int> ready[kMaxDevices][3];
+    static std::atomic<int> ready[kMaxDevices][4];
     const int n_side = a.tall ? a.rows : a.cols;
-    // a cluster of eight CTAs per 8 x 4 steps of 64, while that leaves no SM idle
+    // a cluster of eight CTAs per 8 x 4 steps of 64, as long as all are resident (two a SM)
     const int steps = (n_side + 63) / 64;
-    const int fit = sms / (kCluster * a.batch);
+    const int fit = 2 * sms / (kCluster * a.batch);
     int parts = (steps + 4 * kCluster - 1) / (4 * kCluster);
     parts = parts < fit ? parts : fit;
     parts = parts < 1 ? 1 : parts > kSmallMaxParts ? kSmallMaxParts : parts;
@@ -781,10 +794,11 @@ cudaError_t launch_all(SmallOrtho &a, int device, int sms, cudaStream_t stream)
         return e;
     const int tiles = a.m > 64 ? 2 : 1;
     const int64_t stretches = (n_side + 127) / 128;
-    const int64_t room = (int64_t)sms * (tiles == 2 ? 1 : 3);
-    const int64_t per = (room + a.batch - 1) / a.batch;
-    return launch_kernel(k_small_apply<T, MUON>, dim3((unsigned)(stretches < per ? stretches : per), a.batch),
-                         kThreads, 1024 + 4 * tiles * kTile, true, a, stream, ready[device][2]);
+    const int64_t room = (int64_t)sms * (tiles == 2 ? 1 : 3) / a.batch;  // what is resident at once
+    const dim3 grid((unsigned)(stretches < room ? stretches : room > 0 ? room : 1), a.batch);
+    const int smem = 1024 + 4 * tiles * kTile;
+    return tiles == 2 ? launch_kernel(k_small_apply<T, MUON, 2>, grid, kThreads, smem, true, a, stream, ready[device][2])
+                      : launch_kernel(k_small_apply<T, MUON, 1>, grid, kThreads, smem, true, a, stream, ready[device][3]);
 }
 
 }  // namespace
