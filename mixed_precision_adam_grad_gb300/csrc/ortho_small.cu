@@ -336,47 +336,77 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
 
 // ---- 2: the polynomial ------------------------------------------------------------
 
-// acc (+)= A * B over three terms of pairs (hi, lo 32 KiB apart), all K-major
-// tiles of 128 x 64 (the factors are symmetric).
-__device__ __forceinline__ void issue_pair(uint32_t tmem, uint32_t a, uint32_t b, uint32_t k16, uint32_t idesc)
+// A symmetric m x m pair in shared memory, K-major tiles of 128 rows x 64
+// columns.  TILES = 2 (m > 64): two tiles of hi, two of lo.  TILES = 1: one
+// tile, hi in rows 0..63 and lo in rows 64..127, so that one instruction
+// multiplies a factor by both.
+template <int TILES>
+__device__ __forceinline__ uint32_t pair_at(uint32_t m, int row, int chunk, bool lo)
 {
+    if constexpr (TILES == 1)
+        row += lo ? 64 : 0;
+    else
+        m += (chunk >> 3) * kTile + (lo ? 2 * kTile : 0);
+    return m + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+}
+
+// acc = A * B of pairs, without lo * lo.  TILES = 2: hi*hi + hi*lo + lo*hi in
+// columns 0..n16-1.  TILES = 1: hi*hi + lo*hi there and hi*lo from column 64 on,
+// eight instructions instead of twelve; each takes about 80 cycles whatever
+// its size.
+template <int TILES>
+__device__ __forceinline__ void issue_pair(uint32_t tmem, uint32_t a, uint32_t b, uint32_t n16)
+{
+    const uint32_t k16 = n16 / 16;
+    if constexpr (TILES == 1) {
+        const uint64_t da = operand_desc(a, 16), db = operand_desc(b, 16);
+        const uint32_t both = idesc_of(64 + n16, false, false, false), one = idesc_of(n16, false, false, false);
 #pragma unroll
-    for (int term = 0; term < 3; ++term) {
-        const uint64_t da = operand_desc(a + (term == 2 ? 2 * kTile : 0), 16);
-        const uint64_t db = operand_desc(b + (term == 1 ? 2 * kTile : 0), 16);
-#pragma unroll
-        for (uint32_t j = 0; j < 8; ++j) {
-            constexpr uint32_t kStep = 32;
-            const uint32_t off = ((j >> 2) * kTile + (j & 3) * kStep) >> 4;
+        for (uint32_t j = 0; j < 4; ++j)
             if (j < k16)
-                mma_f16<1>(tmem, da + off, db + off, idesc, term > 0 || j > 0);
+                mma_f16<1>(tmem, da + j * 2, db + j * 2, both, j > 0);
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j)
+            if (j < k16)
+                mma_f16<1>(tmem, da + (64 * 128 >> 4) + j * 2, db + j * 2, one, true);
+    } else {
+        const uint32_t idesc = idesc_of(n16, false, false, false);
+#pragma unroll
+        for (int term = 0; term < 3; ++term) {
+            const uint64_t da = operand_desc(a + (term == 2 ? 2 * kTile : 0), 16);
+            const uint64_t db = operand_desc(b + (term == 1 ? 2 * kTile : 0), 16);
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) {
+                const uint32_t off = ((j >> 2) * kTile + (j & 3) * 32) >> 4;
+                if (j < k16)
+                    mma_f16<1>(tmem, da + off, db + off, idesc, term > 0 || j > 0);
+            }
         }
     }
 }
 
 // Row `row`, columns 32*block.. of a pair, from 32 values.
+template <int TILES>
 __device__ __forceinline__ void put_pair(uint32_t m, int row, int block, const float (&v)[32])
 {
-    const uint32_t tile = m + (block >> 1) * kTile + row * 128;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         const float x[8] = {v[8 * q], v[8 * q + 1], v[8 * q + 2], v[8 * q + 3],
                             v[8 * q + 4], v[8 * q + 5], v[8 * q + 6], v[8 * q + 7]};
         uint4 hi, lo;
         split8<false>(x, hi, lo);
-        const uint32_t at = tile + (((4 * (block & 1) + q) ^ (row & 7)) << 4);
-        sts128(at, hi);
-        sts128(at + 2 * kTile, lo);
+        sts128(pair_at<TILES>(m, row, 4 * block + q, false), hi);
+        sts128(pair_at<TILES>(m, row, 4 * block + q, true), lo);
     }
 }
 
+template <int TILES>
 __device__ __forceinline__ void get_pair(uint32_t m, int row, int block, float (&v)[32])
 {
-    const uint32_t tile = m + (block >> 1) * kTile + row * 128;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        const uint32_t at = tile + (((4 * (block & 1) + q) ^ (row & 7)) << 4);
-        const uint4 hi = lds128(at), lo = lds128(at + 2 * kTile);
+        const uint4 hi = lds128(pair_at<TILES>(m, row, 4 * block + q, false));
+        const uint4 lo = lds128(pair_at<TILES>(m, row, 4 * block + q, true));
         const uint32_t u[4] = {hi.x, hi.y, hi.z, hi.w}, w[4] = {lo.x, lo.y, lo.z, lo.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -388,26 +418,58 @@ __device__ __forceinline__ void get_pair(uint32_t m, int row, int block, float (
     }
 }
 
-constexpr int kPairBytes = 4 * kTile;                 // hi and lo of a 128 x 128 matrix
-constexpr int kPolySmem = 1024 + 3 * kPairBytes;
+// The lane's 32 values of an accumulator.
+template <int TILES>
+__device__ __forceinline__ void read_acc(uint32_t at, float (&v)[32])
+{
+    uint32_t x[32];
+    tmem_load32(at, x);
+    if constexpr (TILES == 1) {
+        uint32_t y[32];
+        tmem_load32(at + 64, y);
+        tmem_wait_load();
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            v[e] = __uint_as_float(x[e]) + __uint_as_float(y[e]);
+    } else {
+        tmem_wait_load();
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            v[e] = __uint_as_float(x[e]);
+    }
+}
 
-// 128 threads per 32 columns.  Warp (quad, block) has rows 32*quad.. and columns
-// 32*block.. of every matrix; warps whose rows all lie beyond m rest.  Rows and columns beyond m
-// inside a used block are zero, those of unused blocks hold anything: they only
-// meet rows of results that nobody reads.
-__global__ void __launch_bounds__(512) k_small_poly(const __grid_constant__ SmallOrtho a)
+constexpr int kPairBytes = 4 * kTile;  // room of a pair, in shared memory and in a.q
+template <int TILES>
+constexpr int kPolyPair = TILES == 2 ? kPairBytes : 2 * kTile;  // with TILES = 1 an instruction reads 192 rows
+template <int TILES>
+constexpr int kPolySmem = 1024 + 3 * kPolyPair<TILES>;
+
+// 128 threads per 32 columns and a last warp that issues the products.  Warp
+// (quad, block) has rows 32*quad.. and columns 32*block.. of every matrix; warps
+// whose rows all lie beyond m rest.  Rows and columns beyond m inside a used
+// block are zero, those of unused blocks hold anything: they only meet rows of
+// results that nobody reads.
+//
+// A step is three products one after the other, G^2, T = R G and R T; Q <- R Q
+// runs behind the third and is taken up while the next step's first is under
+// way.
+template <int TILES>
+__global__ void __launch_bounds__(128 * 2 * TILES + 32) k_small_poly(const __grid_constant__ SmallOrtho a)
 {
     extern __shared__ uint8_t smem_raw[];
     __shared__ Base sh;
     __shared__ double s_trace[4];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-    const uint32_t G = base, R = base + kPairBytes, Q = base + 2 * kPairBytes;
+    const uint32_t G = base, R = base + kPolyPair<TILES>, Q = base + 2 * kPolyPair<TILES>;
     const uint32_t tmem = set_up(sh, 256);
     const int tid = threadIdx.x, warp = warp_number(), lane = tid & 31, b = blockIdx.x;
+    const int blocks = (int)blockDim.x / 128;  // of 32 columns
+    const bool issuer = warp == 4 * blocks;
     const int quad = warp & 3, block = warp >> 2, row = quad * 32 + lane;
-    const uint32_t n16 = (uint32_t)((a.m + 15) & ~15), k16 = n16 / 16, idesc = idesc_of(n16, false, false, false);
-    const uint32_t acc_at = tmem + ((uint32_t)(quad * 32) << 16) + block * 32;
-    const bool mine = quad * 32 < a.m;
+    const uint32_t n16 = (uint32_t)((a.m + 15) & ~15);
+    const uint32_t acc0 = tmem + ((uint32_t)(quad * 32) << 16) + block * 32, acc1 = acc0 + 128;
+    const bool mine = !issuer && quad * 32 < a.m;
     const bool diag = mine && quad == block;  // the lane's diagonal element is its number `lane`
     const int eye_at = diag && row < a.m ? lane : -1;
     launch_dependents();
@@ -417,21 +479,24 @@ __global__ void __launch_bounds__(512) k_small_poly(const __grid_constant__ Smal
 
     // the raw Gram matrix, zero beyond m; its trace is |X|_F^2
     float v[32];
+    if (!issuer) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        const int chunk = block * 8 + c;
-        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (row < a.m && 4 * chunk < (int)n16) {
-            const float4 *p = reinterpret_cast<const float4 *>(a.parts) + (int64_t)b * a.n_parts * 4096 + chunk * 128 + row;
-            for (int k = 0; k < a.n_parts; ++k) {
-                const float4 x = p[(int64_t)k * 4096];
-                sum.x += x.x;
-                sum.y += x.y;
-                sum.z += x.z;
-                sum.w += x.w;
+        for (int c = 0; c < 8; ++c) {
+            const int chunk = block * 8 + c;
+            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (row < a.m && 4 * chunk < (int)n16) {
+                const float4 *p =
+                    reinterpret_cast<const float4 *>(a.parts) + (int64_t)b * a.n_parts * 4096 + chunk * 128 + row;
+                for (int k = 0; k < a.n_parts; ++k) {
+                    const float4 x = p[(int64_t)k * 4096];
+                    sum.x += x.x;
+                    sum.y += x.y;
+                    sum.z += x.z;
+                    sum.w += x.w;
+                }
             }
+            v[4 * c] = sum.x, v[4 * c + 1] = sum.y, v[4 * c + 2] = sum.z, v[4 * c + 3] = sum.w;
         }
-        v[4 * c] = sum.x, v[4 * c + 1] = sum.y, v[4 * c + 2] = sum.z, v[4 * c + 3] = sum.w;
     }
     if (diag) {
         double trace = 0.0;
@@ -447,7 +512,7 @@ __global__ void __launch_bounds__(512) k_small_poly(const __grid_constant__ Smal
     }
     __syncthreads();
     double trace = 0.0;
-    for (int i = 0; i < (int)blockDim.x / 128; ++i)
+    for (int i = 0; i < blocks; ++i)
         trace += s_trace[i];
     // a matrix of zeros stays one, whatever eps
     const float inv = trace == 0.0 && a.eps == 0.0f ? 0.0f : (float)(1.0 / (sqrt(trace) + (double)a.eps));
@@ -457,99 +522,94 @@ __global__ void __launch_bounds__(512) k_small_poly(const __grid_constant__ Smal
 #pragma unroll
         for (int e = 0; e < 32; ++e)
             v[e] = v[e] * inv * (inv * a.g_first);
-        put_pair(G, row, block, v);
+        put_pair<TILES>(G, row, block, v);
     }
-    fence_async_shared();
-    __syncthreads();
-
-    uint32_t phase = 0;
-    // one product (or two), which every thread then waits for
-    auto issue = [&](uint32_t a0, uint32_t b0, uint32_t a1, uint32_t b1) {
-        if (warp == 0 && !a.test_stall) {
+    uint32_t done[2] = {0, 0};  // products waited for on each of the two barriers
+    auto issue = [&](int bar, uint32_t x, uint32_t y) {
+        if (issuer && !a.test_stall) {
             tmem_fence_after();
             if (elect_one()) {
-                issue_pair(tmem, a0, b0, k16, idesc);
-                if (a1)
-                    issue_pair(tmem + 128, a1, b1, k16, idesc);
-                mma_commit<1>(smem_addr(&sh.bar[0]));
+                issue_pair<TILES>(tmem + bar * 128, x, y, n16);
+                mma_commit<1>(smem_addr(&sh.bar[bar]));
             }
             __syncwarp();
         }
     };
-    auto wait = [&] {
-        wait_products(sh, 0, phase & 1, a.status);
-        ++phase;
+    auto wait = [&](int bar) {
+        wait_products(sh, bar, done[bar] & 1, a.status);
+        ++done[bar];
     };
     // this thread's values of an accumulator, times f, into a pair
     auto keep = [&](uint32_t acc, float f, uint32_t to) {
         if (!mine)
             return;
-        uint32_t x[32];
-        tmem_load32(acc, x);
-        tmem_wait_load();
+        read_acc<TILES>(acc, v);
 #pragma unroll
         for (int e = 0; e < 32; ++e)
-            v[e] = __uint_as_float(x[e]) * f;
-        put_pair(to, row, block, v);
+            v[e] *= f;
+        put_pair<TILES>(to, row, block, v);
     };
     auto settle = [&] {
         tmem_fence_before();
         fence_async_shared();
         __syncthreads();
     };
+    settle();
 
     for (int k = 0; k < a.steps && !sh.abort; ++k) {
         const bool more = k + 1 < a.steps;
-        const float eye = a.r_eye[k], bb = a.r_g[k], cc = a.r_g2[k], t_of = a.t_of[k], g_of = a.g_of[k], q_of = a.q_of[k];
-        issue(G, G, 0, 0);
-        if (mine) {  // bG + aI, while the product runs
-            get_pair(G, row, block, v);
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-                v[e] = fmaf(bb, v[e], e == eye_at ? eye : 0.0f);
+        const float eye = a.r_eye[k], bb = a.r_g[k], cc = a.r_g2[k];
+        issue(0, G, G);
+        if (k > 1) {  // the Q of the step before
+            wait(1);
+            keep(acc1, a.q_of[k - 1], Q);
         }
-        wait();
-        if (mine) {  // R = aI + bG + cG^2; the first R is also Q
-            uint32_t x[32];
-            tmem_load32(acc_at, x);
-            tmem_wait_load();
+        float r[32];
+        if (mine) {  // bG + aI
+            get_pair<TILES>(G, row, block, r);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-                v[e] = fmaf(cc, __uint_as_float(x[e]), v[e]);
-            put_pair(R, row, block, v);
+                r[e] = fmaf(bb, r[e], e == eye_at ? eye : 0.0f);
+        }
+        wait(0);
+        if (mine) {  // R = aI + bG + cG^2; the first R is also Q
+            read_acc<TILES>(acc0, v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                v[e] = fmaf(cc, v[e], r[e]);
+            put_pair<TILES>(R, row, block, v);
             if (k == 0) {
+                const float q_of = a.q_of[0];
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
                     v[e] *= q_of;
-                put_pair(Q, row, block, v);
+                put_pair<TILES>(Q, row, block, v);
             }
         }
         settle();
-        // T = R G and Q <- R Q
-        if (more || k > 0) {
-            if (more)
-                issue(R, G, k > 0 ? R : 0, Q);
-            else
-                issue(R, Q, 0, 0);
-            wait();
-            if (more)
-                keep(acc_at, t_of, G);
-            if (k > 0)
-                keep(acc_at + (more ? 128 : 0), q_of, Q);
+        if (more) {
+            const float t_of = a.t_of[k], g_of = a.g_of[k];
+            issue(0, R, G);  // T, in G's place
+            wait(0);
+            keep(acc0, t_of, G);
             settle();
-        }
-        if (more) {  // G <- R T
-            issue(R, G, 0, 0);
-            wait();
-            keep(acc_at, g_of, G);
+            issue(0, R, G);  // the next G, from R and T
+            if (k > 0)
+                issue(1, R, Q);
+            wait(0);
+            keep(acc0, g_of, G);
+            settle();
+        } else if (k > 0) {
+            issue(1, R, Q);
+            wait(1);
+            keep(acc1, a.q_of[k], Q);
             settle();
         }
     }
-    // Q, as it lies: rows beyond m are not read, columns beyond m of a used tile are zero or meet zeros
+    // Q, as it lies; k_small_apply reads its rows below n16, or of lo from row 64 on
     uint4 *out = reinterpret_cast<uint4 *>(a.q) + (int64_t)b * (kPairBytes / 16);
-    for (int i = tid; i < kPairBytes / 16; i += blockDim.x)
-        if ((i & 1023) < (int)n16 * 8)
-            out[i] = lds128(Q + i * 16);
+    for (int i = tid; i < (TILES == 2 ? kPairBytes : kTile) / 16; i += blockDim.x)
+        out[i] = lds128(Q + i * 16);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
@@ -586,9 +646,16 @@ __global__ void __launch_bounds__(kThreads, TILES == 1 ? 3 : 1) k_small_apply(co
     const float back = a.q_last / kApplyScale;
     {
         const uint4 *q = reinterpret_cast<const uint4 *>(a.q) + (int64_t)b * (kPairBytes / 16);
-        for (int i = tid; i < tiles * (kTile / 16); i += kThreads) {
-            sts128(base + i * 16, q[i]);
-            sts128(base + q_lo + i * 16, q[2 * (kTile / 16) + i]);
+        if constexpr (tiles == 2) {
+            for (int i = tid; i < 2 * (kTile / 16); i += kThreads) {
+                sts128(base + i * 16, q[i]);
+                sts128(base + q_lo + i * 16, q[2 * (kTile / 16) + i]);
+            }
+        } else {  // 64 rows of each
+            for (int i = tid; i < kTile / 32; i += kThreads) {
+                sts128(base + i * 16, q[i]);
+                sts128(base + q_lo + i * 16, q[kTile / 32 + i]);
+            }
         }
     }
     const int n_side = a.tall ? a.rows : a.cols;
@@ -754,7 +821,7 @@ cudaError_t launch_kernel(Kernel k, dim3 grid, int threads, int smem, bool behin
                           std::atomic<int> &ready)
 {
     if (!ready.load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kPolySmem);
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kPolySmem<2>);
         if (e != cudaSuccess)
             return e;
         ready.store(1, std::memory_order_release);
@@ -775,7 +842,7 @@ cudaError_t launch_kernel(Kernel k, dim3 grid, int threads, int smem, bool behin
 template <typename T, bool MUON>
 cudaError_t launch_all(SmallOrtho &a, int device, int sms, cudaStream_t stream)
 {
-    static std::atomic<int> ready[kMaxDevices][4];
+    static std::atomic<int> ready[kMaxDevices][5];
     const int n_side = a.tall ? a.rows : a.cols;
     // a cluster of eight CTAs per 8 x 4 steps of 64, as long as all are resident (two a SM)
     const int steps = (n_side + 63) / 64;
@@ -788,11 +855,12 @@ cudaError_t launch_all(SmallOrtho &a, int device, int sms, cudaStream_t stream)
     const int gram = 1024 + (kGramStages * pair * kTile > 65536 ? kGramStages * pair * kTile : 65536);
     cudaError_t e = launch_kernel(k_small_gram<T, MUON>, dim3(kCluster * parts, a.batch), kThreads, gram, false, a, stream,
                                   ready[device][0]);
+    const int tiles = a.m > 64 ? 2 : 1, poly = (a.m + 31) / 32 * 128 + 32;
     if (e == cudaSuccess)
-        e = launch_kernel(k_small_poly, dim3(a.batch), (a.m + 31) / 32 * 128, kPolySmem, true, a, stream, ready[device][1]);
+        e = tiles == 2 ? launch_kernel(k_small_poly<2>, dim3(a.batch), poly, kPolySmem<2>, true, a, stream, ready[device][1])
+                       : launch_kernel(k_small_poly<1>, dim3(a.batch), poly, kPolySmem<1>, true, a, stream, ready[device][4]);
     if (e != cudaSuccess)
         return e;
-    const int tiles = a.m > 64 ? 2 : 1;
     const int64_t stretches = (n_side + 127) / 128;
     const int64_t room = (int64_t)sms * (tiles == 2 ? 1 : 3) / a.batch;  // what is resident at once
     const dim3 grid((unsigned)(stretches < room ? stretches : room > 0 ? room : 1), a.batch);
