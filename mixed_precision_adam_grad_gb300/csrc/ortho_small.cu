@@ -400,24 +400,6 @@ __device__ __forceinline__ void put_pair(uint32_t m, int row, int block, const f
     }
 }
 
-template <int TILES>
-__device__ __forceinline__ void get_pair(uint32_t m, int row, int block, float (&v)[32])
-{
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const uint4 hi = lds128(pair_at<TILES>(m, row, 4 * block + q, false));
-        const uint4 lo = lds128(pair_at<TILES>(m, row, 4 * block + q, true));
-        const uint32_t u[4] = {hi.x, hi.y, hi.z, hi.w}, w[4] = {lo.x, lo.y, lo.z, lo.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u[e]));
-            const float2 l = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
-            v[8 * q + 2 * e] = f.x + l.x;
-            v[8 * q + 2 * e + 1] = f.y + l.y;
-        }
-    }
-}
-
 // The lane's 32 values of an accumulator.
 template <int TILES>
 __device__ __forceinline__ void read_acc(uint32_t at, float (&v)[32])
@@ -460,6 +442,7 @@ __global__ void __launch_bounds__(128 * 2 * TILES + 32) k_small_poly(const __gri
     extern __shared__ uint8_t smem_raw[];
     __shared__ Base sh;
     __shared__ double s_trace[4];
+    __shared__ float s_f[6][kSmallMaxSteps];  // the factors of the steps (from the arguments each would take 200 cycles)
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const uint32_t G = base, R = base + kPolyPair<TILES>, Q = base + 2 * kPolyPair<TILES>;
     const uint32_t tmem = set_up(sh, 256);
@@ -472,6 +455,14 @@ __global__ void __launch_bounds__(128 * 2 * TILES + 32) k_small_poly(const __gri
     const bool mine = !issuer && quad * 32 < a.m;
     const bool diag = mine && quad == block;  // the lane's diagonal element is its number `lane`
     const int eye_at = diag && row < a.m ? lane : -1;
+    if (tid < a.steps) {
+        s_f[0][tid] = a.r_eye[tid];
+        s_f[1][tid] = a.r_g[tid];
+        s_f[2][tid] = a.r_g2[tid];
+        s_f[3][tid] = a.t_of[tid];
+        s_f[4][tid] = a.g_of[tid];
+        s_f[5][tid] = a.q_of[tid];
+    }
     launch_dependents();
     wait_for_previous_grid();
     if (tid == 0 && (*(volatile unsigned *)a.status & kStatusWaitLimit))
@@ -518,6 +509,13 @@ __global__ void __launch_bounds__(128 * 2 * TILES + 32) k_small_poly(const __gri
     const float inv = trace == 0.0 && a.eps == 0.0f ? 0.0f : (float)(1.0 / (sqrt(trace) + (double)a.eps));
     if (tid == 0)
         a.inv[b] = inv;
+    float r[32];  // bG + aI of a step, from G as it was written
+    auto begin_r = [&](int k) {
+        const float eye = s_f[0][k], bb = s_f[1][k];
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            r[e] = fmaf(bb, v[e], e == eye_at ? eye : 0.0f);
+    };
     if (mine) {
 #pragma unroll
         for (int e = 0; e < 32; ++e)
@@ -558,18 +556,13 @@ __global__ void __launch_bounds__(128 * 2 * TILES + 32) k_small_poly(const __gri
 
     for (int k = 0; k < a.steps && !sh.abort; ++k) {
         const bool more = k + 1 < a.steps;
-        const float eye = a.r_eye[k], bb = a.r_g[k], cc = a.r_g2[k];
+        const float cc = s_f[2][k], t_of = s_f[3][k], g_of = s_f[4][k];
         issue(0, G, G);
+        if (mine)
+            begin_r(k);
         if (k > 1) {  // the Q of the step before
             wait(1);
-            keep(acc1, a.q_of[k - 1], Q);
-        }
-        float r[32];
-        if (mine) {  // bG + aI
-            get_pair<TILES>(G, row, block, r);
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-                r[e] = fmaf(bb, r[e], e == eye_at ? eye : 0.0f);
+            keep(acc1, s_f[5][k - 1], Q);
         }
         wait(0);
         if (mine) {  // R = aI + bG + cG^2; the first R is also Q
@@ -579,7 +572,7 @@ __global__ void __launch_bounds__(128 * 2 * TILES + 32) k_small_poly(const __gri
                 v[e] = fmaf(cc, v[e], r[e]);
             put_pair<TILES>(R, row, block, v);
             if (k == 0) {
-                const float q_of = a.q_of[0];
+                const float q_of = s_f[5][0];
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
                     v[e] *= q_of;
@@ -588,7 +581,6 @@ __global__ void __launch_bounds__(128 * 2 * TILES + 32) k_small_poly(const __gri
         }
         settle();
         if (more) {
-            const float t_of = a.t_of[k], g_of = a.g_of[k];
             issue(0, R, G);  // T, in G's place
             wait(0);
             keep(acc0, t_of, G);
@@ -602,7 +594,7 @@ __global__ void __launch_bounds__(128 * 2 * TILES + 32) k_small_poly(const __gri
         } else if (k > 0) {
             issue(1, R, Q);
             wait(1);
-            keep(acc1, a.q_of[k], Q);
+            keep(acc1, s_f[5][k], Q);
             settle();
         }
     }
