@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(128 * 2 * TILES + 32) k_small_poly(const __gri
     const float inv = trace == 0.0 && a.eps == 0.0f ? 0.0f : (float)(1.0 / (sqrt(trace) + (double)a.eps));
     if (tid == 0)
         a.inv[b] = inv;
-    float r[32];  // bG + aI of a step, from G as it was written
+    float r[32];  // bG + aI of the coming step, from G as it is written
     auto begin_r = [&](int k) {
         const float eye = s_f[0][k], bb = s_f[1][k];
 #pragma unroll
@@ -521,6 +521,7 @@ __global__ void __launch_bounds__(128 * 2 * TILES + 32) k_small_poly(const __gri
         for (int e = 0; e < 32; ++e)
             v[e] = v[e] * inv * (inv * a.g_first);
         put_pair<TILES>(G, row, block, v);
+        begin_r(0);
     }
     uint32_t done[2] = {0, 0};  // products waited for on each of the two barriers
     auto issue = [&](int bar, uint32_t x, uint32_t y) {
@@ -558,8 +559,6 @@ __global__ void __launch_bounds__(128 * 2 * TILES + 32) k_small_poly(const __gri
         const bool more = k + 1 < a.steps;
         const float cc = s_f[2][k], t_of = s_f[3][k], g_of = s_f[4][k];
         issue(0, G, G);
-        if (mine)
-            begin_r(k);
         if (k > 1) {  // the Q of the step before
             wait(1);
             keep(acc1, s_f[5][k - 1], Q);
@@ -590,6 +589,7 @@ __global__ void __launch_bounds__(128 * 2 * TILES + 32) k_small_poly(const __gri
                 issue(1, R, Q);
             wait(0);
             keep(acc0, g_of, G);
+            begin_r(k + 1);
             settle();
         } else if (k > 0) {
             issue(1, R, Q);
