@@ -54,7 +54,7 @@ struct SourceArgs {
     float mu, one_minus_mu;
     int nesterov;
     double *parts;            // [batch][kNormParts]
-    unsigned *status;
+    unsigned *status, *count;
 };
 
 __device__ __forceinline__ float widen(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
@@ -143,8 +143,10 @@ __device__ __forceinline__ float muon_value(const SourceArgs &a, float sum, floa
 __device__ __forceinline__ void begin_source(const SourceArgs &a)
 {
     ptx::launch_dependents();
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x <= kMaxPhases)
-        a.status[threadIdx.x] = 0;
+    if (blockIdx.x == 0 && threadIdx.x < kMaxPhases)
+        a.count[(int64_t)threadIdx.x * gridDim.y + blockIdx.y] = 0;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+        *a.status = 0;
 }
 
 // A partial sum of a matrix's squares per block of threads, the matrices lying
@@ -434,7 +436,8 @@ Shape shape_of(int batch, int rows, int cols)
 }
 
 struct Work {
-    unsigned *status;          // and the phases' counters
+    unsigned *status;
+    unsigned *count;           // [kMaxPhases][batch]
     double *parts;
     __half *x_hi[2], *x_lo;
     float *u;                  // a Muon step's update
@@ -469,7 +472,8 @@ Work layout(const Shape &s, char *base)
         p.lo = (__half *)take(2 * n);
         return p;
     };
-    w.status = (unsigned *)take(4 * (1 + kMaxPhases));
+    w.status = (unsigned *)take(4);
+    w.count = (unsigned *)take(4 * (int64_t)kMaxPhases * s.batch);
     w.parts = (double *)take(8 * (int64_t)s.batch * kNormParts);
     w.x_hi[0] = (__half *)take(2 * xb);
     w.x_lo = (__half *)take(2 * xb);
@@ -490,8 +494,8 @@ Work layout(const Shape &s, char *base)
                                                                                : 4 * (int64_t)s.batch * s.rows * s.cols);
     w.u = (float *)w.x_hi[1];
     w.bytes = off;
-    if (s.m <= kSmallSide) {  // status and counters, then the other kernels' arrays
-        off = (int64_t)align_up(4 * (1 + kMaxPhases));
+    if (s.m <= kSmallSide) {  // the status, then the other kernels' arrays
+        off = (int64_t)align_up(4);
         w.inv = (float *)take(4 * (int64_t)s.batch);
         w.small_parts = (float *)take(small_parts_bytes(s.batch));
         w.small_q = (__half *)take(small_q_bytes(s.batch));
@@ -581,6 +585,7 @@ cudaError_t enqueue_products(const Shape &s, const Work &w, const Schedule &sc, 
     OrthoPlan plan{};
     plan.batch = s.batch;
     plan.status = w.status;
+    plan.count = w.count;
     plan.rows = s.rows;
     plan.cols = s.cols;
     plan.w = f.w;
@@ -619,10 +624,10 @@ cudaError_t enqueue_products(const Shape &s, const Work &w, const Schedule &sc, 
         const int p = s.grouped ? (sc.steps - k0 < kGroupSteps ? sc.steps - k0 : kGroupSteps) : 1;
         const bool last = k0 + p == sc.steps;
         if (plan.n_phases + 3 * kGroupSteps + 1 > kMaxPhases) {
-            // the next group goes into a launch of its own, whose counters start at zero again
+            // the next group goes into a launch of its own, whose counts start at zero again
             cudaError_t e = launch_ortho_products(plan, device, stream);
             if (e == cudaSuccess)
-                e = cudaMemsetAsync(w.status + 1, 0, sizeof(unsigned) * kMaxPhases, stream);
+                e = cudaMemsetAsync(w.count, 0, sizeof(unsigned) * kMaxPhases * s.batch, stream);
             if (e != cudaSuccess)
                 return e;
             plan.n_phases = 0;
@@ -843,6 +848,7 @@ cudaError_t enqueue_source(const Shape &s, const Work &w, const Schedule &sc, So
     a.u = w.u;
     a.parts = w.parts;
     a.status = w.status;
+    a.count = w.count;
     const int64_t blocks = (int64_t)s.rblk * s.cblk;
     const int64_t per = (1216 + s.batch - 1) / s.batch;  // eight blocks of threads per SM
     const int64_t most = per < kNormParts ? per : kNormParts;

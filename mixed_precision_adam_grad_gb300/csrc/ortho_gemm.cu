@@ -18,12 +18,15 @@
 // instead, in 32-byte sectors, made room for a sixth stage, but the phases that
 // have them took 15 to 50 % longer.)
 //
-// One launch runs all the products of an iteration, one phase after the other:
-// a CTA whose tiles of a phase are written counts itself in, and the producers
-// wait for the count of all CTAs before they read a phase's results (a
-// cooperative launch, so all CTAs are resident).  Between two products of a
-// small matrix lie 3 us this way, where a launch each, even with programmatic
-// serialisation, left 7 to 9 us.
+// One launch runs all the products of an iteration (a cooperative launch, so all
+// CTAs are resident).  The tiles of all phases, phase after phase and matrix
+// after matrix, form one sequence that the CTAs share out in turn.  A CTA whose
+// tile is written counts it for its matrix and phase, and before the first read
+// of a matrix in the next phase the readers wait for that count: matrices of a
+// batch do not wait for one another, and a phase's last, partly filled round of
+// tiles runs beside the next phase's first.  (With a barrier of all CTAs after
+// each phase 40 matrices of 1000 x 2187 took BARRIER40 us instead of STREAM40,
+// with a launch for each phase another 2 us a phase.)
 //
 // Why FP16 and where FP32 stays: FP16 rounds 8 times finer than BF16 at the
 // same rate, and the iterates are bounded (the matrix is normalised first), so
@@ -61,14 +64,14 @@ struct Tile {
 };
 
 template <int CG>
-__device__ __forceinline__ Tile decode(const OrthoGemm &g, int batch, int t)
+__device__ __forceinline__ Tile decode(const OrthoGemm &g, int t)
 {
     const int mt = (g.mblk + CG - 1) / CG, nt = (g.nblk + CG - 1) / CG;
     const int per = g.sym ? mt * (mt + 1) / 2 : mt * nt;
     const int z = t / per, r = t - z * per;
     Tile x;
-    x.prob = z / batch;
-    x.b = z - x.prob * batch;
+    x.b = z / g.nprob;
+    x.prob = z - x.b * g.nprob;
     if (g.sym) {
         int j = (int)((sqrtf(8.0f * (float)r + 1.0f) - 1.0f) * 0.5f);
         while (j * (j + 1) / 2 > r)
@@ -87,12 +90,51 @@ __device__ __forceinline__ Tile decode(const OrthoGemm &g, int batch, int t)
     return x;
 }
 
+// Tiles of one matrix.
 template <int CG>
-__host__ __device__ __forceinline__ int tile_count(const OrthoGemm &g, int batch)
+__host__ __device__ __forceinline__ int tile_count(const OrthoGemm &g)
 {
     const int mt = (g.mblk + CG - 1) / CG, nt = (g.nblk + CG - 1) / CG;
-    return (g.sym ? mt * (mt + 1) / 2 : mt * nt) * batch * g.nprob;
+    return (g.sym ? mt * (mt + 1) / 2 : mt * nt) * g.nprob;
 }
+
+// A position in the sequence of all tiles.
+template <int CG>
+struct Walk {
+    int f = 0;          // phase
+    int64_t base = 0;   // tiles before it
+    int64_t here;       // tiles in it
+    __device__ __forceinline__ explicit Walk(const OrthoPlan &plan) : here((int64_t)tile_count<CG>(plan.ph[0]) * plan.batch) {}
+    // Moves on to tile t (never back); false beyond the last.
+    __device__ __forceinline__ bool to(const OrthoPlan &plan, int64_t t)
+    {
+        while (t - base >= here) {
+            base += here;
+            if (++f == plan.n_phases)
+                return false;
+            here = (int64_t)tile_count<CG>(plan.ph[f]) * plan.batch;
+        }
+        return true;
+    }
+};
+
+// Before a tile of matrix b in phase f is read for: the phase before it, waited
+// for once per matrix.
+template <int CG>
+struct Before {
+    int f = 0, b = -1;
+    __device__ __forceinline__ bool wait(const OrthoPlan &plan, int phase, int matrix, volatile int *abort)
+    {
+        if (phase == 0 || (phase == f && matrix == b))
+            return true;
+        f = phase;
+        b = matrix;
+        const bool ok = counter_wait(plan.count + (int64_t)(phase - 1) * plan.batch + matrix,
+                                     tile_count<CG>(plan.ph[phase - 1]) * CG, plan.status, kStatusWaitLimit, abort);
+        fence_async();  // it was written, and is read, by the copy engine too
+        return __all_sync(kFullMask, ok);
+    }
+};
 
 // Whether step k of the operand whose tile has index t (in units of CG blocks)
 // is read MN-major: a symmetric matrix keeps block (k, t) for k <= t.
@@ -429,24 +471,23 @@ __device__ __forceinline__ void prefetch_theta(const OrthoPlan &plan, const Tile
 
 // Shared state of a CTA, besides the operand ring and the epilogue's buffers.
 struct Shared {
-    uint64_t full[kStages], empty[kStages], peer[kStages], acc_full[2], acc_empty[2], c[kEpiWarps][2], phase;
+    uint64_t full[kStages], empty[kStages], peer[kStages], acc_full[2], acc_empty[2], c[kEpiWarps][2];
     uint32_t tmem;
-    unsigned written;        // epilogue warps whose tiles of the phase are written
+    unsigned written[4];     // epilogue warps that have written their part of a tile, of every fourth tile: while one
+                             // warp still writes tile n, no other can be beyond tile n + 2
     volatile int abort;
 };
 
-// The tiles of one phase, by one epilogue warp.  n: tiles so far (of all
-// phases); asked: copies of C asked for so far on each of the two barriers.
+// Tile number n of this CTA, x of phase g, by one epilogue warp.  asked: copies
+// of C asked for so far on each of the two barriers.
 template <int CG, int EPI>
-__device__ __forceinline__ bool epilogue_tiles(const OrthoPlan &plan, const OrthoGemm &g, Shared &sh, uint32_t tmem,
-                                               uint32_t mine, int warp, int lane, uint32_t rank, uint32_t &n,
-                                               uint32_t (&asked)[2])
+__device__ __forceinline__ bool epilogue_tile(const OrthoPlan &plan, const OrthoGemm &g, const Tile &x, Shared &sh,
+                                              uint32_t tmem, uint32_t mine, int warp, int lane, uint32_t rank, uint32_t n,
+                                              uint32_t (&asked)[2])
 {
     // warp (quad, half): rows 32*quad.., every second chunk of 64 columns
     const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
-    const int n_tiles = tile_count<CG>(g, plan.batch);
-    for (int t = blockIdx.x / CG; t < n_tiles; t += gridDim.x / CG, ++n) {
-        const Tile x = decode<CG>(g, plan.batch, t);
+    {
         const OrthoProduct &p = g.p[x.prob];
         const uint32_t buf = n & 1, use = n >> 1;
         const int ib = x.i * CG + rank, gi = ib * 128 + row;
@@ -577,9 +618,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_ortho_products(const __grid_con
         for (int w = 0; w < kEpiWarps; ++w)
             for (int i = 0; i < 2; ++i)
                 mbar_init(smem_addr(&sh.c[w][i]), 1);
-        mbar_init(smem_addr(&sh.phase), 1);
         sh.abort = 0;
-        sh.written = 0;
+        for (int i = 0; i < 4; ++i)
+            sh.written[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_shared();
     }
@@ -598,36 +639,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_ortho_products(const __grid_con
     if (warp == 0) {
         uint32_t it = 0;
         bool ok = true;
-        for (int f = 0; f < plan.n_phases && ok; ++f) {
-            const OrthoGemm &g = plan.ph[f];
-            if (f > 0) {  // the phase before is written, by every CTA
-                ok = __all_sync(kFullMask, counter_wait(plan.status + f, gridDim.x, plan.status, kStatusWaitLimit, &sh.abort));
+        Walk<CG> walk(plan);
+        Before<CG> before;
+        for (int64_t t = first; ok && !plan.test_stall && walk.to(plan, t); t += stride) {
+            const OrthoGemm &g = plan.ph[walk.f];
+            const Tile x = decode<CG>(g, (int)(t - walk.base));
+            ok = before.wait(plan, walk.f, x.b, &sh.abort);
+            const __half *a = g.p[x.prob].a + (int64_t)x.b * g.a_stride;
+            const __half *b = g.p[x.prob].b + (int64_t)x.b * g.b_stride;
+            for (int k = 0; k < g.k64 && ok; ++k, ++it) {
+                const uint32_t s = it % kStages, ph = (it / kStages) & 1;
+                ok = __all_sync(kFullMask, mbar_wait(smem_addr(&sh.empty[s]), ph ^ 1, &sh.abort));
                 if (!ok)
                     break;
-                fence_async();
-                if (elect_one())
-                    mbar_arrive(smem_addr(&sh.phase));
-                __syncwarp();
-            }
-            const int n_tiles = plan.test_stall ? 0 : tile_count<CG>(g, plan.batch);
-            for (int t = first; t < n_tiles && ok; t += stride) {
-                const Tile x = decode<CG>(g, plan.batch, t);
-                const __half *a = g.p[x.prob].a + (int64_t)x.b * g.a_stride;
-                const __half *b = g.p[x.prob].b + (int64_t)x.b * g.b_stride;
-                for (int k = 0; k < g.k64; ++k, ++it) {
-                    const uint32_t s = it % kStages, ph = (it / kStages) & 1;
-                    ok = __all_sync(kFullMask, mbar_wait(smem_addr(&sh.empty[s]), ph ^ 1, &sh.abort));
-                    if (!ok)
-                        break;
-                    const uint32_t bar = smem_addr(&sh.full[s]), slot = ring + s * kStageBytes;
-                    const bool a_mn = reads_mn<CG>(g.a_kind, x.i, k), b_mn = reads_mn<CG>(g.b_kind, x.j, k);
-                    if (elect_one()) {
-                        mbar_expect_tx(bar, kStageBytes);
-                        load_operand(slot, a, g.a_c64, x.i * CG + rank, k, a_mn, bar);
-                        load_operand(slot + kSlot, b, g.b_c64, x.j * CG + rank, k, b_mn, bar);
-                    }
-                    __syncwarp();
+                const uint32_t bar = smem_addr(&sh.full[s]), slot = ring + s * kStageBytes;
+                const bool a_mn = reads_mn<CG>(g.a_kind, x.i, k), b_mn = reads_mn<CG>(g.b_kind, x.j, k);
+                if (elect_one()) {
+                    mbar_expect_tx(bar, kStageBytes);
+                    load_operand(slot, a, g.a_c64, x.i * CG + rank, k, a_mn, bar);
+                    load_operand(slot + kSlot, b, g.b_c64, x.j * CG + rank, k, b_mn, bar);
                 }
+                __syncwarp();
             }
         }
         if (!ok) {
@@ -641,48 +673,46 @@ __global__ void __launch_bounds__(kThreads, 1) k_ortho_products(const __grid_con
     } else if (warp == 1) {
         uint32_t it = 0, n = 0;
         bool ok = true;
-        for (int f = 0; f < plan.n_phases && ok; ++f) {
-            const OrthoGemm &g = plan.ph[f];
-            const int n_tiles = tile_count<CG>(g, plan.batch);
-            for (int t = first; t < n_tiles && ok; t += stride, ++n) {
-                const Tile x = decode<CG>(g, plan.batch, t);
-                const uint32_t buf = n & 1, use = n >> 1;
-                if (rank == 0) {
-                    ok = __all_sync(kFullMask, mbar_wait(smem_addr(&sh.acc_empty[buf]), (use & 1) ^ 1, &sh.abort));
-                    if (!ok)
-                        break;
-                    tmem_fence_after();
-                }
-                for (int k = 0; k < g.k64; ++k, ++it) {
-                    const uint32_t s = it % kStages, ph = (it / kStages) & 1;
-                    ok = mbar_wait(smem_addr(&sh.full[s]), ph, &sh.abort);
-                    if (CG == 2 && rank == 0)
-                        ok = ok && mbar_wait(smem_addr(&sh.peer[s]), ph, &sh.abort);
-                    ok = __all_sync(kFullMask, ok);
-                    if (!ok)
-                        break;
-                    if (CG == 2 && rank != 0) {
-                        if (elect_one())
-                            mbar_arrive_cluster(map_to_rank(smem_addr(&sh.peer[s]), 0));
-                        __syncwarp();
-                        continue;
-                    }
-                    const bool a_mn = reads_mn<CG>(g.a_kind, x.i, k), b_mn = reads_mn<CG>(g.b_kind, x.j, k);
-                    const uint32_t idesc = f16_idesc(128 * CG, 128 * CG, a_mn, b_mn);
-                    const uint32_t slot = ring + s * kStageBytes;
-                    const uint64_t a_desc = operand_desc(slot, kSlot / 2), b_desc = operand_desc(slot + kSlot, kSlot / 2);
-                    const uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
-                    if (elect_one()) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            mma_f16<CG>(tmem + buf * 128 * CG, a_desc + j * a_step, b_desc + j * b_step, idesc,
-                                        k > 0 || j > 0);
-                        mma_commit<CG>(smem_addr(&sh.empty[s]));
-                        if (k + 1 == g.k64)
-                            mma_commit<CG>(smem_addr(&sh.acc_full[buf]));
-                    }
+        Walk<CG> walk(plan);
+        for (int64_t t = first; ok && walk.to(plan, t); t += stride, ++n) {
+            const OrthoGemm &g = plan.ph[walk.f];
+            const Tile x = decode<CG>(g, (int)(t - walk.base));
+            const uint32_t buf = n & 1, use = n >> 1;
+            if (rank == 0) {
+                ok = __all_sync(kFullMask, mbar_wait(smem_addr(&sh.acc_empty[buf]), (use & 1) ^ 1, &sh.abort));
+                if (!ok)
+                    break;
+                tmem_fence_after();
+            }
+            for (int k = 0; k < g.k64; ++k, ++it) {
+                const uint32_t s = it % kStages, ph = (it / kStages) & 1;
+                ok = mbar_wait(smem_addr(&sh.full[s]), ph, &sh.abort);
+                if (CG == 2 && rank == 0)
+                    ok = ok && mbar_wait(smem_addr(&sh.peer[s]), ph, &sh.abort);
+                ok = __all_sync(kFullMask, ok);
+                if (!ok)
+                    break;
+                if (CG == 2 && rank != 0) {
+                    if (elect_one())
+                        mbar_arrive_cluster(map_to_rank(smem_addr(&sh.peer[s]), 0));
                     __syncwarp();
+                    continue;
                 }
+                const bool a_mn = reads_mn<CG>(g.a_kind, x.i, k), b_mn = reads_mn<CG>(g.b_kind, x.j, k);
+                const uint32_t idesc = f16_idesc(128 * CG, 128 * CG, a_mn, b_mn);
+                const uint32_t slot = ring + s * kStageBytes;
+                const uint64_t a_desc = operand_desc(slot, kSlot / 2), b_desc = operand_desc(slot + kSlot, kSlot / 2);
+                const uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
+                if (elect_one()) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma_f16<CG>(tmem + buf * 128 * CG, a_desc + j * a_step, b_desc + j * b_step, idesc,
+                                    k > 0 || j > 0);
+                    mma_commit<CG>(smem_addr(&sh.empty[s]));
+                    if (k + 1 == g.k64)
+                        mma_commit<CG>(smem_addr(&sh.acc_full[buf]));
+                }
+                __syncwarp();
             }
         }
         if (!ok) {
@@ -700,29 +730,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_ortho_products(const __grid_con
         const uint32_t mine = ring + kStages * kStageBytes + ew * kEpiBytes;
         uint32_t n = 0, asked[2] = {0, 0};
         bool ok = true;
-        for (int f = 0; f < plan.n_phases && ok; ++f) {
-            const OrthoGemm &g = plan.ph[f];
-            if (f > 0) {
-                ok = __all_sync(kFullMask, mbar_wait(smem_addr(&sh.phase), (f - 1) & 1, &sh.abort));
-                if (!ok)
-                    break;
-                fence_async();
+        Walk<CG> walk(plan);
+        Before<CG> before;
+        for (int64_t t = first; walk.to(plan, t); t += stride, ++n) {
+            const OrthoGemm &g = plan.ph[walk.f];
+            const Tile x = decode<CG>(g, (int)(t - walk.base));
+            ok = before.wait(plan, walk.f, x.b, &sh.abort);
+            if (ok) {
+                switch (g.epi) {
+                case kEpiGram: ok = epilogue_tile<CG, kEpiGram>(plan, g, x, sh, tmem, mine, ew, lane, rank, n, asked); break;
+                case kEpiPoly: ok = epilogue_tile<CG, kEpiPoly>(plan, g, x, sh, tmem, mine, ew, lane, rank, n, asked); break;
+                case kEpiSym: ok = epilogue_tile<CG, kEpiSym>(plan, g, x, sh, tmem, mine, ew, lane, rank, n, asked); break;
+                case kEpiApply: ok = epilogue_tile<CG, kEpiApply>(plan, g, x, sh, tmem, mine, ew, lane, rank, n, asked); break;
+                case kEpiOut: ok = epilogue_tile<CG, kEpiOut>(plan, g, x, sh, tmem, mine, ew, lane, rank, n, asked); break;
+                default: ok = epilogue_tile<CG, kEpiMuon>(plan, g, x, sh, tmem, mine, ew, lane, rank, n, asked); break;
+                }
             }
-            switch (g.epi) {
-            case kEpiGram: ok = epilogue_tiles<CG, kEpiGram>(plan, g, sh, tmem, mine, ew, lane, rank, n, asked); break;
-            case kEpiPoly: ok = epilogue_tiles<CG, kEpiPoly>(plan, g, sh, tmem, mine, ew, lane, rank, n, asked); break;
-            case kEpiSym: ok = epilogue_tiles<CG, kEpiSym>(plan, g, sh, tmem, mine, ew, lane, rank, n, asked); break;
-            case kEpiApply: ok = epilogue_tiles<CG, kEpiApply>(plan, g, sh, tmem, mine, ew, lane, rank, n, asked); break;
-            case kEpiOut: ok = epilogue_tiles<CG, kEpiOut>(plan, g, sh, tmem, mine, ew, lane, rank, n, asked); break;
-            default: ok = epilogue_tiles<CG, kEpiMuon>(plan, g, sh, tmem, mine, ew, lane, rank, n, asked); break;
+            if (!ok)
+                break;
+            if (walk.f + 1 < plan.n_phases) {  // the CTA's last warp counts the tile
+                bulk_wait<0>();
+                __syncwarp();
+                if (lane == 0 && add_shared(smem_addr(&sh.written[n & 3]), 1u) % kEpiWarps == kEpiWarps - 1)
+                    add_release(plan.count + (int64_t)walk.f * plan.batch + x.b, 1u);
+                __syncwarp();
             }
-            bulk_wait<0>();
-            __syncwarp();
-            if (ok && f + 1 < plan.n_phases && lane == 0)  // the CTA's last warp counts it in
-                if (add_shared(smem_addr(&sh.written), 1u) == (unsigned)((f + 1) * kEpiWarps - 1))
-                    add_release(plan.status + f + 1, 1u);
-            __syncwarp();
         }
+        bulk_wait<0>();
         if (!ok) {
             sh.abort = 1;
             if (lane == 0)
@@ -750,7 +784,7 @@ cudaError_t launch(const OrthoPlan &plan, int groups, cudaStream_t stream)
 {
     int most = 1;
     for (int f = 0; f < plan.n_phases; ++f) {
-        const int t = tile_count<CG>(plan.ph[f], plan.batch);
+        const int t = tile_count<CG>(plan.ph[f]) * plan.batch;
         most = t > most ? t : most;
     }
     cudaLaunchConfig_t cfg{};
@@ -803,14 +837,16 @@ cudaError_t resident_groups(std::atomic<int> &cache, int device, int *groups)
     return cudaSuccess;
 }
 
-// Steps of the ring on the busiest CTA.
+// Steps of the ring on the busiest CTA.  Of a single matrix each phase waits
+// for the one before; those of a batch run into one another.
 template <int CG>
-int64_t steps(const OrthoPlan &plan, int groups)
+double steps(const OrthoPlan &plan, int groups)
 {
-    int64_t sum = 0;
+    double sum = 0.0;
     for (int f = 0; f < plan.n_phases; ++f) {
-        const int t = tile_count<CG>(plan.ph[f], plan.batch);
-        sum += (int64_t)((t + groups - 1) / groups) * plan.ph[f].k64;
+        const int t = tile_count<CG>(plan.ph[f]) * plan.batch;
+        const double rounds = plan.batch == 1 ? (t + groups - 1) / groups : t > groups ? (double)t / groups : 1.0;
+        sum += rounds * plan.ph[f].k64;
     }
     return sum;
 }
@@ -832,7 +868,7 @@ cudaError_t launch_ortho_products(const OrthoPlan &plan, int device, cudaStream_
     // 128 x 128 0.33 us with every SM at it (both bound by what L2 delivers,
     // 15 TB/s): pairs do 3.3 times the work per step, but a matrix has four
     // times fewer tiles for them.
-    if (39 * steps<2>(plan, n2) <= 33 * steps<1>(plan, n1))
+    if (0.39 * steps<2>(plan, n2) <= 0.33 * steps<1>(plan, n1))
         return launch<2>(plan, n2, stream);
     return launch<1>(plan, n1, stream);
 }

@@ -75,7 +75,8 @@ constexpr int kMaxPhases = 32;  // products of one launch, one after the other
 struct OrthoPlan {
     OrthoGemm ph[kMaxPhases];
     int n_phases, batch;
-    unsigned *status;        // a word, and behind it an arrival counter per phase (zero at the start)
+    unsigned *status;
+    unsigned *count;         // [n_phases][batch] CTAs' tiles written so far, zero at the start
     // kEpiOut and kEpiMuon
     int rows, cols;
     uint16_t *w;
