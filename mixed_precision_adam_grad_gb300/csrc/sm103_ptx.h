@@ -115,6 +115,37 @@ __device__ __forceinline__ bool counter_wait(const unsigned *counter, unsigned t
     return ok;
 }
 
+// A word of shared memory that one thread raises and others of the CTA wait
+// for: who sees the value sees what the thread that stored it had seen.
+__device__ __forceinline__ void store_shared(uint32_t addr, unsigned v)
+{
+    asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ unsigned load_shared(uint32_t addr)
+{
+    unsigned v;
+    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// Wait until the word has reached `target`; false if the limit passed first or
+// *abort was seen.
+__device__ __forceinline__ bool shared_wait(uint32_t addr, unsigned target, volatile int *abort)
+{
+    if (load_shared(addr) >= target)
+        return true;
+    const unsigned long long t0 = global_ns();
+    for (uint32_t round = 0; round < kWaitLimitTries / 32; ++round) {
+        for (int i = 0; i < 32; ++i)
+            if (load_shared(addr) >= target)
+                return true;
+        if (*abort || global_ns() - t0 > kWaitLimitNs)
+            return false;
+    }
+    return false;
+}
+
 // 1-D bulk copies: global -> shared (completes `bytes` on the mbarrier) and
 // shared -> global (in this thread's bulk group).  16-byte aligned, sizes
 // multiples of 16.
