@@ -54,7 +54,7 @@ struct SourceArgs {
     float mu, one_minus_mu;
     int nesterov;
     double *parts;            // [batch][kNormParts]
-    unsigned *status, *count;
+    unsigned *status, *count, *joined;
 };
 
 __device__ __forceinline__ float widen(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
@@ -145,8 +145,12 @@ __device__ __forceinline__ void begin_source(const SourceArgs &a)
     ptx::launch_dependents();
     if (blockIdx.x == 0 && threadIdx.x < kMaxPhases)
         a.count[(int64_t)threadIdx.x * gridDim.y + blockIdx.y] = 0;
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
-        *a.status = 0;
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+        for (int i = threadIdx.x; i < kJoinWords; i += kPrepThreads)
+            a.joined[i] = 0;
+        if (threadIdx.x == 0)
+            *a.status = 0;
+    }
 }
 
 // A partial sum of a matrix's squares per block of threads, the matrices lying
@@ -438,6 +442,7 @@ Shape shape_of(int batch, int rows, int cols)
 struct Work {
     unsigned *status;
     unsigned *count;           // [kMaxPhases][batch]
+    unsigned *joined;          // [kJoinWords]
     double *parts;
     __half *x_hi[2], *x_lo;
     float *u;                  // a Muon step's update
@@ -474,6 +479,7 @@ Work layout(const Shape &s, char *base)
     };
     w.status = (unsigned *)take(4);
     w.count = (unsigned *)take(4 * (int64_t)kMaxPhases * s.batch);
+    w.joined = (unsigned *)take(4 * kJoinWords);
     w.parts = (double *)take(8 * (int64_t)s.batch * kNormParts);
     w.x_hi[0] = (__half *)take(2 * xb);
     w.x_lo = (__half *)take(2 * xb);
@@ -586,6 +592,14 @@ cudaError_t enqueue_products(const Shape &s, const Work &w, const Schedule &sc, 
     plan.batch = s.batch;
     plan.status = w.status;
     plan.count = w.count;
+    plan.joined = w.joined;
+    if (s.grouped) {
+        __half *const free[8] = {w.o[0], w.o[1], w.t.hi, w.t.lo, w.q[0].hi, w.q[0].lo, w.q[1].hi, w.q[1].lo};
+        for (__half *p : free)
+            plan.area[plan.areas++] = (float *)p;
+        plan.area_slots = s.mpad * s.mpad / 2;
+        plan.area_matrix = w.m_elems / 2;
+    }
     plan.rows = s.rows;
     plan.cols = s.cols;
     plan.w = f.w;
@@ -600,6 +614,7 @@ cudaError_t enqueue_products(const Shape &s, const Work &w, const Schedule &sc, 
 
     OrthoGemm base{};
     base.nprob = 1;
+    base.parts = 1;
     base.d_stride = mdim;
 
     OrthoGemm mm = base;  // a symmetric m x m product of symmetric factors
@@ -849,6 +864,7 @@ cudaError_t enqueue_source(const Shape &s, const Work &w, const Schedule &sc, So
     a.parts = w.parts;
     a.status = w.status;
     a.count = w.count;
+    a.joined = w.joined;
     const int64_t blocks = (int64_t)s.rblk * s.cblk;
     const int64_t per = (1216 + s.batch - 1) / s.batch;  // eight blocks of threads per SM
     const int64_t most = per < kNormParts ? per : kNormParts;

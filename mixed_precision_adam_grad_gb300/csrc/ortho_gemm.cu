@@ -43,6 +43,7 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <cmath>
 
 #include "slide_ortho.h"
 #include "sm103_ptx.h"
@@ -61,11 +62,14 @@ constexpr int kThreads = (kWatchWarp + 1) * 32;
 constexpr int kPiece = 4096;                      // 32 rows of a tile
 constexpr int kEpiBytes = 2 * kPiece;             // an epilogue warp's buffer: hi and lo of a chunk, or hi of two
 constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiWarps * kEpiBytes;
+constexpr int kMaxParts = 8;  // of a Gram matrix's K
 constexpr unsigned kStatusWaitLimit = 2u;
 constexpr unsigned kFullMask = 0xffffffffu;
 
 struct Tile {
     int prob, b, i, j;
+    int part;   // of the K of the tile, where it is split
+    int index;  // of the tile among those of all matrices
 };
 
 template <int CG>
@@ -73,8 +77,14 @@ __device__ __forceinline__ Tile decode(const OrthoGemm &g, int t)
 {
     const int mt = (g.mblk + CG - 1) / CG, nt = (g.nblk + CG - 1) / CG;
     const int per = g.sym ? mt * (mt + 1) / 2 : mt * nt;
-    const int z = t / per, r = t - z * per;
     Tile x;
+    x.index = t;
+    x.part = 0;
+    if (CG == 1 && g.parts > 1) {
+        x.index = t / g.parts;
+        x.part = t - x.index * g.parts;
+    }
+    const int z = x.index / per, r = x.index - z * per;
     x.b = z / g.nprob;
     x.prob = z - x.b * g.nprob;
     if (g.sym) {
@@ -95,12 +105,19 @@ __device__ __forceinline__ Tile decode(const OrthoGemm &g, int t)
     return x;
 }
 
-// Tiles of one matrix.
+// Tiles of one matrix, each part of one counted.
 template <int CG>
 __host__ __device__ __forceinline__ int tile_count(const OrthoGemm &g)
 {
     const int mt = (g.mblk + CG - 1) / CG, nt = (g.nblk + CG - 1) / CG;
-    return (g.sym ? mt * (mt + 1) / 2 : mt * nt) * g.nprob;
+    return (g.sym ? mt * (mt + 1) / 2 : mt * nt) * g.nprob * g.parts;
+}
+
+// The first step of a part of K (pairs of CTAs take all of it).
+template <int CG>
+__device__ __forceinline__ int first_step(const OrthoGemm &g, int part)
+{
+    return CG == 2 || g.parts == 1 ? part * g.k64 : part * g.k64 / g.parts;
 }
 
 // A position in the sequence of all tiles.
@@ -217,7 +234,7 @@ constexpr bool kHasC = EPI != kEpiGram;
 // How C enters: hi times one factor; hi and lo times the row's factor; hi times
 // the row's and lo times the column's (EpilogueKind: dvec2); hi and lo times
 // the column's factor.
-enum CMode { kCHigh = 0, kCRow = 1, kCTwo = 2, kCCol = 3 };
+enum CMode { kCHigh = 0, kCRow = 1, kCTwo = 2, kCCol = 3, kCParts = 4 };
 
 // What a warp needs of a product's arguments, in registers.
 struct Local {
@@ -225,6 +242,7 @@ struct Local {
     const float *d_col;   // of the matrix; kCTwo, kCCol
     float *d_out;         // of the matrix; NULL: the diagonal stays
     __half *out_hi, *out_lo;  // out_lo NULL: only the high half is kept
+    int parts, slot, warp;    // of a Gram matrix: the first part's slot, the warp's place
 };
 
 __device__ __forceinline__ void put_bf16(uint32_t piece, int lane, int h, const float (&v)[32])
@@ -254,7 +272,10 @@ __device__ __forceinline__ float muon_weight(const OrthoPlan &plan, float th, fl
 
 // Writes a piece (32 rows from row0, 64 columns from gj) to the caller's
 // array, along the rows: eight lanes a row where vectors fit, else one row at a
-// time, 32 neighbouring columns together.
+// time, 32 neighbouring columns together.  More loads of a Muon step's weights
+// in flight would cost registers that all epilogues then spill to memory (four
+// rows and sixteen: 40 matrices of 1000 x 2187 1360 us instead of 1240, and the
+// Muon steps themselves 2 to 6 % longer).
 template <int EPI>
 __device__ __forceinline__ void write_rows(const OrthoPlan &plan, int b, int row0, int gj, int lane, uint32_t buf)
 {
@@ -264,53 +285,41 @@ __device__ __forceinline__ void write_rows(const OrthoPlan &plan, int b, int row
     const int lim = min(32, plan.rows - row0), n = plan.cols - gj;
     if (plan.vec && n >= 64) {
         const int c = lane & 7;
-        constexpr int kAtOnce = 4;
 #pragma unroll 1
-        for (int r0 = lane >> 3; r0 < 32; r0 += 4 * kAtOnce) {
-            uint32_t th[kAtOnce][8];
+        for (int r = lane >> 3; r < lim; r += 4) {
+            const int64_t at = at0 + r * next + c * 8;
+            uint32_t th[8];
+            if constexpr (EPI == kEpiMuon)
+                asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                             : "=r"(th[0]), "=r"(th[1]), "=r"(th[2]), "=r"(th[3]), "=r"(th[4]), "=r"(th[5]), "=r"(th[6]),
+                               "=r"(th[7])
+                             : "l"(plan.theta + at));
+            uint4 w = lds128(buf + r * 128 + ((c ^ (r & 7)) << 4));
             if constexpr (EPI == kEpiMuon) {
+                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                uint32_t y[4];
 #pragma unroll
-                for (int j = 0; j < kAtOnce; ++j)
-                    if (r0 + 4 * j < lim)
-                        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                                     : "=r"(th[j][0]), "=r"(th[j][1]), "=r"(th[j][2]), "=r"(th[j][3]), "=r"(th[j][4]),
-                                       "=r"(th[j][5]), "=r"(th[j][6]), "=r"(th[j][7])
-                                     : "l"(plan.theta + at0 + (r0 + 4 * j) * next + c * 8));
-            }
-#pragma unroll
-            for (int j = 0; j < kAtOnce; ++j) {
-                const int r = r0 + 4 * j;
-                if (r >= lim)
-                    continue;
-                uint4 w = lds128(buf + r * 128 + ((c ^ (r & 7)) << 4));
-                const int64_t at = at0 + r * next + c * 8;
-                if constexpr (EPI == kEpiMuon) {
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t y[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 o = unpack_half2(u[e]);
-                        const float p = muon_weight(plan, __uint_as_float(th[j][2 * e]), o.x);
-                        const float q = muon_weight(plan, __uint_as_float(th[j][2 * e + 1]), o.y);
-                        th[j][2 * e] = __float_as_uint(p);
-                        th[j][2 * e + 1] = __float_as_uint(q);
-                        const __nv_bfloat162 z = __floats2bfloat162_rn(p, q);
-                        y[e] = *reinterpret_cast<const uint32_t *>(&z);
-                    }
-                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(plan.theta + at),
-                                 "r"(th[j][0]), "r"(th[j][1]), "r"(th[j][2]), "r"(th[j][3]), "r"(th[j][4]), "r"(th[j][5]),
-                                 "r"(th[j][6]), "r"(th[j][7])
-                                 : "memory");
-                    w = make_uint4(y[0], y[1], y[2], y[3]);
+                for (int e = 0; e < 4; ++e) {
+                    const float2 o = unpack_half2(u[e]);
+                    const float p = muon_weight(plan, __uint_as_float(th[2 * e]), o.x);
+                    const float q = muon_weight(plan, __uint_as_float(th[2 * e + 1]), o.y);
+                    th[2 * e] = __float_as_uint(p);
+                    th[2 * e + 1] = __float_as_uint(q);
+                    const __nv_bfloat162 z = __floats2bfloat162_rn(p, q);
+                    y[e] = *reinterpret_cast<const uint32_t *>(&z);
                 }
-                *reinterpret_cast<uint4 *>(plan.w + at) = w;
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(plan.theta + at), "r"(th[0]),
+                             "r"(th[1]), "r"(th[2]), "r"(th[3]), "r"(th[4]), "r"(th[5]), "r"(th[6]), "r"(th[7])
+                             : "memory");
+                w = make_uint4(y[0], y[1], y[2], y[3]);
             }
+            *reinterpret_cast<uint4 *>(plan.w + at) = w;
         }
         return;
     }
-    constexpr int kAtOnce = 16;  // rows whose loads are in flight together
+    constexpr int kAtOnce = 8;  // rows whose loads are in flight together
 #pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2 * (32 / kAtOnce); ++i) {
         const int col = lane + 32 * (i & 1), r0 = (i >> 1) * kAtOnce;
         if (col >= n)
             continue;
@@ -348,6 +357,53 @@ __device__ __forceinline__ void read_half(uint32_t piece, int lane, int h, uint3
     }
 }
 
+// A tile of a Gram matrix whose K is split: each part's sums of a warp's 32 rows
+// x 64 columns, FP32, half after half, four columns of all lanes together.
+constexpr int kPartElems = 32 * 64;
+
+// Where a warp's lie: the slots of a matrix, of 128 x 128 values each, fill the
+// areas one after another.
+__device__ __forceinline__ float *part_at(const OrthoPlan &plan, int b, int slot, int warp)
+{
+    const int area = slot / plan.area_slots;
+    return plan.area[area] + b * plan.area_matrix + (int64_t)(slot - area * plan.area_slots) * (kEpiWarps * kPartElems) +
+           warp * kPartElems;
+}
+
+__device__ __forceinline__ void leave_part(float *to, int lane, uint32_t acc_addr)
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t acc[32];
+        tmem_load32(acc_addr + h * 32, acc);
+        tmem_wait_load();
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            __stcg(reinterpret_cast<uint4 *>(to) + (h * 8 + q) * 32 + lane,
+                   make_uint4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]));
+    }
+}
+
+// Half h of their sum, part after part.
+__device__ __forceinline__ void add_parts(const OrthoPlan &plan, const Local &k, int b, int lane, int h, uint32_t (&sum)[32])
+{
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+        sum[e] = 0u;
+#pragma unroll 2
+    for (int p = 0; p < k.parts; ++p) {
+        const float4 *from = reinterpret_cast<const float4 *>(part_at(plan, b, k.slot + p, k.warp)) + h * 256 + lane;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const float4 w = __ldcg(from + q * 32);
+            const float x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                sum[4 * q + e] = __float_as_uint(__uint_as_float(sum[4 * q + e]) + x[e]);
+        }
+    }
+}
+
 // One chunk: this warp's 32 rows (the lane's is gi) x 64 columns from gj on.
 // buf holds C (hi, and lo behind it) and is where results leave from; at: the
 // chunk's place in the operands, in values.
@@ -355,14 +411,17 @@ template <int EPI, int MODE>
 __device__ __forceinline__ void epilogue_chunk(const OrthoPlan &plan, const Local &k, int b, int gi, int gj, int lane,
                                                uint32_t acc_addr, uint32_t buf, int64_t at)
 {
-    uint32_t chi[kHasC<EPI> ? 16 : 1], clo[MODE == kCHigh ? 1 : 16];
+    uint32_t chi[kHasC<EPI> ? 16 : 1], clo[MODE == kCHigh || MODE == kCParts ? 1 : 16];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         uint32_t acc[32];
-        tmem_load32(acc_addr + h * 32, acc);
+        if constexpr (MODE == kCParts)
+            add_parts(plan, k, b, lane, h, acc);
+        else
+            tmem_load32(acc_addr + h * 32, acc);
         if constexpr (kHasC<EPI>)
             read_half(buf, lane, h, chi);
-        if constexpr (MODE != kCHigh)
+        if constexpr (MODE != kCHigh && MODE != kCParts)
             read_half(buf + kPiece, lane, h, clo);
         tmem_wait_load();
         float v[32];
@@ -553,7 +612,25 @@ __device__ __forceinline__ bool epilogue_tile(const OrthoPlan &plan, const Ortho
                 prefetch_theta(plan, x, ib * 128 + quad * 32, x.j * CG * 128 + c * 64, lane);
         bool ok = __all_sync(kFullMask, mbar_wait(smem_addr(&sh.acc_full[buf]), use & 1, &sh.abort));
         tmem_fence_after();
-        for (int c = c0; c < c1 && ok; c += 2) {
+        bool mine_to_do = true;
+        if constexpr (EPI == kEpiGram) {
+            k.parts = g.parts;
+            if (CG == 1 && k.parts > 1 && ok) {
+                // (c0 is the warp's only chunk.)  The last part to come adds
+                // them all up, in their order.
+                k.slot = (x.index - x.b * (g.mblk * (g.mblk + 1) / 2)) * g.parts;
+                k.warp = warp;
+                leave_part(part_at(plan, x.b, k.slot + x.part, warp), lane,
+                           tmem + ((uint32_t)(quad * 32) << 16) + buf * 128 * CG + c0 * 64);
+                __syncwarp();
+                unsigned before = 0;
+                if (lane == 0)
+                    before = add_acq_rel(plan.joined + x.index * kEpiWarps + warp, 1u);
+                mine_to_do = (int)(__shfl_sync(kFullMask, before, 0) % g.parts) == g.parts - 1;
+                __syncwarp();
+            }
+        }
+        for (int c = c0; c < c1 && ok && mine_to_do; c += 2) {
             const int i = both && c != c0;
             if constexpr (kHasC<EPI>)
                 ok = __all_sync(kFullMask, mbar_wait(smem_addr(&sh.c[warp][i]), (asked[i] - 1) & 1, &sh.abort));
@@ -562,6 +639,12 @@ __device__ __forceinline__ bool epilogue_tile(const OrthoPlan &plan, const Ortho
             const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + buf * 128 * CG + c * 64;
             const int gj = x.j * CG * 128 + c * 64;
             if constexpr (EPI == kEpiGram || EPI == kEpiPoly) {
+                if constexpr (CG == 1 && EPI == kEpiGram) {
+                    if (k.parts > 1) {
+                        epilogue_chunk<EPI, kCParts>(plan, k, x.b, gi, gj, lane, acc, mine + i * kPiece, place(c));
+                        continue;
+                    }
+                }
                 epilogue_chunk<EPI, kCHigh>(plan, k, x.b, gi, gj, lane, acc, mine + i * kPiece, place(c));
             } else if constexpr (EPI == kEpiSym) {
                 if (two)
@@ -645,7 +728,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_ortho_products(const __grid_con
             const __half *a = g.p[x.prob].a + (int64_t)x.b * g.a_stride;
             const __half *b = g.p[x.prob].b + (int64_t)x.b * g.b_stride;
             ok = clear_to_read(sh, n);
-            for (int k = 0; k < g.k64 && ok; ++k, ++it) {
+            const int k1 = first_step<CG>(g, x.part + 1);
+            for (int k = first_step<CG>(g, x.part); k < k1 && ok; ++k, ++it) {
                 const uint32_t s = it % kStages, ph = (it / kStages) & 1;
                 ok = __all_sync(kFullMask, mbar_wait(smem_addr(&sh.empty[s]), ph ^ 1, &sh.abort));
                 if (!ok)
@@ -682,7 +766,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_ortho_products(const __grid_con
                     break;
                 tmem_fence_after();
             }
-            for (int k = 0; k < g.k64; ++k, ++it) {
+            const int k0 = first_step<CG>(g, x.part), k1 = first_step<CG>(g, x.part + 1);
+            for (int k = k0; k < k1; ++k, ++it) {
                 const uint32_t s = it % kStages, ph = (it / kStages) & 1;
                 ok = mbar_wait(smem_addr(&sh.full[s]), ph, &sh.abort);
                 if (CG == 2 && rank == 0)
@@ -705,9 +790,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_ortho_products(const __grid_con
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         mma_f16<CG>(tmem + buf * 128 * CG, a_desc + j * a_step, b_desc + j * b_step, idesc,
-                                    k > 0 || j > 0);
+                                    k > k0 || j > 0);
                     mma_commit<CG>(smem_addr(&sh.empty[s]));
-                    if (k + 1 == g.k64)
+                    if (k + 1 == k1)
                         mma_commit<CG>(smem_addr(&sh.acc_full[buf]));
                 }
                 __syncwarp();
@@ -800,6 +885,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_ortho_products(const __grid_con
 
 constexpr int kMaxDevices = 64;
 
+// Splits K of the Gram matrices where their tiles leave CTAs without work.  A
+// step takes 0.33 us, the joining of parts 2 us and another 0.65 us a part (64
+// KiB read at the rate of one SM): best with sqrt(K / 2 steps) parts, from 24
+// steps on.  2 matrices of 238 x 14962 took 332 us without, 238 with it.
+void split_gram(OrthoPlan &plan, int groups)
+{
+    for (int f = 0; f < plan.n_phases; ++f) {
+        OrthoGemm &g = plan.ph[f];
+        if (g.epi != kEpiGram || plan.areas == 0 || g.k64 < 24)
+            continue;
+        const int tiles = tile_count<1>(g), all = tiles * plan.batch;
+        int parts = (int)std::sqrt(0.5 * g.k64);
+        parts = parts < kMaxParts ? parts : kMaxParts;
+        parts = parts < groups / all ? parts : groups / all;
+        parts = parts < plan.areas * plan.area_slots / tiles ? parts : plan.areas * plan.area_slots / tiles;
+        if (parts >= 2 && all <= kJoinTiles)
+            g.parts = parts;
+    }
+}
+
 template <int CG>
 cudaError_t launch(const OrthoPlan &plan, int groups, cudaStream_t stream)
 {
@@ -867,7 +972,7 @@ double steps(const OrthoPlan &plan, int groups)
     for (int f = 0; f < plan.n_phases; ++f) {
         const int t = tile_count<CG>(plan.ph[f]) * plan.batch;
         const double rounds = plan.batch == 1 ? (t + groups - 1) / groups : t > groups ? (double)t / groups : 1.0;
-        sum += rounds * plan.ph[f].k64;
+        sum += rounds * ((plan.ph[f].k64 + plan.ph[f].parts - 1) / plan.ph[f].parts);
     }
     return sum;
 }
@@ -889,9 +994,11 @@ cudaError_t launch_ortho_products(const OrthoPlan &plan, int device, cudaStream_
     // 128 x 128 0.33 us with every SM at it (both bound by what L2 delivers,
     // 15 TB/s): pairs do 3.3 times the work per step, but a matrix has four
     // times fewer tiles for them.
-    if (0.39 * steps<2>(plan, n2) <= 0.33 * steps<1>(plan, n1))
+    OrthoPlan split = plan;
+    split_gram(split, n1);
+    if (0.39 * steps<2>(plan, n2) <= 0.33 * steps<1>(split, n1))
         return launch<2>(plan, n2, stream);
-    return launch<1>(plan, n1, stream);
+    return launch<1>(split, n1, stream);
 }
 
 }  // namespace slide

@@ -68,15 +68,25 @@ struct OrthoGemm {
     int d_stride;            // floats of dvec per matrix
     int d_by_col;            // dvec scales columns
     float coef_a;
+    int parts;               // of K, set by the launch (1 in a plan): for kEpiGram, joined by the last CTA to come
 };
 
 constexpr int kMaxPhases = 32;  // products of one launch, one after the other
+constexpr int kJoinTiles = 80;  // most tiles, of all matrices, whose K is split: with two parts each they fill the SMs
+constexpr int kJoinWords = kJoinTiles * 8;
 
 struct OrthoPlan {
     OrthoGemm ph[kMaxPhases];
     int n_phases, batch;
     unsigned *status;
     unsigned *count;         // [n_phases][batch] CTAs' tiles written so far, zero at the start
+    unsigned *joined;        // [kJoinTiles][8] parts of a tile (a warp's rows and columns of it) so far, zero at the start
+    // for parts, memory that nothing else uses during a Gram phase of the same
+    // matrix: `areas` arrays (0: no splitting) of [batch] of area_slots times
+    // 128 x 128 floats, a matrix's area_matrix floats from the next one's
+    float *area[8];
+    int areas, area_slots;
+    int64_t area_matrix;
     // kEpiOut and kEpiMuon
     int rows, cols;
     uint16_t *w;

@@ -86,6 +86,14 @@ __device__ __forceinline__ void add_release(unsigned *p, unsigned v)
     asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
+// The old value: who adds sees what those that added before had written.
+__device__ __forceinline__ unsigned add_acq_rel(unsigned *p, unsigned v)
+{
+    unsigned old;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
+}
+
 // Add to a word of shared memory; the old value.  Orders like a barrier between
 // the threads of the CTA that meet in the word.
 __device__ __forceinline__ unsigned add_shared(uint32_t addr, unsigned v)

@@ -93,6 +93,23 @@ def test_factor(S, batch, rows, cols, dtype):
     assert off(orthogonalize(S, x), factor64(x)) <= FACTOR + BF16
 
 
+@pytest.mark.parametrize("batch,rows,cols", [(1, 129, 1535), (1, 129, 1537), (2, 238, 14962), (3, 2100, 300), (1, 6401, 513),
+                                             (25, 200, 2000), (26, 200, 2000), (1, 1025, 2085)])
+@pytest.mark.parametrize("more", [0, 11])
+def test_long_sides_of_few_tiles(S, batch, rows, cols, more):
+    """The sums over a long side taken apart among CTAs: right, and the same
+    bits each time (the parts are added in their order, whoever comes last).
+    The steps after the quintic's five draw the singular values to 1, where
+    their slope is 0, so they let no error grow."""
+    coeffs = [QUINTIC] * 5 + [(1.875, -1.25, 0.375)] * more
+    x = matrix(batch, rows, cols, rows + cols)
+    params = S.ortho_params(steps=5 + more, coeffs=coeffs)
+    first = orthogonalize(S, x, params)
+    assert off(first, factor64(x, 5 + more, coeffs)) <= FACTOR + BF16
+    for _ in range(5):
+        assert torch.equal(orthogonalize(S, x, params).view(torch.int16), first.view(torch.int16))
+
+
 @pytest.mark.parametrize("rows,cols", [(33, 33), (100, 300), (257, 256), (640, 200), (384, 1500)])
 @pytest.mark.parametrize("kind", ["flat", "one value"])
 def test_spectra(S, rows, cols, kind):
