@@ -476,8 +476,8 @@ SLIDE_API slide_status slide_streamed_timeline(slide_state *st, double *out, int
  *   mom and th are FP32 and updated in place; momentum's and theta's lines are
  *   one FP32 operation each, the scalars formed in double and rounded once.
  *   The products run on FP16 operands (scaled by powers of two) with FP32
- *   accumulators, and the diagonals of the left factors and the iterate itself
- *   stay in FP32.  Against the polynomial in 64 bits (2-norm of the difference
+ *   accumulators; the diagonals of the left factors stay in FP32 and act on the
+ *   iterate in 22 bits.  Against the polynomial in 64 bits (2-norm of the difference
  *   over 2-norm) X is off by 5e-4 to 1.3e-3 for gradients' spectra, from noise
  *   to a few strong directions, and by up to 3e-2 for a matrix of one repeated
  *   value, whose roundings all have one sign.

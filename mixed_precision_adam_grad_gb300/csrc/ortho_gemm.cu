@@ -2,8 +2,9 @@
 // fifth-generation tensor cores (tcgen05, accumulators in tensor memory).
 //
 // Each product is D = A*B with FP16 operands and FP32 accumulators, followed
-// by an epilogue that adds the FP32 part of the iterate and forms the operands
-// of the next product (slide_ortho.h lists them).  All operands lie in the
+// by an epilogue that adds the diagonal's part of the left factor times the
+// iterate and forms the operands of the next product (slide_ortho.h lists
+// them).  All operands lie in the
 // tiled layouts of slide_ortho.h, so the producer needs plain bulk copies
 // only.
 //
@@ -37,7 +38,7 @@
 // each operand is stored times a power of two that keeps it in range.  What is
 // rounded enters the result only through a product with off-diagonal values:
 // the diagonal of every left factor is kept apart in FP32 and applied to the
-// FP32 copy of the iterate.  Off by 5e-4 to 1.2e-3 (2-norm over 2-norm) from
+// iterate's full 22 bits.  Off by 5e-4 to 1.2e-3 (2-norm over 2-norm) from
 // the polynomial in 64 bits for spectra from flat to a single spike, where
 // BF16 operands are 1e-2 to 1e-1 off.
 #include <cuda_bf16.h>
