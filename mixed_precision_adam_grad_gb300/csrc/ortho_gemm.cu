@@ -172,6 +172,13 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr)
     return v;
 }
 
+__device__ __forceinline__ float lds32(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ uint16_t lds16(uint32_t addr)
 {
     uint16_t v;
@@ -273,10 +280,11 @@ __device__ __forceinline__ float muon_weight(const OrthoPlan &plan, float th, fl
 
 // Writes a piece (32 rows from row0, 64 columns from gj) to the caller's
 // array, along the rows: eight lanes a row where vectors fit, else one row at a
-// time, 32 neighbouring columns together.  More loads of a Muon step's weights
-// in flight would cost registers that all epilogues then spill to memory (four
-// rows and sixteen: 40 matrices of 1000 x 2187 1360 us instead of 1240, and the
-// Muon steps themselves 2 to 6 % longer).
+// time, 32 neighbouring columns together.  A Muon step's weights come through
+// the place behind the piece, 16 rows at a time: that many loads in flight take
+// no registers.  (Four rows and sixteen in registers made all epilogues spill
+// them to memory, 40 matrices of 1000 x 2187 took 1360 us instead of 1235; one
+// row and eight 464 us instead of 449 for a Muon step of 7 of 1001 x 2731.)
 template <int EPI>
 __device__ __forceinline__ void write_rows(const OrthoPlan &plan, int b, int row0, int gj, int lane, uint32_t buf)
 {
@@ -284,67 +292,67 @@ __device__ __forceinline__ void write_rows(const OrthoPlan &plan, int b, int row
     const int64_t at0 = EPI == kEpiMuon ? ((int64_t)b * plan.rows + row0) * plan.cols + gj
                                         : (int64_t)b * plan.w_batch + (int64_t)row0 * plan.w_row + gj;
     const int lim = min(32, plan.rows - row0), n = plan.cols - gj;
-    if (plan.vec && n >= 64) {
-        const int c = lane & 7;
+    const bool vec = plan.vec && n >= 64;
+    constexpr int kAtOnce = 16;
+    const uint32_t stage = buf + kPiece;  // [kAtOnce][64] floats, each written and read by the same lane
 #pragma unroll 1
-        for (int r = lane >> 3; r < lim; r += 4) {
-            const int64_t at = at0 + r * next + c * 8;
-            uint32_t th[8];
-            if constexpr (EPI == kEpiMuon)
-                asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                             : "=r"(th[0]), "=r"(th[1]), "=r"(th[2]), "=r"(th[3]), "=r"(th[4]), "=r"(th[5]), "=r"(th[6]),
-                               "=r"(th[7])
-                             : "l"(plan.theta + at));
-            uint4 w = lds128(buf + r * 128 + ((c ^ (r & 7)) << 4));
+    for (int r0 = 0; r0 < lim; r0 += kAtOnce) {
+        const int r1 = min(kAtOnce, lim - r0);
+        if (vec) {
+            const int c = lane & 7;
             if constexpr (EPI == kEpiMuon) {
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                uint32_t y[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 o = unpack_half2(u[e]);
-                    const float p = muon_weight(plan, __uint_as_float(th[2 * e]), o.x);
-                    const float q = muon_weight(plan, __uint_as_float(th[2 * e + 1]), o.y);
-                    th[2 * e] = __float_as_uint(p);
-                    th[2 * e + 1] = __float_as_uint(q);
-                    const __nv_bfloat162 z = __floats2bfloat162_rn(p, q);
-                    y[e] = *reinterpret_cast<const uint32_t *>(&z);
+                for (int r = lane >> 3; r < r1; r += 4) {
+                    const float *th = plan.theta + at0 + (r0 + r) * next + c * 8;
+                    copy_async16(stage + r * 256 + c * 32, th);
+                    copy_async16(stage + r * 256 + c * 32 + 16, th + 4);
                 }
-                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(plan.theta + at), "r"(th[0]),
-                             "r"(th[1]), "r"(th[2]), "r"(th[3]), "r"(th[4]), "r"(th[5]), "r"(th[6]), "r"(th[7])
-                             : "memory");
-                w = make_uint4(y[0], y[1], y[2], y[3]);
+                copy_async_wait();
             }
-            *reinterpret_cast<uint4 *>(plan.w + at) = w;
-        }
-        return;
-    }
-    constexpr int kAtOnce = 8;  // rows whose loads are in flight together
-#pragma unroll 1
-    for (int i = 0; i < 2 * (32 / kAtOnce); ++i) {
-        const int col = lane + 32 * (i & 1), r0 = (i >> 1) * kAtOnce;
-        if (col >= n)
-            continue;
-        float *th = EPI == kEpiMuon ? plan.theta + at0 + r0 * next + col : nullptr;
-        uint16_t *w = plan.w + at0 + r0 * next + col;
-        const uint32_t at = buf + r0 * 128 + (lane & 7) * 2;
-        const int c = col >> 3;
-        float old[kAtOnce];
-        if constexpr (EPI == kEpiMuon) {
+            for (int r = lane >> 3; r < r1; r += 4) {
+                const int64_t at = at0 + (r0 + r) * next + c * 8;
+                uint4 w = lds128(buf + (r0 + r) * 128 + ((c ^ (r & 7)) << 4));
+                if constexpr (EPI == kEpiMuon) {
+                    const uint4 lo = lds128(stage + r * 256 + c * 32), hi = lds128(stage + r * 256 + c * 32 + 16);
+                    uint32_t th[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t y[4];
 #pragma unroll
-            for (int r = 0; r < kAtOnce; ++r)
-                old[r] = r0 + r < lim ? __ldcs(th + r * next) : 0.0f;
-        }
-#pragma unroll
-        for (int r = 0; r < kAtOnce; ++r) {
-            uint16_t u = lds16(at + r * 128 + ((c ^ (r & 7)) << 4));
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 o = unpack_half2(u[e]);
+                        const float p = muon_weight(plan, __uint_as_float(th[2 * e]), o.x);
+                        const float q = muon_weight(plan, __uint_as_float(th[2 * e + 1]), o.y);
+                        th[2 * e] = __float_as_uint(p);
+                        th[2 * e + 1] = __float_as_uint(q);
+                        const __nv_bfloat162 z = __floats2bfloat162_rn(p, q);
+                        y[e] = *reinterpret_cast<const uint32_t *>(&z);
+                    }
+                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(plan.theta + at),
+                                 "r"(th[0]), "r"(th[1]), "r"(th[2]), "r"(th[3]), "r"(th[4]), "r"(th[5]), "r"(th[6]), "r"(th[7])
+                                 : "memory");
+                    w = make_uint4(y[0], y[1], y[2], y[3]);
+                }
+                *reinterpret_cast<uint4 *>(plan.w + at) = w;
+            }
+        } else {
             if constexpr (EPI == kEpiMuon) {
-                const float p = muon_weight(plan, old[r], __half2float(__ushort_as_half(u)));
-                u = __bfloat16_as_ushort(__float2bfloat16_rn(p));
-                if (r0 + r < lim)
-                    __stcs(th + r * next, p);
+                for (int col = lane; col < min(n, 64); col += 32)
+                    for (int r = 0; r < r1; ++r)
+                        copy_async4(stage + r * 256 + col * 4, plan.theta + at0 + (r0 + r) * next + col);
+                copy_async_wait();
             }
-            if (r0 + r < lim)
-                w[r * next] = u;
+            for (int col = lane; col < min(n, 64); col += 32) {
+#pragma unroll 4
+                for (int r = 0; r < r1; ++r) {
+                    const int64_t at = at0 + (r0 + r) * next + col;
+                    uint16_t u = lds16(buf + (r0 + r) * 128 + (((col >> 3) ^ (r & 7)) << 4) + (lane & 7) * 2);
+                    if constexpr (EPI == kEpiMuon) {
+                        const float p = muon_weight(plan, lds32(stage + r * 256 + col * 4), __half2float(__ushort_as_half(u)));
+                        u = __bfloat16_as_ushort(__float2bfloat16_rn(p));
+                        __stcs(plan.theta + at, p);
+                    }
+                    plan.w[at] = u;
+                }
+            }
         }
     }
 }
@@ -405,7 +413,11 @@ __device__ __forceinline__ void add_parts(const OrthoPlan &plan, const Local &k,
     }
 }
 
-// One chunk: this warp's 32 rows (the lane's is gi) x 64 columns from gj on.
+// One chunk: this warp's 32 rows (the lane's is gi) x 64 columns from gj on, in
+// two halves; a loop, not unrolled, since a CTA that comes to a phase for a
+// tile or two waits for its instructions (2 matrices of 1024 x 2560 234 us
+// unrolled, 221 as a loop; a single piece of code for all kinds of epilogues
+// again 230).
 // buf holds C (hi, and lo behind it) and is where results leave from; at: the
 // chunk's place in the operands, in values.
 template <int EPI, int MODE>
@@ -413,7 +425,7 @@ __device__ __forceinline__ void epilogue_chunk(const OrthoPlan &plan, const Loca
                                                uint32_t acc_addr, uint32_t buf, int64_t at)
 {
     uint32_t chi[kHasC<EPI> ? 16 : 1], clo[MODE == kCHigh || MODE == kCParts ? 1 : 16];
-#pragma unroll
+#pragma unroll 1
     for (int h = 0; h < 2; ++h) {
         uint32_t acc[32];
         if constexpr (MODE == kCParts)

@@ -154,6 +154,20 @@ __device__ __forceinline__ bool shared_wait(uint32_t addr, unsigned target, vola
     return false;
 }
 
+// Copies of 4 or 16 bytes to shared memory that go past the registers, and the
+// wait for all of this thread's.
+__device__ __forceinline__ void copy_async4(uint32_t dst_smem, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst_smem), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void copy_async16(uint32_t dst_smem, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst_smem), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // 1-D bulk copies: global -> shared (completes `bytes` on the mbarrier) and
 // shared -> global (in this thread's bulk group).  16-byte aligned, sizes
 // multiples of 16.
