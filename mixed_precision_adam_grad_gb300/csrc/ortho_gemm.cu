@@ -69,8 +69,9 @@ constexpr unsigned kFullMask = 0xffffffffu;
 
 struct Tile {
     int prob, b, i, j;
+    int half;   // of the tile's columns, where it is narrow
     int part;   // of the K of the tile, where it is split
-    int index;  // of the tile among those of all matrices
+    int index;  // of the tile among those of all matrices (halves and parts not counted)
 };
 
 template <int CG>
@@ -80,10 +81,14 @@ __device__ __forceinline__ Tile decode(const OrthoGemm &g, int t)
     const int per = g.sym ? mt * (mt + 1) / 2 : mt * nt;
     Tile x;
     x.index = t;
-    x.part = 0;
+    x.part = x.half = 0;
     if (CG == 1 && g.parts > 1) {
         x.index = t / g.parts;
         x.part = t - x.index * g.parts;
+    }
+    if (CG == 1 && g.narrow) {
+        x.half = x.index & 1;
+        x.index >>= 1;
     }
     const int z = x.index / per, r = x.index - z * per;
     x.b = z / g.nprob;
@@ -106,12 +111,12 @@ __device__ __forceinline__ Tile decode(const OrthoGemm &g, int t)
     return x;
 }
 
-// Tiles of one matrix, each part of one counted.
+// Tiles of one matrix, each half and part of one counted.
 template <int CG>
 __host__ __device__ __forceinline__ int tile_count(const OrthoGemm &g)
 {
     const int mt = (g.mblk + CG - 1) / CG, nt = (g.nblk + CG - 1) / CG;
-    return (g.sym ? mt * (mt + 1) / 2 : mt * nt) * g.nprob * g.parts;
+    return (g.sym ? mt * (mt + 1) / 2 : mt * nt) * g.nprob * g.parts * (g.narrow ? 2 : 1);
 }
 
 // The first step of a part of K (pairs of CTAs take all of it).
@@ -149,7 +154,16 @@ __device__ __forceinline__ bool reads_mn(int kind, int t, int k)
     return kind == kOperandSym ? (k >> 1) <= CG * t : kind == kOperandMN;
 }
 
-// Copy the 128 x 64 operand block (blk along M or N, step k) into a slot.
+// Copy the 128 x 64 operand block (blk along M or N, step k) into a slot, or of
+// a narrow tile's B half of it, 64 x 64.
+__device__ __forceinline__ void load_half_operand(uint32_t slot, const __half *m, int c64, int blk, int half, int k,
+                                                  bool mn, uint32_t bar)
+{
+    const __half *t = mn ? m + ((int64_t)(k >> 1) * c64 + 2 * blk + half) * kTileElems + (k & 1) * (kTileElems / 2)
+                         : m + ((int64_t)blk * c64 + k) * kTileElems + half * (kTileElems / 2);
+    bulk_load(slot, t, kSlot / 2, bar);
+}
+
 __device__ __forceinline__ void load_operand(uint32_t slot, const __half *m, int c64, int blk, int k, bool mn,
                                              uint32_t bar)
 {
@@ -554,8 +568,11 @@ __device__ __forceinline__ bool epilogue_tile(const OrthoPlan &plan, const Ortho
                                               uint32_t tmem, uint32_t mine, int warp, int lane, uint32_t rank, uint32_t n,
                                               uint32_t (&asked)[2])
 {
-    // warp (quad, half): rows 32*quad.., every second chunk of 64 columns
-    const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
+    // warp (quad, half): rows 32*quad.., every second chunk of 64 columns; the
+    // one chunk of a narrow tile is every second tile's for the same four warps
+    const int quad = warp & 3, row = quad * 32 + lane;
+    const bool narrow = CG == 1 && g.narrow;
+    const int half = narrow ? x.half : warp >> 2, place_of = quad + 4 * half;
     {
         const OrthoProduct &p = g.p[x.prob];
         const uint32_t buf = n & 1, use = n >> 1;
@@ -563,7 +580,7 @@ __device__ __forceinline__ bool epilogue_tile(const OrthoPlan &plan, const Ortho
         // the chunks of the tile that exist (and, of a symmetric result, are
         // kept): c0 and c0 + 2
         const int c0 = (g.sym ? max(0, 2 * (ib - x.j * CG)) : 0) + half;
-        const int c1 = ib < g.mblk ? min(2 * CG, 2 * (g.nblk - x.j * CG)) : 0;
+        const int c1 = ib < g.mblk && !(narrow && (warp >> 2) != (int)(n & 1)) ? min(2 * CG, 2 * (g.nblk - x.j * CG)) : 0;
         const bool has_lo = kHasC<EPI> && EPI != kEpiPoly && p.c.lo != nullptr;
         // both chunks fit side by side if they have no low halves
         const bool both = EPI == kEpiPoly || (EPI == kEpiSym && !has_lo && !p.out.lo);
@@ -628,17 +645,17 @@ __device__ __forceinline__ bool epilogue_tile(const OrthoPlan &plan, const Ortho
         bool mine_to_do = true;
         if constexpr (EPI == kEpiGram) {
             k.parts = g.parts;
-            if (CG == 1 && k.parts > 1 && ok) {
+            if (CG == 1 && k.parts > 1 && ok && c0 < c1) {
                 // (c0 is the warp's only chunk.)  The last part to come adds
                 // them all up, in their order.
                 k.slot = (x.index - x.b * (g.mblk * (g.mblk + 1) / 2)) * g.parts;
-                k.warp = warp;
-                leave_part(part_at(plan, x.b, k.slot + x.part, warp), lane,
-                           tmem + ((uint32_t)(quad * 32) << 16) + buf * 128 * CG + c0 * 64);
+                k.warp = place_of;
+                leave_part(part_at(plan, x.b, k.slot + x.part, place_of), lane,
+                           tmem + ((uint32_t)(quad * 32) << 16) + buf * 128 * CG + (narrow ? 0 : c0) * 64);
                 __syncwarp();
                 unsigned before = 0;
                 if (lane == 0)
-                    before = add_acq_rel(plan.joined + x.index * kEpiWarps + warp, 1u);
+                    before = add_acq_rel(plan.joined + x.index * kEpiWarps + place_of, 1u);
                 mine_to_do = (int)(__shfl_sync(kFullMask, before, 0) % g.parts) == g.parts - 1;
                 __syncwarp();
             }
@@ -649,7 +666,7 @@ __device__ __forceinline__ bool epilogue_tile(const OrthoPlan &plan, const Ortho
                 ok = __all_sync(kFullMask, mbar_wait(smem_addr(&sh.c[warp][i]), (asked[i] - 1) & 1, &sh.abort));
             if (!ok)
                 break;
-            const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + buf * 128 * CG + c * 64;
+            const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + buf * 128 * CG + (narrow ? 0 : c) * 64;
             const int gj = x.j * CG * 128 + c * 64;
             if constexpr (EPI == kEpiGram || EPI == kEpiPoly) {
                 if constexpr (CG == 1 && EPI == kEpiGram) {
@@ -750,9 +767,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_ortho_products(const __grid_con
                 const uint32_t bar = smem_addr(&sh.full[s]), slot = ring + s * kStageBytes;
                 const bool a_mn = reads_mn<CG>(g.a_kind, x.i, k), b_mn = reads_mn<CG>(g.b_kind, x.j, k);
                 if (elect_one()) {
-                    mbar_expect_tx(bar, kStageBytes);
+                    mbar_expect_tx(bar, CG == 1 && g.narrow ? kSlot + kSlot / 2 : kStageBytes);
                     load_operand(slot, a, g.a_c64, x.i * CG + rank, k, a_mn, bar);
-                    load_operand(slot + kSlot, b, g.b_c64, x.j * CG + rank, k, b_mn, bar);
+                    if (CG == 1 && g.narrow)
+                        load_half_operand(slot + kSlot, b, g.b_c64, x.j, x.half, k, b_mn, bar);
+                    else
+                        load_operand(slot + kSlot, b, g.b_c64, x.j * CG + rank, k, b_mn, bar);
                 }
                 __syncwarp();
             }
@@ -795,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ortho_products(const __grid_con
                     continue;
                 }
                 const bool a_mn = reads_mn<CG>(g.a_kind, x.i, k), b_mn = reads_mn<CG>(g.b_kind, x.j, k);
-                const uint32_t idesc = f16_idesc(128 * CG, 128 * CG, a_mn, b_mn);
+                const uint32_t idesc = f16_idesc(128 * CG, CG == 1 && g.narrow ? 64 : 128 * CG, a_mn, b_mn);
                 const uint32_t slot = ring + s * kStageBytes;
                 const uint64_t a_desc = operand_desc(slot, kSlot / 2), b_desc = operand_desc(slot + kSlot, kSlot / 2);
                 const uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
@@ -918,6 +938,17 @@ void split_gram(OrthoPlan &plan, int groups)
     }
 }
 
+// Halves the tiles of phases that leave two thirds of the CTAs without work all
+// the same: less to load for a step and half the epilogue, whose time is that of
+// its instructions.  A Muon step of 228 x 705 took 134 us without, 122 with it,
+// 300 x 8000 157 and 147; with 72 tiles of 152 (2 matrices of 1024 x 2560) it
+// gains nothing (222 and 224).
+void narrow_tiles(OrthoPlan &plan, int groups)
+{
+    for (int f = 0; f < plan.n_phases; ++f)
+        plan.ph[f].narrow = 3 * tile_count<1>(plan.ph[f]) * plan.batch <= groups;
+}
+
 template <int CG>
 cudaError_t launch(const OrthoPlan &plan, int groups, cudaStream_t stream)
 {
@@ -985,7 +1016,7 @@ double steps(const OrthoPlan &plan, int groups)
     for (int f = 0; f < plan.n_phases; ++f) {
         const int t = tile_count<CG>(plan.ph[f]) * plan.batch;
         const double rounds = plan.batch == 1 ? (t + groups - 1) / groups : t > groups ? (double)t / groups : 1.0;
-        sum += rounds * ((plan.ph[f].k64 + plan.ph[f].parts - 1) / plan.ph[f].parts);
+        sum += rounds * ((plan.ph[f].k64 + plan.ph[f].parts - 1) / plan.ph[f].parts) * (plan.ph[f].narrow ? 0.76 : 1.0);
     }
     return sum;
 }
@@ -1009,6 +1040,7 @@ cudaError_t launch_ortho_products(const OrthoPlan &plan, int device, cudaStream_
     // times fewer tiles for them.
     OrthoPlan split = plan;
     split_gram(split, n1);
+    narrow_tiles(split, n1);
     if (0.39 * steps<2>(plan, n2) <= 0.33 * steps<1>(split, n1))
         return launch<2>(plan, n2, stream);
     return launch<1>(split, n1, stream);

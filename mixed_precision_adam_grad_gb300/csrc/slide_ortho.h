@@ -69,6 +69,7 @@ struct OrthoGemm {
     int d_by_col;            // dvec scales columns
     float coef_a;
     int parts;               // of K, set by the launch (1 in a plan): for kEpiGram, joined by the last CTA to come
+    int narrow;              // tiles of 128 x 64 instead of 128 x 128, set by the launch (0 in a plan)
 };
 
 constexpr int kMaxPhases = 32;  // products of one launch, one after the other
