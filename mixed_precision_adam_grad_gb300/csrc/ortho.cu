@@ -49,9 +49,11 @@ struct SourceArgs {
     int rows, cols;
     int rblk, cblk;           // blocks of 128
     int vec;                  // rows can be read eight values at a time
+    int vec4;                 // BF16: four at a time
     // Muon step only: contiguous
     float *mom, *u;
     float mu, one_minus_mu;
+    float inv_r;              // 1/R where that is exact (a division of zeros takes long), else 0
     int nesterov;
     double *parts;            // [batch][kNormParts]
     unsigned *status, *count, *joined;
@@ -135,7 +137,7 @@ __device__ __forceinline__ void load_vec(const float *p, float (&v)[V])
 // One value of a Muon step: the replicas' mean into the momentum, the update.
 __device__ __forceinline__ float muon_value(const SourceArgs &a, float sum, float &m)
 {
-    const float g = __fmul_rn(a.one_minus_mu, __fdiv_rn(sum, (float)a.R));
+    const float g = __fmul_rn(a.one_minus_mu, a.inv_r > 0.0f ? sum * a.inv_r : __fdiv_rn(sum, (float)a.R));
     m = __fadd_rn(__fmul_rn(m, a.mu), g);
     return a.nesterov ? __fadd_rn(__fmul_rn(m, a.mu), g) : m;
 }
@@ -811,9 +813,11 @@ cudaError_t enqueue_small(const Shape &s, const Work &w, const Schedule &sc, con
     o.tall = s.tall;
     o.fp32 = fp32;
     o.muon = muon;
-    o.vec = a.vec;
+    o.vec = a.vec ? 1 : a.vec4 ? kVecHalves : 0;
+    o.mom_vec = s.cols % 4 == 0;
     o.mom = a.mom;
     o.u = w.small_u;
+    o.inv_r = a.inv_r;
     o.mu = a.mu;
     o.one_minus_mu = a.one_minus_mu;
     o.nesterov = a.nesterov;
@@ -1028,6 +1032,7 @@ extern "C" slide_status slide_orthogonalize(int32_t batch, int32_t rows, int32_t
     a.batch_stride = x_batch_stride;
     const int64_t per16 = x_type == SLIDE_TYPE_FP32 ? 4 : 8;  // elements of 16 bytes
     a.vec = !misaligned(x, 16) && x_row_stride % per16 == 0 && (batch == 1 || x_batch_stride % per16 == 0);
+    a.vec4 = x_type == SLIDE_TYPE_BF16 && !misaligned(x, 8) && x_row_stride % 4 == 0 && (batch == 1 || x_batch_stride % 4 == 0);
     Finish f{};
     f.epi = kEpiOut;
     f.w = (uint16_t *)bf16_out;
@@ -1085,10 +1090,12 @@ extern "C" slide_status slide_muon_step(int32_t batch, int32_t rows, int32_t col
     a.row_stride = cols;
     a.batch_stride = (int64_t)rows * cols;
     a.mom = momentum;
+    a.inv_r = (n_replicas & (n_replicas - 1)) == 0 ? 1.0f / (float)n_replicas : 0.0f;
     a.mu = hp->momentum;
     a.one_minus_mu = (float)(1.0 - (double)hp->momentum);
     a.nesterov = hp->nesterov != 0;
     a.vec = cols % (grads_type == SLIDE_TYPE_FP32 ? 4 : 8) == 0;
+    a.vec4 = grads_type == SLIDE_TYPE_BF16 && cols % 4 == 0;
     Finish f{};
     f.epi = kEpiMuon;
     f.w = (uint16_t *)bf16_out;

@@ -58,12 +58,18 @@ __device__ __forceinline__ float widen(float x) { return x; }
 
 // Values at .. at+7 of a row, of which n lie inside it (zero beyond).
 template <typename T>
-__device__ __forceinline__ void load8(const void *base, int64_t at, int n, bool vec, float (&v)[8])
+__device__ __forceinline__ void load8(const void *base, int64_t at, int n, int vec, float (&v)[8])
 {
     const T *p = static_cast<const T *>(base) + at;
     if (vec && n >= 8) {
         if constexpr (sizeof(T) == 2) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(p);
+            uint4 w;
+            if (vec == kVecHalves) {
+                const uint2 x = reinterpret_cast<const uint2 *>(p)[0], y = reinterpret_cast<const uint2 *>(p)[1];
+                w = make_uint4(x.x, x.y, y.x, y.y);
+            } else {
+                w = *reinterpret_cast<const uint4 *>(p);
+            }
             const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -162,45 +168,10 @@ __device__ __forceinline__ void wait_products(Base &b, int i, uint32_t parity, u
 
 // ---- 1: the Gram matrix ---------------------------------------------------------
 
-// Chunk (row, eight columns) of the matrix; a Muon step forms the update there
-// and writes it and the momentum.
-template <typename T, bool MUON>
-__device__ __forceinline__ void load_chunk(const SmallOrtho &a, int b, int row, int col, float (&v)[8])
-{
-    const int n = a.cols - col;
-    if (row >= a.rows || n <= 0) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] = 0.0f;
-        return;
-    }
-    const int64_t at = (int64_t)b * a.batch_stride + (int64_t)row * a.row_stride + col;
-    load8<T>(a.g.p[0], at, n, a.vec, v);
-    if constexpr (MUON) {
-        float m[8];
-        load8<float>(a.mom, at, n, a.vec, m);
-        for (int k = 1; k < a.R; ++k) {
-            float w[8];
-            load8<T>(a.g.p[k], at, n, a.vec, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[e] = __fadd_rn(v[e], w[e]);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float g = __fmul_rn(a.one_minus_mu, __fdiv_rn(v[e], (float)a.R));
-            m[e] = __fadd_rn(__fmul_rn(m[e], a.mu), g);
-            v[e] = a.nesterov ? __fadd_rn(__fmul_rn(m[e], a.mu), g) : m[e];
-        }
-        store8(a.mom + at, n, a.vec, m);
-        store8(a.u + at, n, a.vec, v);
-    }
-}
-
 // Grid: (8 * n_parts, batch), clusters of 8 along x.  A step takes 64 of the
 // long side.  PAIR: the values need a second BF16.
 template <typename T, bool MUON>
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
+__global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCluster, 1, 1)
     k_small_gram(const __grid_constant__ SmallOrtho a)
 {
     constexpr bool kPair = sizeof(T) == 4 || MUON;
@@ -220,48 +191,111 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
     const uint32_t idesc = idesc_of(n16, a.tall, a.tall, true);
     const int mchunks = (a.m + 7) / 8;  // chunks along the short side (tall)
 
-    // chunk i of a step: wide: row i >> 3, columns 8*(i & 7); tall: row i >> 4, columns 8*(i & 15)
-    float v[4][8];
-    int place[4];
+    // Chunk number tid + j*kThreads of step k, of 8 a row (16 if tall with m >
+    // 64); n: how many of its eight values exist (0 or less: none).  place: in
+    // the stage, negative where nothing is put (what lies in rows beyond n16
+    // reaches only rows of the result that nobody reads).
+    const int row_shift = a.tall && a.m > 64 ? 4 : 3, per_thread = a.m > 64 ? 4 : 2;
+    struct Chunk {
+        int64_t at;
+        int n, place;
+    };
+    auto chunk = [&](int k, int j) {
+        const int i = tid + j * kThreads, r = i >> row_shift, c = i & ((1 << row_shift) - 1);
+        const int row = a.tall ? k * 64 + r : r, col = a.tall ? c * 8 : k * 64 + c * 8;
+        Chunk x;
+        if (a.tall)
+            x.place = c < ((mchunks + 7) & ~7) ? (c >> 3) * (kTile / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4) : -1;
+        else
+            x.place = r < (int)n16 ? r * 128 + ((c ^ (r & 7)) << 4) : -1;
+        x.n = x.place >= 0 && row < a.rows ? a.cols - col : 0;
+        x.at = (int64_t)b * a.batch_stride + (int64_t)row * a.row_stride + col;
+        return x;
+    };
+    auto put = [&](uint32_t stage, int place, const float (&v)[8]) {
+        if (place < 0)
+            return;
+        uint4 hi, lo;
+        split8<true>(v, hi, lo);
+        sts128(stage + place, hi);
+        if constexpr (kPair)
+            sts128(stage + kTile + place, lo);
+    };
+    // A Muon step forms the update on the way, and writes it and the momentum:
+    // a chunk at a time, in a loop, what the next step reads on its way into L2
+    // meanwhile.  (All four at once in registers took longer, the instructions
+    // had to be fetched: a step of six of 18 x 3696 61 us instead of 35.)
+    auto muon_step = [&](int k, uint32_t stage) {
+#pragma unroll 1
+        for (int j = 0; j < per_thread && (a.tall || j * 32 < (int)n16); ++j) {
+            const Chunk x = chunk(k, j);
+            float v[8], m[8];
+            load8<T>(a.g.p[0], x.at, x.n, a.vec, v);
+            load8<float>(a.mom, x.at, x.n, a.mom_vec, m);
+#pragma unroll 1
+            for (int r = 1; r < a.R; ++r) {
+                float w[8];
+                load8<T>(a.g.p[r], x.at, x.n, a.vec, w);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int i = tid + j * kThreads;
-        if (a.tall) {
-            const int r = i >> 4, c = i & 15;
-            place[j] = c < ((mchunks + 7) & ~7) ? (c >> 3) * (kTile / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4) : -1;
-        } else {
-            const int r = i >> 3, c = i & 7;
-            place[j] = r * 128 + ((c ^ (r & 7)) << 4);
+                for (int e = 0; e < 8; ++e)
+                    v[e] = __fadd_rn(v[e], w[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float g = __fmul_rn(a.one_minus_mu, a.inv_r > 0.0f ? v[e] * a.inv_r : __fdiv_rn(v[e], (float)a.R));
+                m[e] = __fadd_rn(__fmul_rn(m[e], a.mu), g);
+                v[e] = a.nesterov ? __fadd_rn(__fmul_rn(m[e], a.mu), g) : m[e];
+            }
+            store8(a.mom + x.at, x.n, a.mom_vec, m);
+            store8(a.u + x.at, x.n, a.mom_vec, v);
+            put(stage, x.place, v);
         }
-    }
+    };
+    auto muon_prefetch = [&](int k) {
+#pragma unroll 1
+        for (int j = 0; j < per_thread; ++j) {
+            const Chunk x = chunk(k, j);
+            if (x.n <= 0)
+                continue;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(a.mom + x.at));
+#pragma unroll 1
+            for (int r = 0; r < a.R; ++r)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const T *>(a.g.p[r]) + x.at));
+        }
+    };
+    float v[4][8];  // of the next step (not for a Muon step)
     auto load_step = [&](int k) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int i = tid + j * kThreads;
-            if (place[j] >= 0)
-                load_chunk<T, MUON>(a, b, a.tall ? k * 64 + (i >> 4) : i >> 3, a.tall ? (i & 15) * 8 : k * 64 + (i & 7) * 8,
-                                    v[j]);
+            if (j >= per_thread)
+                break;
+            const Chunk x = chunk(k, j);
+            load8<T>(a.g.p[0], x.at, x.n, a.vec, v[j]);
         }
     };
-    if (k0 < k1)
-        load_step(k0);
+    if (k0 < k1) {
+        if constexpr (MUON)
+            muon_prefetch(k0);
+        else
+            load_step(k0);
+    }
     for (int k = k0; k < k1; ++k) {
         const int it = k - k0, s = it % kGramStages;
         if (it >= kGramStages)
             wait_products(sh, s, (it / kGramStages - 1) & 1, a.status);
         const uint32_t stage = ring + s * kStage;
+        if constexpr (MUON) {
+            if (k + 1 < k1)
+                muon_prefetch(k + 1);
+            muon_step(k, stage);
+        } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (place[j] < 0)
-                continue;
-            uint4 hi, lo;
-            split8<true>(v[j], hi, lo);
-            sts128(stage + place[j], hi);
-            if constexpr (kPair)
-                sts128(stage + kTile + place[j], lo);
+            for (int j = 0; j < 4; ++j)
+                if (j < per_thread)
+                    put(stage, chunk(k, j).place, v[j]);
+            if (k + 1 < k1)
+                load_step(k + 1);
         }
-        if (k + 1 < k1)
-            load_step(k + 1);
         fence_async_shared();
         __syncthreads();
         if (warp == 0 && elect_one() && !a.test_stall) {
@@ -664,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, TILES == 1 ? 3 : 1) k_small_apply(co
             if (row < a.rows && n > 0) {
                 const int64_t at = (int64_t)b * a.batch_stride + (int64_t)row * a.row_stride + col;
                 if constexpr (MUON)
-                    load8<float>(a.u, at, n, a.vec, v[j]);
+                    load8<float>(a.u, at, n, a.mom_vec, v[j]);
                 else
                     load8<T>(a.g.p[0], at, n, a.vec, v[j]);
             } else {

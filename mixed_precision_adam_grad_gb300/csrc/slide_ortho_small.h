@@ -13,6 +13,8 @@ constexpr int kSmallSide = 128;
 constexpr int kSmallMaxSteps = 6;
 constexpr int kSmallMaxParts = 4;  // clusters along the long side, one partial Gram matrix each
 
+constexpr int kVecHalves = 2;
+
 struct SmallOrtho {
     // the matrices, or the R replicas of a Muon step
     ReplicaPtrs g;
@@ -23,10 +25,12 @@ struct SmallOrtho {
     int tall;
     int fp32;                   // type of the matrices or replicas
     int muon;
-    int vec;                    // rows can be read eight values at a time
+    int vec;                    // rows can be read eight values at a time (kVecHalves: as two vectors of four)
+    int mom_vec;                // rows of mom and u can
     // Muon: contiguous
     float *mom, *u;
     float mu, one_minus_mu;
+    float inv_r;                // 1/R where that is exact, else 0
     int nesterov;
     // the polynomial: G, R = aI + bG + cG^2, T = R G and Q, the product of the
     // R, are FP16 pairs times powers of two; per step the factors that take an
