@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCluster, 1, 1)
     // row r at c ^ (r & 31)), then adds up 16 rows of all of them.
     const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
     if (half * 64 < (int)n16) {
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
             uint32_t acc[32];
             if (k1 > k0) {
@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, TILES == 1 ? 3 : 1) k_small_apply(co
         const int d_cols = a.tall ? 64 * tiles : 128, d_rows = a.tall ? 128 : 64 * tiles, chunks = d_cols / 4;
         const int row = quad * 32 + lane;
         if (row < d_rows && half * 64 < d_cols) {
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 uint32_t x[32];
                 tmem_load32(tmem + ((uint32_t)(quad * 32) << 16) + half * 64 + h * 32, x);
@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, TILES == 1 ? 3 : 1) k_small_apply(co
         // four columns of a row at a time: 16 or 32 threads per row
         const int per_row = d_cols / 4, at_once = kThreads / per_row;
         const int c = (tid % per_row) * 4;
-        constexpr int kAhead = 4;
+        constexpr int kAhead = MUON ? 4 : 1;
         for (int r0 = tid / per_row; r0 < r_end; r0 += at_once * kAhead) {
             float th[kAhead][4];
             if constexpr (MUON) {
@@ -870,10 +870,11 @@ cudaError_t launch_all(SmallOrtho &a, int device, int sms, cudaStream_t stream)
 {
     static std::atomic<int> ready[kMaxDevices][5];
     const int n_side = a.tall ? a.rows : a.cols;
-    // a cluster of eight CTAs per 8 x 4 steps of 64, as long as all are resident (two a SM)
+    // a cluster of eight CTAs per 8 x 2 steps of 64, as long as all are resident (two a SM): with 8 x 4
+    // a Muon step of 2 x 4096 x 100 took 76 us instead of 66
     const int steps = (n_side + 63) / 64;
     const int fit = 2 * sms / (kCluster * a.batch);
-    int parts = (steps + 4 * kCluster - 1) / (4 * kCluster);
+    int parts = (steps + 2 * kCluster - 1) / (2 * kCluster);
     parts = parts < fit ? parts : fit;
     parts = parts < 1 ? 1 : parts > kSmallMaxParts ? kSmallMaxParts : parts;
     a.n_parts = parts;
