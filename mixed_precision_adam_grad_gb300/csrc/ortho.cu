@@ -12,9 +12,8 @@
 //     G <- R G R and Q <- R Q commute and stay symmetric m x m matrices, and
 //     X is multiplied by Q once per group.  A group of p steps costs
 //     3 m^2 n + (4p - 3) m^3 instead of p (3 m^2 n + m^3).
-// The second form needs fewer operations as soon as n > m and is used from n =
-// 1.25 m on.  A group is at most
-// kGroupSteps = 3 steps: small singular values are multiplied by a^p in Q
+// The second form needs fewer operations as soon as n > m; shape_of says from
+// where on it is used.  A group is at most kGroupSteps = 3 steps: small singular values are multiplied by a^p in Q
 // while G still holds their squares, and the FP16 operands then cost 6e-4 to
 // 1.2e-3 (2-norm) with groups of 3 + 2, but up to 5e-3 with one group of 5
 // when a few directions dominate.
@@ -437,7 +436,14 @@ Shape shape_of(int batch, int rows, int cols)
     // in groups of 3 + 2: equal at n = m.  Near there the groups gain nothing
     // and lose accuracy (a square matrix of noise has singular values near
     // zero: 2.7e-3 against 1e-3 at 1000 x 1001), so they start at n = 1.25 m.
-    s.grouped = 4 * (int64_t)s.n >= 5 * (int64_t)s.m;
+    // Small matrices are bound by latency, and step by step there are 15
+    // phases instead of 17 and 10 with a K of m instead of 15: 15 us + 0.026 m
+    // less, against 0.0121 us n for three more Gram matrices and 0.9 ms for
+    // each 1e12 operations more.  Fitted to 45 shapes from 200 x 260 to 4000 x
+    // 32000, of which the rule misses two by 3 and 7 %: 200 x 600 95 us step by
+    // step, 110 in groups; 1000 x 3000 229 and 197.
+    const double n = s.n, m = s.m, less = 15.0 + 0.026 * m, more = 0.0121 * n + 0.9e-9 * 9.0 * (n - m) * m * m * batch;
+    s.grouped = 4 * (int64_t)s.n >= 5 * (int64_t)s.m && more > less;
     return s;
 }
 
