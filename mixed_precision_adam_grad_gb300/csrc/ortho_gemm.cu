@@ -266,7 +266,7 @@ enum CMode { kCHigh = 0, kCRow = 1, kCTwo = 2, kCCol = 3, kCParts = 4 };
 
 // What a warp needs of a product's arguments, in registers.
 struct Local {
-    float alpha, s_out, d_row, c_scale, col_scale, eye;
+    float alpha, s_out, d_row, col_scale, eye;
     const float *d_col;   // of the matrix; kCTwo, kCCol
     float *d_out;         // of the matrix; NULL: the diagonal stays
     __half *out_hi, *out_lo;  // out_lo NULL: only the high half is kept
@@ -617,7 +617,6 @@ __device__ __forceinline__ bool epilogue_tile(const OrthoPlan &plan, const Ortho
         k.s_out = p.s_out;
         k.out_hi = p.out.hi;
         k.out_lo = p.out.lo;
-        k.c_scale = p.c_scale;
         k.d_row = p.c_scale;
         k.eye = EPI == kEpiPoly ? g.coef_a : 0.0f;
         k.col_scale = p.c_scale;
