@@ -607,6 +607,12 @@ cudaError_t enqueue_products(const Shape &s, const Work &w, const Schedule &sc, 
             plan.area[plan.areas++] = (float *)p;
         plan.area_slots = s.mpad * s.mpad / 2;
         plan.area_matrix = w.m_elems / 2;
+    } else {  // the other copy of X
+        plan.area[0] = (float *)w.x_hi[0];
+        plan.area[1] = (float *)w.x_hi[1];
+        plan.areas = 1;
+        plan.area_slots = s.rpad * s.cpad / 2;
+        plan.area_matrix = w.x_elems / 2;
     }
     plan.rows = s.rows;
     plan.cols = s.cols;
@@ -665,6 +671,7 @@ cudaError_t enqueue_products(const Shape &s, const Work &w, const Schedule &sc, 
         g.sym = 1;
         g.out_c64 = mc64;
         g.out_stride = w.m_elems;
+        g.area = s.grouped ? 0 : cur ^ 1;
         g.p[0].a = g.p[0].b = w.x_hi[cur];
         g.p[0].alpha = 1.0f / (sc.sx[k0] * sc.sx[k0]);
         g.p[0].out.hi = w.g.hi;

@@ -653,7 +653,7 @@ __device__ __forceinline__ bool epilogue_tile(const OrthoPlan &plan, const Ortho
             if (CG == 1 && k.parts > 1 && ok && c0 < c1) {
                 // (c0 is the warp's only chunk.)  The last part to come adds
                 // them all up, in their order.
-                k.slot = (x.index - x.b * (g.mblk * (g.mblk + 1) / 2)) * g.parts;
+                k.slot = g.area * plan.area_slots + (x.index - x.b * (g.mblk * (g.mblk + 1) / 2)) * g.parts;
                 k.warp = place_of;
                 leave_part(part_at(plan, x.b, k.slot + x.part, place_of), lane,
                            tmem + ((uint32_t)(quad * 32) << 16) + buf * 128 * CG + (narrow ? 0 : c0) * 64);
@@ -931,7 +931,7 @@ void split_gram(OrthoPlan &plan, int groups)
 {
     for (int f = 0; f < plan.n_phases; ++f) {
         OrthoGemm &g = plan.ph[f];
-        if (g.epi != kEpiGram || plan.areas == 0 || g.k64 < 24)
+        if (g.epi != kEpiGram || g.k64 < 24)
             continue;
         const int tiles = tile_count<1>(g), all = tiles * plan.batch;
         int parts = (int)std::sqrt(0.5 * g.k64);

@@ -69,6 +69,7 @@ struct OrthoGemm {
     int d_by_col;            // dvec scales columns
     float coef_a;
     int parts;               // of K, set by the launch (1 in a plan): for kEpiGram, joined by the last CTA to come
+    int area;                // of a Gram matrix: the first area for its parts
     int narrow;              // tiles of 128 x 64 instead of 128 x 128, set by the launch (0 in a plan)
 };
 
@@ -83,8 +84,8 @@ struct OrthoPlan {
     unsigned *count;         // [n_phases][batch] CTAs' tiles written so far, zero at the start
     unsigned *joined;        // [kJoinTiles][8] parts of a tile (a warp's rows and columns of it) so far, zero at the start
     // for parts, memory that nothing else uses during a Gram phase of the same
-    // matrix: `areas` arrays (0: no splitting) of [batch] of area_slots times
-    // 128 x 128 floats, a matrix's area_matrix floats from the next one's
+    // matrix: `areas` arrays from OrthoGemm::area on, each [batch] of area_slots
+    // times 128 x 128 floats, a matrix's area_matrix floats from the next one's
     float *area[8];
     int areas, area_slots;
     int64_t area_matrix;
