@@ -94,7 +94,8 @@ def test_factor(S, batch, rows, cols, dtype):
 
 
 @pytest.mark.parametrize("batch,rows,cols", [(1, 129, 1535), (1, 129, 1537), (2, 238, 14962), (3, 2100, 300), (1, 6401, 513),
-                                             (25, 200, 2000), (26, 200, 2000), (1, 1025, 2085)])
+                                             (25, 200, 2000), (26, 200, 2000), (1, 1025, 2085), (1, 200, 1600), (1, 1900, 400),
+                                             (3, 150, 1545)])
 @pytest.mark.parametrize("more", [0, 11])
 def test_long_sides_of_few_tiles(S, batch, rows, cols, more):
     """The sums over a long side taken apart among CTAs: right, and the same
