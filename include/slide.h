@@ -481,8 +481,9 @@ SLIDE_API slide_status slide_streamed_timeline(slide_state *st, double *out, int
  *   over 2-norm) X is off by 5e-4 to 1.3e-3 for gradients' spectra, from noise
  *   to a few strong directions, and by up to 3e-2 for a matrix of one repeated
  *   value, whose roundings all have one sign.
- * Zeros give zeros; a NaN or an infinity in a matrix makes that matrix's
- * result NaN and touches no other matrix of the batch. */
+ * Finite values may lie anywhere in their type's range, the norm too.  Zeros
+ * give zeros; a NaN or an infinity in a matrix makes that matrix's result NaN
+ * and touches no other matrix of the batch. */
 enum { SLIDE_TYPE_BF16 = 0, SLIDE_TYPE_FP32 = 1 };
 
 typedef struct {

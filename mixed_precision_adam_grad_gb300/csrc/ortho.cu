@@ -104,6 +104,27 @@ __device__ __forceinline__ double block_sum(double x)
     return t;
 }
 
+// Squares are added up in FP32 a few at a time and those sums in double.  A
+// sum outside this range (values beyond about 1e18, or all below 1e-15) may
+// have lost squares to FP32's range: it is formed again in double, from memory
+// (the values would take registers until then).
+constexpr float kSquaresLow = 0x1p-100f, kSquaresHigh = 0x1p120f;
+
+__device__ __forceinline__ bool squares_fit(float sum) { return sum >= kSquaresLow && sum <= kSquaresHigh; }
+
+template <typename T>
+__device__ __forceinline__ double squares_again(const T *p, int n)
+{
+    double sum = 0.0;
+#pragma unroll 1
+    for (int e = 0; e < n; ++e) {
+        const float x = widen(p[e]);
+        if (x != 0.0f)  // FP64 is slow, and zeros have nothing to add
+            sum += (double)x * (double)x;
+    }
+    return sum;
+}
+
 constexpr int kRowsAtOnce = kPrepThreads / 16;  // rows of 128 columns, eight a thread
 
 // V values from an address that is aligned to V of them.
@@ -224,7 +245,20 @@ __global__ void __launch_bounds__(kPrepThreads) k_ortho_source(const __grid_cons
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
             part += square(v[j]);
-        sum += (double)part;
+        if (squares_fit(part)) {
+            sum += (double)part;
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < kAhead; ++j) {
+                const int64_t at = (k + j * kPrepThreads) * V;
+                if (at + V <= to) {
+                    if constexpr (MUON)
+                        sum += squares_again(a.u + at, V);
+                    else
+                        sum += squares_again(x + at, V);
+                }
+            }
+        }
     }
     // the matrix's first and last values outside whole vectors
     const int head = (int)((v0 * V < to ? v0 * V : to) - from), tail = v1 >= v0 ? (int)(to - v1 * V) : 0;
@@ -240,7 +274,7 @@ __global__ void __launch_bounds__(kPrepThreads) k_ortho_source(const __grid_cons
             a.mom[at] = m;
             a.u[at] = u;
         }
-        sum += (double)(u * u);
+        sum += (double)u * (double)u;
     }
     sum = block_sum(sum);
     if (threadIdx.x == 0)
@@ -266,9 +300,15 @@ __global__ void __launch_bounds__(kPrepThreads) k_ortho_source_strided(const __g
                 float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
                 if (row < a.rows)
                     load8<T>(a.g.p[0], (int64_t)b * a.batch_stride + (int64_t)row * a.row_stride + col, n, a.vec, v);
+                float s = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    part = fmaf(v[e], v[e], part);
+                    s = fmaf(v[e], v[e], s);
+                if (squares_fit(s))
+                    part += s;
+                else if (row < a.rows)
+                    sum += squares_again(static_cast<const T *>(a.g.p[0]) + (int64_t)b * a.batch_stride +
+                                             (int64_t)row * a.row_stride + col, min(n, 8));
             }
         }
         sum += (double)part;
@@ -360,7 +400,7 @@ __device__ __forceinline__ void load8_shifted(uintptr_t row, int n, int c8, uint
 template <typename T, bool SHIFTED>
 __global__ void __launch_bounds__(kPrepThreads) k_ortho_scale(const __grid_constant__ ScaleArgs a)
 {
-    __shared__ float s_inv;
+    __shared__ InverseNorm s_inv;
     const int b = blockIdx.y, r0 = threadIdx.x >> 4, c8 = threadIdx.x & 15;
     ptx::launch_dependents();
     ptx::wait_for_previous_grid();
@@ -368,10 +408,10 @@ __global__ void __launch_bounds__(kPrepThreads) k_ortho_scale(const __grid_const
     for (int i = threadIdx.x; i < a.n_parts; i += kPrepThreads)
         x += a.parts[(int64_t)b * kNormParts + i];
     x = block_sum(x);
-    if (threadIdx.x == 0)  // a matrix of zeros stays one, whatever eps
-        s_inv = x == 0.0 && a.eps == 0.0f ? 0.0f : (float)(1.0 / (sqrt(x) + (double)a.eps));
+    if (threadIdx.x == 0)
+        s_inv = inverse_norm(sqrt(x) + (double)a.eps);
     __syncthreads();
-    const float inv = s_inv, scale = a.scale;
+    const float pow2 = s_inv.pow2, rest = s_inv.rest * a.scale;
     const uintptr_t lo_at = (uintptr_t)a.x;
     const uintptr_t hi_at = (uintptr_t)(static_cast<const T *>(a.x) + (int64_t)(gridDim.y - 1) * a.batch_stride +
                                         (int64_t)(a.rows - 1) * a.row_stride + a.cols);
@@ -392,7 +432,7 @@ __global__ void __launch_bounds__(kPrepThreads) k_ortho_scale(const __grid_const
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float y = v[2 * e] * inv * scale, z = v[2 * e + 1] * inv * scale;
+                const float y = v[2 * e] * pow2 * rest, z = v[2 * e + 1] * pow2 * rest;
                 const __half2 p = __floats2half2_rn(y, z);
                 const float2 f = __half22float2(p);
                 const __half2 q = __floats2half2_rn((y - f.x) * kLoScale, (z - f.y) * kLoScale);
@@ -461,7 +501,8 @@ struct Work {
     OrthoPair t, q[2];
     float *dq;
     // the kernels for a small side, in the same place
-    float *inv, *small_parts, *small_u;
+    InverseNorm *inv;
+    float *small_parts, *small_u;
     __half *small_q;
     int64_t x_elems, m_elems;  // per matrix
     int64_t bytes;
@@ -510,7 +551,7 @@ Work layout(const Shape &s, char *base)
     w.bytes = off;
     if (s.m <= kSmallSide) {  // the status, then the other kernels' arrays
         off = (int64_t)align_up(4);
-        w.inv = (float *)take(4 * (int64_t)s.batch);
+        w.inv = (InverseNorm *)take((int64_t)sizeof(InverseNorm) * s.batch);
         w.small_parts = (float *)take(small_parts_bytes(s.batch));
         w.small_q = (__half *)take(small_q_bytes(s.batch));
         w.small_u = (float *)take(4 * (int64_t)s.batch * s.rows * s.cols);

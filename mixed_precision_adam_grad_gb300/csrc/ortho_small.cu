@@ -463,6 +463,99 @@ constexpr int kPolyPair = TILES == 2 ? kPairBytes : 2 * kTile;  // with TILES = 
 template <int TILES>
 constexpr int kPolySmem = 1024 + 3 * kPolyPair<TILES>;
 
+// Traces outside this range may have lost squares to FP32's range.  Below it
+// that matters only where eps does not dwarf the norm (below 2^-45).
+constexpr float kTraceHigh = 0x1p100f, kTraceLow = 0x1p-90f, kEpsLow = 0x1p-25f, kEpsHigh = 0x1p100f;
+
+__device__ __forceinline__ bool trace_fits(float trace, float eps)
+{
+    return trace <= kTraceHigh && (trace >= kTraceLow || eps >= kEpsLow) && eps <= kEpsHigh;
+}
+
+// For a matrix whose trace does not fit: its Gram matrix once more, by this CTA
+// alone, in FP32, from the values times the power of two that brings the
+// largest one to 1.  It takes the place of the first part, and zeros that of the
+// others; a.inv gets 1/(|X| + eps) and *inv that for the scaled values.
+// `stage`: 64 rows of kStageRow floats of shared memory.  (No matrix
+// instructions: with this 64 x 2560 takes 0.44 ms instead of 32 us, 128 x 16384
+// 4.8 ms, which only such matrices pay.)
+constexpr int kStageRow = 132;
+
+__device__ __forceinline__ void gram_again(const SmallOrtho &a, uint32_t stage, int blocks, float *inv)
+{
+    __shared__ unsigned s_top;
+    __shared__ float s_diag[128];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x;
+    auto value = [&](int row, int col) {
+        if (a.muon)
+            return a.u[((int64_t)b * a.rows + row) * a.cols + col];
+        const int64_t at = (int64_t)b * a.batch_stride + (int64_t)row * a.row_stride + col;
+        return a.fp32 ? static_cast<const float *>(a.g.p[0])[at] : widen(static_cast<const uint16_t *>(a.g.p[0])[at]);
+    };
+    if (tid == 0)
+        s_top = 0;
+    if (tid < 128)
+        s_diag[tid] = 0.0f;
+    __syncthreads();
+    unsigned top = 0;
+    for (int row = warp; row < a.rows; row += (int)blockDim.x / 32)
+        for (int col = lane; col < a.cols; col += 32)
+            top = max(top, __float_as_uint(value(row, col)) & 0x7fffffffu);
+    atomicMax(&s_top, top);
+    __syncthreads();
+    top = s_top;
+    const bool finite = top < 0x7f800000u, some = finite && top != 0;
+    const int e = some ? ilogbf(__uint_as_float(top)) : 0, e1 = max(-126, min(126, -e));
+    const float f1 = exp2f((float)e1), f2 = exp2f((float)(-e - e1));
+    const int row = tid & 127, block = tid >> 7, n_side = a.tall ? a.rows : a.cols;
+    const bool mine = block < blocks && row < a.m;
+    float4 *out = reinterpret_cast<float4 *>(a.parts) + (int64_t)b * a.n_parts * 4096 + block * 8 * 128 + row;
+    for (int s0 = 0; s0 < n_side && some; s0 += 64) {
+        __syncthreads();
+        for (int i = tid; i < 64 * 128; i += blockDim.x) {
+            const int k = a.tall ? i >> 7 : i & 63, j = a.tall ? i & 127 : i >> 6;
+            const float x = j < a.m && s0 + k < n_side ? (a.tall ? value(s0 + k, j) : value(j, s0 + k)) : 0.0f;
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(stage + (k * kStageRow + j) * 4), "f"(x * f1 * f2) : "memory");
+        }
+        __syncthreads();
+        for (int q = 0; q < 8 && mine; ++q) {  // four columns at a time, the sums of 64 to those before
+            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int k = 0; k < 64; ++k) {
+                float x;
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(stage + (k * kStageRow + row) * 4) : "memory");
+                const uint4 y = lds128(stage + (k * kStageRow + block * 32 + 4 * q) * 4);
+                sum.x = fmaf(x, __uint_as_float(y.x), sum.x);
+                sum.y = fmaf(x, __uint_as_float(y.y), sum.y);
+                sum.z = fmaf(x, __uint_as_float(y.z), sum.z);
+                sum.w = fmaf(x, __uint_as_float(y.w), sum.w);
+            }
+            if (s0 > 0) {
+                const float4 before = out[q * 128];
+                sum.x += before.x;
+                sum.y += before.y;
+                sum.z += before.z;
+                sum.w += before.w;
+            }
+            out[q * 128] = sum;
+            if (block * 32 + 4 * q == (row & ~3))
+                s_diag[row] = (row & 3) == 0 ? sum.x : (row & 3) == 1 ? sum.y : (row & 3) == 2 ? sum.z : sum.w;
+        }
+    }
+    for (int part = 1; part < a.n_parts && mine && some; ++part)
+        for (int q = 0; q < 8; ++q)
+            out[part * 4096 + q * 128] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    __syncthreads();
+    if (tid == 0) {
+        double trace = 0.0;
+        for (int i = 0; i < a.m; ++i)
+            trace += s_diag[i];
+        const InverseNorm r = inverse_norm(finite ? ldexp(sqrt(trace), e) + (double)a.eps : NAN);
+        a.inv[b] = r;
+        *inv = (float)ldexp((double)r.pow2 * r.rest, e);
+    }
+    __syncthreads();
+}
+
 // 128 threads per 32 columns and a last warp that issues the products.  Warp
 // (quad, block) has rows 32*quad.. and columns 32*block.. of every matrix; warps
 // whose rows all lie beyond m rest.  Rows and columns beyond m inside a used
@@ -478,6 +571,8 @@ __global__ void __launch_bounds__(128 * 2 * TILES + 32) k_small_poly(const __gri
     extern __shared__ uint8_t smem_raw[];
     __shared__ Base sh;
     __shared__ double s_trace[4];
+    __shared__ float s_inv;
+    __shared__ int s_again;
     __shared__ float s_f[6][kSmallMaxSteps];  // the factors of the steps (from the arguments each would take 200 cycles)
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const uint32_t G = base, R = base + kPolyPair<TILES>, Q = base + 2 * kPolyPair<TILES>;
@@ -501,9 +596,14 @@ __global__ void __launch_bounds__(128 * 2 * TILES + 32) k_small_poly(const __gri
     }
     launch_dependents();
     wait_for_previous_grid();
-    if (tid == 0 && (*(volatile unsigned *)a.status & kStatusWaitLimit))
-        sh.abort = 1;  // the launch before gave up: no waits of the full length
+    if (tid == 0) {
+        s_again = 0;
+        if (*(volatile unsigned *)a.status & kStatusWaitLimit)
+            sh.abort = 1;  // the launch before gave up: no waits of the full length
+    }
+    uint32_t done[2] = {0, 0};  // products waited for on each of the two barriers
 
+again:
     // the raw Gram matrix, zero beyond m; its trace is |X|_F^2
     float v[32];
     if (!issuer) {
@@ -538,13 +638,16 @@ __global__ void __launch_bounds__(128 * 2 * TILES + 32) k_small_poly(const __gri
             s_trace[quad] = trace;
     }
     __syncthreads();
-    double trace = 0.0;
-    for (int i = 0; i < blocks; ++i)
-        trace += s_trace[i];
-    // a matrix of zeros stays one, whatever eps
-    const float inv = trace == 0.0 && a.eps == 0.0f ? 0.0f : (float)(1.0 / (sqrt(trace) + (double)a.eps));
-    if (tid == 0)
-        a.inv[b] = inv;
+    if (tid == 0 && !s_again) {  // one thread: FP64 is slow
+        double trace = 0.0;
+        for (int i = 0; i < blocks; ++i)
+            trace += s_trace[i];
+        // a matrix of zeros stays one, whatever eps
+        s_inv = trace == 0.0 && a.eps == 0.0f ? 0.0f : (float)(1.0 / (sqrt(trace) + (double)a.eps));
+        a.inv[b] = InverseNorm{1.0f, s_inv};
+    }
+    __syncthreads();
+    const float inv = s_inv;
     float r[32];  // bG + aI of the coming step, from G as it is written
     auto begin_r = [&](int k) {
         const float eye = s_f[0][k], bb = s_f[1][k];
@@ -559,7 +662,6 @@ __global__ void __launch_bounds__(128 * 2 * TILES + 32) k_small_poly(const __gri
         put_pair<TILES>(G, row, block, v);
         begin_r(0);
     }
-    uint32_t done[2] = {0, 0};  // products waited for on each of the two barriers
     auto issue = [&](int bar, uint32_t x, uint32_t y) {
         if (issuer && !a.test_stall) {
             tmem_fence_after();
@@ -638,6 +740,20 @@ __global__ void __launch_bounds__(128 * 2 * TILES + 32) k_small_poly(const __gri
     uint4 *out = reinterpret_cast<uint4 *>(a.q) + (int64_t)b * (kPairBytes / 16);
     for (int i = tid; i < (TILES == 2 ? kPairBytes : kTile) / 16; i += blockDim.x)
         out[i] = lds128(Q + i * 16);
+    // Only now, off the straight way (each CTA runs through its instructions
+    // once, and fetching them counts): was the Gram matrix what it should be?
+    if (!s_again && !sh.abort) {
+        double trace = 0.0;
+        for (int i = 0; i < blocks; ++i)
+            trace += s_trace[i];
+        if (!trace_fits((float)trace, a.eps)) {
+            gram_again(a, base, blocks, &s_inv);
+            if (tid == 0)
+                s_again = 1;
+            __syncthreads();
+            goto again;
+        }
+    }
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
@@ -670,7 +786,8 @@ __global__ void __launch_bounds__(kThreads, TILES == 1 ? 3 : 1) k_small_apply(co
     if (tid == 0 && (*(volatile unsigned *)a.status & kStatusWaitLimit))
         sh.abort = 1;
     __syncthreads();
-    const float inv = a.inv[b] * kApplyScale;
+    const InverseNorm inverse = a.inv[b];
+    const float pow2 = inverse.pow2, inv = inverse.rest * kApplyScale;  // pow2 is 1 wherever 1/norm has room in FP32
     const float back = a.q_last / kApplyScale;
     {
         const uint4 *q = reinterpret_cast<const uint4 *>(a.q) + (int64_t)b * (kPairBytes / 16);
@@ -720,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, TILES == 1 ? 3 : 1) k_small_apply(co
             float x[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                x[e] = v[j][e] * inv;
+                x[e] = v[j][e] * pow2 * inv;
             uint4 hi, lo;
             split8<false>(x, hi, lo);
             sts128(X + place, hi);

@@ -101,4 +101,28 @@ struct OrthoPlan {
 
 cudaError_t launch_ortho_products(const OrthoPlan &plan, int device, cudaStream_t stream);
 
+// 1/d as a power of two times a factor, for a d = |X|_F + eps that may lie
+// anywhere among the norms of finite FP32 matrices (1/d itself need not be an
+// FP32 value): x*pow2 is exact but for what lies 2^-126 below the norm, so
+// (x*pow2)*rest is x times the rounded 1/d.  0 of zeros, whatever eps; NaN
+// where the matrix has a NaN or an infinity.
+struct InverseNorm {
+    float pow2, rest;
+};
+
+__device__ __forceinline__ InverseNorm inverse_norm(double d)
+{
+    InverseNorm r = {1.0f, 0.0f};
+    if (d == 0.0)
+        return r;
+    if (!(d < 1e300)) {
+        r.rest = __int_as_float(0x7fffffff);
+        return r;
+    }
+    const int e = min(126, max(-126, ilogb(d)));
+    r.pow2 = exp2f((float)-e);
+    r.rest = (float)(ldexp(1.0, e) / d);
+    return r;
+}
+
 }  // namespace slide

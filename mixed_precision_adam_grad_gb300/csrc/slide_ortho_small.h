@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "slide_kernels.h"
+#include "slide_ortho.h"
 
 namespace slide {
 
@@ -48,7 +49,7 @@ struct SmallOrtho {
     // scratch
     float *parts;               // [batch][n_parts][128 x 128]
     __half *q;                  // [batch][hi, lo][128 x 128], tiles as in slide_ortho.h
-    float *inv;                 // [batch]
+    InverseNorm *inv;           // [batch]
     unsigned *status;
     int n_parts;                // set by the launch
     // results

@@ -1,0 +1,77 @@
+"""slide_orthogonalize and the Muon steps at their limits: values at the ends of
+their type's range, non-finite ones, waits that run out.  Formulas and
+tolerances are test_gpu_ortho's.
+"""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from test_gpu_ortho import (BF16, FACTOR, S, check_muon, factor64, gen, matrix, off, orthogonalize,  # noqa: E402, F401
+                            workspace)
+
+
+@pytest.mark.parametrize("batch,rows,cols", [(2, 50, 70), (1, 64, 2560), (2, 3000, 100), (1, 1, 7), (2, 200, 333),
+                                             (1, 300, 900), (1, 900, 300)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("scale", [1e-38, 1e-30, 1e-22, 1e-16, 1e18, 1e22, 1e30, 1e37])
+def test_values_at_the_ends_of_the_range(S, batch, rows, cols, dtype, scale):
+    """The squares of finite values, and the norm, may lie outside FP32's range.
+    Denormal BF16 and FP32 values are what they are: the formula sees the same."""
+    x = matrix(batch, rows, cols, 9, rms=1.0)
+    x[batch - 1] *= 0.5                                        # a norm of its own
+    x = (x * scale).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    assert x.isfinite().all() and (x != 0).any()
+    assert off(orthogonalize(S, x, S.ortho_params(eps=0.0)), factor64(x, eps=0.0)) <= FACTOR + BF16
+    if scale > 1:
+        assert off(orthogonalize(S, x), factor64(x)) <= FACTOR + BF16
+    r, c = rows + 1, cols + 3                                  # rows apart
+    big = torch.zeros(batch, r, c, dtype=x.dtype, device="cuda")
+    big[:, :rows, 1:1 + cols] = x
+    out = torch.empty(x.shape, dtype=torch.bfloat16, device="cuda")
+    S.slide_orthogonalize(batch, rows, cols, big[:, :, 1:], out, S.ortho_params(eps=0.0), workspace(S, batch, rows, cols),
+                          x_type=S.SLIDE_TYPE_FP32 if dtype == "fp32" else S.SLIDE_TYPE_BF16, x_row_stride=c,
+                          x_batch_stride=r * c)
+    assert off(out, factor64(x, eps=0.0)) <= FACTOR + BF16
+
+
+@pytest.mark.parametrize("rows,cols", [(60, 90), (120, 40), (200, 340)])
+def test_one_batch_of_many_magnitudes(S, rows, cols):
+    """Each matrix has a range of its own; zeros among them; within a matrix
+    values far below the largest play no part."""
+    x = matrix(6, rows, cols, 12, rms=1.0)
+    for k, s in enumerate((1e-33, 1e30, 0.0, 1.0, 1e-21, 1e21)):
+        x[k] *= s
+    x[1, ::2] *= 1e-25
+    got, want = orthogonalize(S, x, S.ortho_params(eps=0.0)), factor64(x, eps=1e-300)
+    assert (got[2] == 0).all()
+    keep = [0, 1, 3, 4, 5]
+    assert off(got[keep], want[keep]) <= FACTOR + BF16
+
+
+@pytest.mark.parametrize("rows,cols", [(50, 70), (1, 9), (9, 1), (100, 900), (200, 333), (300, 300)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_a_nonfinite_value_makes_all_of_its_matrix_nan(S, rows, cols, dtype, bad):
+    x = matrix(3, rows, cols, 13).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    x[1, rows // 2, cols // 3] = bad
+    got = orthogonalize(S, x)
+    assert torch.isnan(got[1]).all()
+    assert off(got[::2], factor64(x[::2])) <= FACTOR + BF16
+
+
+@pytest.mark.parametrize("rows,cols", [(64, 300), (300, 100), (200, 331)])
+@pytest.mark.parametrize("size", [1e-30, 1e24, 1e33])
+def test_muon_step_of_values_at_the_ends_of_the_range(S, rows, cols, size):
+    grads = [matrix(2, rows, cols, k, rms=1.0) * size for k in (1, 2)]
+    mom, th = matrix(2, rows, cols, 3, rms=1.0) * size, torch.randn(2, rows, cols, generator=gen(4), device="cuda")
+    lr, mu, scale = 0.1, 0.9, 0.5
+    g = torch.stack([x.double() for x in grads]).mean(0)
+    m64 = mu * mom.double() + (1 - mu) * g
+    o = factor64(mu * m64 + (1 - mu) * g, eps=0.0)
+    want, th0 = (th.double() - lr * scale * o, m64, o), th.clone()
+    w = torch.empty(th.shape, dtype=torch.bfloat16, device="cuda")
+    S.slide_muon_step(2, rows, cols, grads, th, mom, w, S.muon_hparams(lr=lr, momentum=mu, weight_decay=0.0, scale=scale, eps=0.0),
+                      workspace(S, 2, rows, cols), grads_type=S.SLIDE_TYPE_FP32)
+    torch.cuda.synchronize()
+    check_muon(S, th, mom, w, want, lr, scale, th0)
