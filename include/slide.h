@@ -342,7 +342,8 @@ SLIDE_API slide_status slide_layer_last_clip_coef(slide_state *st, int32_t layer
 /* Status of the steps of `layer` since the previous call (HBM residency):
  * waits for the device, reads and clears the layer's status word, and returns
  *   SLIDE_ERR_TIMEOUT   if a bounded wait inside the update kernel's copy
- *                       pipeline ran out (the step is incomplete; restore the
+ *                       pipeline, or inside the matrix products of
+ *                       slide_layer_muon_step, ran out (the step is incomplete; restore the
  *                       layer with slide_layer_set);
  *   SLIDE_ERR_NONFINITE with SLIDE_FLAG_CHECK_FINITE, if a mean gradient held
  *                       a NaN or Inf (the update was applied: the caller
@@ -542,9 +543,9 @@ SLIDE_API slide_status slide_muon_step(int32_t batch, int32_t rows, int32_t cols
                                        void *workspace, int64_t workspace_bytes, slide_stream_t stream);
 
 /* Status of the last slide_orthogonalize or slide_muon_step with this
- * workspace: waits for `stream` and returns SLIDE_ERR_TIMEOUT if a bounded
- * wait inside a product ran out (2 s; that call's results are undefined),
- * else SLIDE_OK.
+ * workspace, or of all blocks of the last slide_layer_muon_step with it: waits
+ * for `stream` and returns SLIDE_ERR_TIMEOUT if a bounded wait inside a product
+ * ran out (2 s; that call's results are undefined), else SLIDE_OK.
  * Defined by: no passage; it completes the two calls above. */
 SLIDE_API slide_status slide_ortho_status(const void *workspace, slide_stream_t stream);
 
@@ -565,6 +566,8 @@ typedef struct {
  *   workspace: at least the largest slide_ortho_workspace of the blocks; the
  *     blocks use it one after another.
  * The other arguments as in slide_layer_step.  Trace events are not recorded.
+ * A bounded wait that runs out in any block shows in slide_ortho_status and in
+ * slide_layer_status.
  * Defined by: the passages of slide_layer_step ("SlideDP: Scaling
  * Host-Resident LLM Fine-Tuning Across Multiple GPUs", Core method); the
  * update rule of the matrices is in no passage. */

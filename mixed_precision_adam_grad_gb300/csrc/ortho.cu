@@ -21,6 +21,7 @@
 
 #include <cmath>
 #include <cstdlib>
+#include <cstring>
 
 #include "slide.h"
 #include "slide_ortho.h"
@@ -56,6 +57,7 @@ struct SourceArgs {
     int nesterov;
     double *parts;            // [batch][kNormParts]
     unsigned *status, *count, *joined;
+    int keep_status;          // add to *status instead of clearing it first
 };
 
 __device__ __forceinline__ float widen(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
@@ -170,7 +172,7 @@ __device__ __forceinline__ void begin_source(const SourceArgs &a)
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         for (int i = threadIdx.x; i < kJoinWords; i += kPrepThreads)
             a.joined[i] = 0;
-        if (threadIdx.x == 0)
+        if (threadIdx.x == 0 && !a.keep_status)
             *a.status = 0;
     }
 }
@@ -620,6 +622,7 @@ slide_status schedule_of(const slide_ortho_params *p, int m, Schedule *out)
 }
 
 struct Finish {
+    MuonBlock block;
     int epi;
     uint16_t *w;
     int64_t w_row, w_batch;
@@ -627,7 +630,13 @@ struct Finish {
     float decay, step;
 };
 
-bool test_stall() { return getenv("SLIDE_TEST_PIPELINE_STALL") != nullptr; }
+// Tests only: whether the kernels issue no products, so that their waits run
+// out.  "first": those of a layer's first block.
+bool test_stall(const MuonBlock &block)
+{
+    const char *v = getenv("SLIDE_TEST_PIPELINE_STALL");
+    return v && (block.index == 0 || strcmp(v, "first") != 0);
+}
 
 // The products, from the matrix in x_hi[0] and x_lo to the caller's array.
 cudaError_t enqueue_products(const Shape &s, const Work &w, const Schedule &sc, const Finish &f, int device,
@@ -640,6 +649,7 @@ cudaError_t enqueue_products(const Shape &s, const Work &w, const Schedule &sc, 
     OrthoPlan plan{};
     plan.batch = s.batch;
     plan.status = w.status;
+    plan.layer_status = f.block.layer_status;
     plan.count = w.count;
     plan.joined = w.joined;
     if (s.grouped) {
@@ -665,7 +675,7 @@ cudaError_t enqueue_products(const Shape &s, const Work &w, const Schedule &sc, 
     plan.theta = f.theta;
     plan.decay = f.decay;
     plan.step = f.step;
-    plan.test_stall = test_stall();
+    plan.test_stall = test_stall(f.block);
 
     OrthoGemm base{};
     base.nprob = 1;
@@ -898,6 +908,8 @@ cudaError_t enqueue_small(const Shape &s, const Work &w, const Schedule &sc, con
     o.q = w.small_q;
     o.inv = w.inv;
     o.status = w.status;
+    o.layer_status = f.block.layer_status;
+    o.keep_status = f.block.index > 0;
     o.w = f.w;
     o.w_row = f.w_row;
     o.w_batch = f.w_batch;
@@ -906,14 +918,15 @@ cudaError_t enqueue_small(const Shape &s, const Work &w, const Schedule &sc, con
     o.step = f.step;
     o.w_vec = muon ? s.cols % 4 == 0
                    : (uintptr_t)f.w % 8 == 0 && f.w_row % 4 == 0 && (s.batch == 1 || f.w_batch % 4 == 0);
-    o.test_stall = test_stall();
+    o.test_stall = test_stall(f.block);
     return launch_ortho_small(o, device, stream);
 }
 
 // The norms (and a Muon step's update), then the normalised operands.
-cudaError_t enqueue_source(const Shape &s, const Work &w, const Schedule &sc, SourceArgs a, bool fp32, bool muon,
-                           float eps, cudaStream_t stream)
+cudaError_t enqueue_source(const Shape &s, const Work &w, const Schedule &sc, SourceArgs a, bool keep_status, bool fp32,
+                           bool muon, float eps, cudaStream_t stream)
 {
+    a.keep_status = keep_status;
     a.rows = s.rows;
     a.cols = s.cols;
     a.rblk = s.rblk;
@@ -979,7 +992,7 @@ cudaError_t enqueue(const Shape &s, const Work &w, const Schedule &sc, const Sou
 {
     if (is_small(s, sc))
         return enqueue_small(s, w, sc, a, f, fp32, muon, eps, device, stream);
-    const cudaError_t e = enqueue_source(s, w, sc, a, fp32, muon, eps, stream);
+    const cudaError_t e = enqueue_source(s, w, sc, a, f.block.index > 0, fp32, muon, eps, stream);
     return e == cudaSuccess ? enqueue_products(s, w, sc, f, device, stream) : e;
 }
 
@@ -1099,10 +1112,10 @@ extern "C" slide_status slide_orthogonalize(int32_t batch, int32_t rows, int32_t
     return SLIDE_OK;
 }
 
-extern "C" slide_status slide_muon_step(int32_t batch, int32_t rows, int32_t cols, int32_t n_replicas,
-                                        const void *const *grad_replicas, int32_t grads_type, float *master,
-                                        float *momentum, void *bf16_out, const slide_muon_hparams *hp,
-                                        void *workspace, int64_t workspace_bytes, slide_stream_t stream)
+slide_status slide::muon_step(int32_t batch, int32_t rows, int32_t cols, int32_t n_replicas,
+                              const void *const *grad_replicas, int32_t grads_type, float *master, float *momentum,
+                              void *bf16_out, const slide_muon_hparams *hp, void *workspace, int64_t workspace_bytes,
+                              const MuonBlock &block, slide_stream_t stream)
 {
     slide_status rc = check_shape(batch, rows, cols);
     if (rc == SLIDE_OK)
@@ -1151,6 +1164,7 @@ extern "C" slide_status slide_muon_step(int32_t batch, int32_t rows, int32_t col
     a.vec = cols % (grads_type == SLIDE_TYPE_FP32 ? 4 : 8) == 0;
     a.vec4 = grads_type == SLIDE_TYPE_BF16 && cols % 4 == 0;
     Finish f{};
+    f.block = block;
     f.epi = kEpiMuon;
     f.w = (uint16_t *)bf16_out;
     f.theta = master;
@@ -1162,6 +1176,15 @@ extern "C" slide_status slide_muon_step(int32_t batch, int32_t rows, int32_t col
         return fail_cuda(e, "muon step launch");
     clear_error();
     return SLIDE_OK;
+}
+
+extern "C" slide_status slide_muon_step(int32_t batch, int32_t rows, int32_t cols, int32_t n_replicas,
+                                        const void *const *grad_replicas, int32_t grads_type, float *master,
+                                        float *momentum, void *bf16_out, const slide_muon_hparams *hp,
+                                        void *workspace, int64_t workspace_bytes, slide_stream_t stream)
+{
+    return muon_step(batch, rows, cols, n_replicas, grad_replicas, grads_type, master, momentum, bf16_out, hp, workspace,
+                     workspace_bytes, MuonBlock{}, stream);
 }
 
 extern "C" slide_status slide_ortho_status(const void *workspace, slide_stream_t stream)

@@ -70,7 +70,6 @@ constexpr int kPiece = 4096;                      // 32 rows of a tile
 constexpr int kEpiBytes = 2 * kPiece;             // an epilogue warp's buffer: hi and lo of a chunk, or hi of two
 constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiWarps * kEpiBytes;
 constexpr int kMaxParts = 8;  // of a Gram matrix's K
-constexpr unsigned kStatusWaitLimit = 2u;
 constexpr unsigned kFullMask = 0xffffffffu;
 
 struct Tile {
@@ -785,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ortho_products(const __grid_con
         if (!ok) {
             sh.abort = 1;
             if (lane == 0)
-                atomicOr(plan.status, kStatusWaitLimit);
+                report_wait_limit(plan.status, plan.layer_status);
         }
         // copies in flight land before the CTA ends
         for (uint32_t d = it > kStages ? it - kStages : 0; d < it; ++d)
@@ -839,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ortho_products(const __grid_con
         if (!ok) {
             sh.abort = 1;
             if (lane == 0)
-                atomicOr(plan.status, kStatusWaitLimit);
+                report_wait_limit(plan.status, plan.layer_status);
         }
         // the matrix instructions in flight end before the CTA does: the
         // commits of the last stages have arrived
@@ -867,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ortho_products(const __grid_con
         if (!ok) {
             sh.abort = 1;
             if (lane == 0)
-                atomicOr(plan.status, kStatusWaitLimit);
+                report_wait_limit(plan.status, plan.layer_status);
         }
     } else {
         const int w = warp - 2;
@@ -904,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ortho_products(const __grid_con
         if (!ok) {
             sh.abort = 1;
             if (lane == 0)
-                atomicOr(plan.status, kStatusWaitLimit);
+                report_wait_limit(plan.status, plan.layer_status);
             for (int i = 0; i < 2; ++i)  // copies of C may be in flight
                 if (asked[i] > 0)
                     mbar_wait(smem_addr(&sh.c[ew][i]), (asked[i] - 1) & 1, nullptr);

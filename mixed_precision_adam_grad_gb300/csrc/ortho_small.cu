@@ -33,7 +33,6 @@ using namespace ptx;
 
 constexpr int kThreads = 256;
 constexpr int kCluster = 8;
-constexpr unsigned kStatusWaitLimit = 2u;
 constexpr int kTile = 16384;           // 128 rows x 64 columns of 16-bit values
 constexpr int kGramStages = 3;
 constexpr float kApplyScale = 1024.0f; // of X / |X| in k_small_apply: entries are at most 1
@@ -157,14 +156,12 @@ __device__ __forceinline__ uint32_t set_up(Base &b, uint32_t cols)
 // registers, which the matrix instructions take (80 cycles each otherwise).
 __device__ __forceinline__ int warp_number() { return __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0); }
 
-// Wait for a barrier that tensor-core products arrive on; on a wait that runs
-// out the call is marked.
-__device__ __forceinline__ void wait_products(Base &b, int i, uint32_t parity, unsigned *status)
+// Wait for a barrier that tensor-core products arrive on; a wait that runs out
+// ends the CTA's work, which it reports at its end.
+__device__ __forceinline__ void wait_products(Base &b, int i, uint32_t parity)
 {
-    if (!mbar_wait(smem_addr(&b.bar[i]), parity, &b.abort)) {
+    if (!mbar_wait(smem_addr(&b.bar[i]), parity, &b.abort))
         b.abort = 1;
-        atomicOr(status, kStatusWaitLimit);
-    }
     tmem_fence_after();
 }
 
@@ -184,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCluster, 1, 1)
     const uint32_t tmem = set_up(sh, 128);
     const int tid = threadIdx.x, warp = warp_number(), lane = tid & 31, b = blockIdx.y;
     launch_dependents();
-    if (blockIdx.x == 0 && b == 0 && tid == 0)
+    if (blockIdx.x == 0 && b == 0 && tid == 0 && !a.keep_status)
         *a.status = 0;
     const int n_side = a.tall ? a.rows : a.cols;
     const int steps = (n_side + 63) / 64, per = (steps + gridDim.x - 1) / gridDim.x;
@@ -284,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCluster, 1, 1)
     for (int k = k0; k < k1; ++k) {
         const int it = k - k0, s = it % kGramStages;
         if (it >= kGramStages)
-            wait_products(sh, s, (it / kGramStages - 1) & 1, a.status);
+            wait_products(sh, s, (it / kGramStages - 1) & 1);
         const uint32_t stage = ring + s * kStage;
         if constexpr (MUON) {
             if (k + 1 < k1)
@@ -316,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCluster, 1, 1)
     }
     // the last products of each stage
     for (int it = max(0, k1 - k0 - kGramStages); it < k1 - k0; ++it)
-        wait_products(sh, it % kGramStages, (it / kGramStages) & 1, a.status);
+        wait_products(sh, it % kGramStages, (it / kGramStages) & 1);
     __syncthreads();
 
     // The cluster's sum: each CTA puts its part into shared memory (chunk c of
@@ -368,6 +365,8 @@ __global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCluster, 1, 1)
     tmem_fence_after();
     if (warp == 0)
         tmem_free<1>(tmem, 128);
+    if (tid == 0 && sh.abort)
+        report_wait_limit(a.status, a.layer_status);
 }
 
 // ---- 2: the polynomial ------------------------------------------------------------
@@ -673,7 +672,7 @@ again:
         }
     };
     auto wait = [&](int bar) {
-        wait_products(sh, bar, done[bar] & 1, a.status);
+        wait_products(sh, bar, done[bar] & 1);
         ++done[bar];
     };
     // this thread's values of an accumulator, times f, into a pair
@@ -759,6 +758,8 @@ again:
     tmem_fence_after();
     if (warp == 0)
         tmem_free<1>(tmem, 256);
+    if (tid == 0 && sh.abort)
+        report_wait_limit(a.status, a.layer_status);
 }
 
 // ---- 3: the result ------------------------------------------------------------------
@@ -863,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, TILES == 1 ? 3 : 1) k_small_apply(co
             mma_commit<1>(smem_addr(&sh.bar[0]));
         }
         __syncwarp();
-        wait_products(sh, 0, phase & 1, a.status);
+        wait_products(sh, 0, phase & 1);
         // rows x cols of the result: tall 128 x m, wide m x 128; FP32 in X's
         // place, chunk c of row r at c ^ (r & (chunks of a row - 1))
         const int d_cols = a.tall ? 64 * tiles : 128, d_rows = a.tall ? 128 : 64 * tiles, chunks = d_cols / 4;
@@ -957,6 +958,8 @@ __global__ void __launch_bounds__(kThreads, TILES == 1 ? 3 : 1) k_small_apply(co
     tmem_fence_after();
     if (warp == 0)
         tmem_free<1>(tmem, 128);
+    if (tid == 0 && sh.abort)
+        report_wait_limit(a.status, a.layer_status);
 }
 
 constexpr int kMaxDevices = 64;

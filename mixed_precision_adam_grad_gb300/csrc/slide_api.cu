@@ -656,16 +656,18 @@ slide_status slide_layer_muon_step(slide_state *st, int32_t layer, const slide_m
         return e == cudaSuccess ? SLIDE_OK : fail_cuda(e, "grad_reduce_adamw_cast launch");
     };
     int64_t done = 0;
+    MuonBlock block{0, L.scratch.status};
     for (int32_t k = 0; k < n_blocks && rc == SLIDE_OK; ++k) {
         const slide_matrix_block &b = blocks[k];
+        const int64_t size = (int64_t)b.rows * b.cols * b.batch;
         rc = adam_range(done, b.offset);
-        if (rc == SLIDE_OK) {
+        if (rc == SLIDE_OK && size > 0) {
             const ReplicaPtrs g = replicas_at(b.offset);
-            rc = slide_muon_step(b.batch, b.rows, b.cols, R, g.p, f32g ? SLIDE_TYPE_FP32 : SLIDE_TYPE_BF16,
-                                 L.theta + b.offset, L.m + b.offset, w + b.offset, muon, workspace, workspace_bytes,
-                                 stream);
+            rc = muon_step(b.batch, b.rows, b.cols, R, g.p, f32g ? SLIDE_TYPE_FP32 : SLIDE_TYPE_BF16, L.theta + b.offset,
+                           L.m + b.offset, w + b.offset, muon, workspace, workspace_bytes, block, stream);
+            ++block.index;
         }
-        done = b.offset + (int64_t)b.rows * b.cols * b.batch;
+        done = b.offset + size;
     }
     if (rc == SLIDE_OK)
         rc = adam_range(done, L.n);

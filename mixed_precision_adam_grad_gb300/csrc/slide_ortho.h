@@ -80,7 +80,7 @@ constexpr int kJoinWords = kJoinTiles * 8;
 struct OrthoPlan {
     OrthoGemm ph[kMaxPhases];
     int n_phases, batch;
-    unsigned *status;
+    unsigned *status, *layer_status;  // layer_status may be NULL
     unsigned *count;         // [n_phases][batch] CTAs' tiles written so far, zero at the start
     unsigned *joined;        // [kJoinTiles][8] parts of a tile (a warp's rows and columns of it) so far, zero at the start
     // for parts, memory that nothing else uses during a Gram phase of the same
@@ -98,6 +98,15 @@ struct OrthoPlan {
     float decay, step;
     int test_stall;
 };
+
+constexpr unsigned kStatusWaitLimit = 2u;  // bit of a status word: a wait ran out
+
+__device__ __forceinline__ void report_wait_limit(unsigned *status, unsigned *layer_status)
+{
+    atomicOr(status, kStatusWaitLimit);
+    if (layer_status)
+        atomicOr(layer_status, kStatusWaitLimit);
+}
 
 cudaError_t launch_ortho_products(const OrthoPlan &plan, int device, cudaStream_t stream);
 

@@ -50,7 +50,8 @@ struct SmallOrtho {
     float *parts;               // [batch][n_parts][128 x 128]
     __half *q;                  // [batch][hi, lo][128 x 128], tiles as in slide_ortho.h
     InverseNorm *inv;           // [batch]
-    unsigned *status;
+    unsigned *status, *layer_status;  // layer_status may be NULL
+    int keep_status;            // add to *status instead of clearing it first
     int n_parts;                // set by the launch
     // results
     uint16_t *w;

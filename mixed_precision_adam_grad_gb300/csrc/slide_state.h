@@ -82,6 +82,18 @@ AdamScalars adam_scalars_for(const slide_adam_hparams &hp, int64_t t);
 slide_status check_hparams(const slide_adam_hparams *hp);
 slide_status check_muon_hparams(const slide_muon_hparams *hp);  // ortho.cu
 
+// slide_muon_step as block number `index` of a layer's step (ortho.cu): the
+// first one clears the workspace's status word, the others add to it, and what
+// they report goes to the layer's own word too.
+struct MuonBlock {
+    int index;
+    unsigned *layer_status;  // may be NULL
+};
+slide_status muon_step(int32_t batch, int32_t rows, int32_t cols, int32_t n_replicas, const void *const *grad_replicas,
+                       int32_t grads_type, float *master, float *momentum, void *bf16_out,
+                       const slide_muon_hparams *hp, void *workspace, int64_t workspace_bytes, const MuonBlock &block,
+                       slide_stream_t stream);
+
 // Most copy-in or write-back chunks a streamed unit may have.
 constexpr int64_t kMaxChunksPerUnit = 65536;
 

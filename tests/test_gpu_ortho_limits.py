@@ -75,3 +75,29 @@ def test_muon_step_of_values_at_the_ends_of_the_range(S, rows, cols, size):
                       workspace(S, 2, rows, cols), grads_type=S.SLIDE_TYPE_FP32)
     torch.cuda.synchronize()
     check_muon(S, th, mom, w, want, lr, scale, th0)
+
+
+@pytest.mark.parametrize("blocks", [((0, 1, 64, 96), (6144, 1, 200, 72)), ((0, 1, 300, 200), (60000, 1, 64, 96)),
+                                    ((0, 1, 200, 200), (40000, 0, 8, 8), (40000, 2, 150, 160), (88000, 3, 40, 8))])
+def test_a_wait_that_runs_out_in_a_layers_first_block_is_reported(S, monkeypatch, blocks):
+    """By the workspace's word and the layer's, though the blocks after it share
+    the workspace; the next step starts afresh."""
+    n = blocks[-1][0] + blocks[-1][1] * blocks[-1][2] * blocks[-1][3] + 16
+    st = S.slide_state_create([n], 1)
+    grads = [torch.randn(n, generator=gen(1), device="cuda").bfloat16()]
+    ws = torch.full((max(S.slide_ortho_workspace(*b[1:]) for b in blocks),), 0xff, dtype=torch.uint8, device="cuda")
+    try:
+        def step():
+            S.slide_layer_muon_step(st, 0, blocks, grads, S.muon_hparams(), S.hparams(), ws)
+        monkeypatch.setenv("SLIDE_TEST_PIPELINE_STALL", "first")
+        step()
+        assert S.slide_ortho_status(ws) == S.SLIDE_ERR_TIMEOUT
+        assert S.slide_layer_status(st, 0) == S.SLIDE_ERR_TIMEOUT
+        monkeypatch.delenv("SLIDE_TEST_PIPELINE_STALL")
+        step()
+        assert S.slide_ortho_status(ws) == S.SLIDE_OK and S.slide_layer_status(st, 0) == S.SLIDE_OK
+        step()
+        step()
+        assert S.slide_ortho_status(ws) == S.SLIDE_OK and S.slide_layer_status(st, 0) == S.SLIDE_OK
+    finally:
+        S.slide_state_destroy(st)
