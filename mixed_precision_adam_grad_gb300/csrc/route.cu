@@ -505,6 +505,11 @@ __device__ __forceinline__ T narrow(float x)
     }
 }
 
+// Gradients of normalised weights are differences: of an expert's upstream
+// value g_i and the mean sum_j p_j g_j of the token's, times p_i.  The
+// difference is formed as sum_j p_j (g_i - g_j), term by term: where one expert
+// has nearly all the weight, g_i - sum_j p_j g_j keeps no digit of its gradient.
+
 // Gradient where only the chosen experts have one: W = 1, 2, 4, ... 32 lanes
 // (at least top_k) per token, 32/W tokens per warp at a time.  The rows are
 // filled with zeros, then the chosen experts' values go over them.
@@ -521,7 +526,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_route_back_sparse(const BackArg
         float dw = 0.0f;
         if (t < a.tokens && place < a.K && (!a.mask || a.mask[t])) {
             e = a.experts[t * a.K + place];
-            dw = a.d_weights[t * a.K + place] * a.scale;
+            dw = a.d_weights[t * a.K + place];
             if (e < 0 || e >= a.E) {
                 e = -1;
                 dw = 0.0f;
@@ -545,6 +550,19 @@ __global__ void __launch_bounds__(kWarps * 32) k_route_back_sparse(const BackArg
                 v += __shfl_xor_sync(kFull, v, o);
             return v;
         };
+        auto differences = [&](float p) {  // sum_j p_j (dw - dw_j)
+            float v = 0.0f;
+            auto add = [&](int o) {
+                v = fmaf(__shfl_xor_sync(kFull, p, o), dw - __shfl_xor_sync(kFull, dw, o), v);
+            };
+            if (W > 1)
+                add(1);
+            if (W > 2)
+                add(2), add(3);
+            for (int o = 4; o < W; o += 4)
+                add(o), add(o + 1), add(o + 2), add(o + 3);
+            return v;
+        };
         float dx;
         if constexpr (SIGMOID) {
             const float p = e >= 0 ? sigmoid(x) : 0.0f;
@@ -552,9 +570,9 @@ __global__ void __launch_bounds__(kWarps * 32) k_route_back_sparse(const BackArg
             float dp = dw;
             if (a.renorm) {
                 const float total = sum_of(p) + kTiny;
-                dp = (dw - sum_of(dw * p) / total) / total;
+                dp = fmaf(dw, kTiny, differences(p)) / total / total;
             }
-            dx = dp * p * q;
+            dx = dp * a.scale * p * q;
         } else {
             float top = x;
             for (int o = 1; o < W; o <<= 1)
@@ -562,7 +580,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_route_back_sparse(const BackArg
             float p = e >= 0 ? expf(x - top) : 0.0f;
             const float total = sum_of(p);
             p = total > 0.0f ? p / total : 0.0f;
-            dx = p * (dw - sum_of(dw * p));
+            dx = p * differences(p) * a.scale;
         }
         __syncwarp();
         if (e >= 0)
@@ -575,6 +593,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_route_back_sparse(const BackArg
 template <typename T, int NV>
 __global__ void __launch_bounds__(kWarps * 32) k_route_back_dense(const BackArgs a)
 {
+    __shared__ unsigned chosen[kWarps][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kPer = 16 / sizeof(T);
     for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.tokens; t += (int64_t)gridDim.x * kWarps) {
@@ -586,13 +605,17 @@ __global__ void __launch_bounds__(kWarps * 32) k_route_back_dense(const BackArgs
             e = a.experts[t * a.K + lane];
             e = e < a.E ? e : -1;
             if (e >= 0)
-                dw = a.d_weights[t * a.K + lane] * a.scale;
+                dw = a.d_weights[t * a.K + lane];
         }
         const bool any = __any_sync(kFull, e >= 0);
         float x[NV], dx = 0.0f, base = 0.0f;
         if (any) {
+            chosen[warp][lane] = 0;  // a bit for each expert
+            __syncwarp();
+            if (e >= 0)
+                atomicOr(&chosen[warp][e >> 5], 1u << (e & 31));
             const float xe = e >= 0 ? fminf(widen(row[e]), FLT_MAX) : -INFINITY;
-            float top = -INFINITY, sum = 0.0f;
+            float top = -INFINITY, rest = 0.0f;
             load_row<T, NV>(row, lane, a.E, a.vec, x);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -600,16 +623,28 @@ __global__ void __launch_bounds__(kWarps * 32) k_route_back_dense(const BackArgs
                 top = fmaxf(top, x[i]);
             }
             top = warp_max(top);
+            __syncwarp();
+            const unsigned mine = chosen[warp][lane * NV >> 5] >> (lane * NV & 31);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 x[i] = expf(x[i] - top);
-                sum += x[i];
+                rest += mine >> i & 1 ? 0.0f : x[i];
             }
-            sum = warp_sum(sum);
-            const float p = e >= 0 ? expf(xe - top) / sum : 0.0f;
-            base = warp_sum(dw * p);
-            dx = p * (dw - base);
-            base = -base / sum;
+            float p = e >= 0 ? expf(xe - top) : 0.0f;
+            rest = warp_sum(rest);
+            float all = warp_sum(p);
+            const float one = 1.0f / (rest + all);
+            p *= one;
+            all *= one;
+            rest *= one;
+            // g_i - sum_j p_j g_j = (g_i - g_r) sum_j p_j - sum_j p_j (g_j - g_r) + g_i (1 - sum_j p_j), r the
+            // expert with the largest p
+            const unsigned largest = __reduce_max_sync(kFull, __float_as_uint(p));
+            const int at = __ffs(__ballot_sync(kFull, __float_as_uint(p) == largest)) - 1;
+            const float dr = __shfl_sync(kFull, dw, at), h = e >= 0 ? dw - dr : 0.0f;
+            const float mean = warp_sum(p * h);
+            dx = p * fmaf(dw, rest, fmaf(h, all, -mean)) * a.scale;
+            base = -fmaf(dr, all, mean) * one * a.scale;
         }
         // the row, then the chosen experts over it
         bool done = false;
