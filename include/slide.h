@@ -587,6 +587,8 @@ SLIDE_API slide_status slide_layer_muon_step(slide_state *st, int32_t layer, con
  *            ranked by the sum of their best two keys or by their best key
  *   chosen = the top_k largest keys among the kept groups, largest first
  *   w      = s[chosen];  w = w / (sum w + 1e-20) if renormalize;  w = w * scale
+ *            (a softmax that is renormalised: the softmax of the chosen logits,
+ *            the same but for the 1e-20, however small the chosen scores are)
  *   load[e] += number of tokens that chose e
  * The bias only moves the choice, never the weights.  Ties go to the lowest
  * index, for groups and experts.  Each line that enters a choice is one FP32

@@ -456,10 +456,22 @@ __global__ void __launch_bounds__((ANY ? kAnyWarps : kWarps) * 32) k_route(const
         }
         best += my_owner * NV;
         best = my_key <= kKeyNone || nan || !live ? -1 : best;
+        const float y = best >= 0 ? widen(row[best]) : -INFINITY;
         float score = 0.0f;
-        if (best >= 0) {
-            const float y = widen(row[best]);
-            score = SIGMOID ? sigmoid(y) : __fdiv_rn(expf(fminf(y, FLT_MAX) - top), sum);
+        if constexpr (SIGMOID) {
+            if (best >= 0)
+                score = sigmoid(y);
+        } else {
+            if (a.renorm && !by_logit) {
+                // a bias can leave the row's largest logit out: relative to the
+                // largest chosen one, as the gradient has it
+                top = fminf(y, FLT_MAX), sum = 1.0f;
+#pragma unroll
+                for (int o = LPT / 2; o > 0; o >>= 1)
+                    top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+            }
+            if (best >= 0)
+                score = __fdiv_rn(expf(fminf(y, FLT_MAX) - top), sum);
         }
         if (a.renorm)
             score = __fdiv_rn(score, __fadd_rn(token_sum<LPT>(score), kTiny));

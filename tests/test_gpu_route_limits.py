@@ -67,3 +67,39 @@ def test_small_gradients_of_confident_routers(S, c, spread, dtype):
         assert bool((out >= (want - tol).bfloat16()).all()) and bool((out <= (want + tol).bfloat16()).all())
     else:
         assert bool(((out.double() - want).abs() <= tol).all()), float(((out.double() - want).abs() / tol).max())
+
+
+@pytest.mark.parametrize("K", [1, 2, 3, 5])
+@pytest.mark.parametrize("groups", [1, 2])
+@pytest.mark.parametrize("depth", [1.0, 30.0, 150.0])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_renormalised_softmax_where_the_bias_picks_tiny_scores(S, K, groups, depth, dtype):
+    """Weights and gradient are those of the softmax of the chosen logits, down
+    to scores that FP32 does not hold.  The picks' biases are further apart than
+    their scores are large."""
+    g = torch.Generator(device="cuda").manual_seed(K)
+    E, T, favoured = 16, 100, torch.tensor([3, 5, 8, 12, 13], device="cuda")
+    x = torch.randn(T, E, generator=g, device="cuda")
+    x[:, favoured] = -20 - depth * torch.rand(T, 5, generator=g, device="cuda")
+    x = x.to(dtype)
+    bias = torch.zeros(E, device="cuda")
+    bias[favoured] = 2 + 0.01 * favoured.float()
+    c = Cfg(E, K, "softmax", groups=groups, top_groups=groups, scale=1.5)
+    w, e = torch.empty(T, K, device="cuda"), torch.empty(T, K, dtype=torch.int32, device="cuda")
+    kind = S.SLIDE_TYPE_FP32 if dtype == torch.float32 else S.SLIDE_TYPE_BF16
+    S.slide_route_experts(T, x, w, e, c.of(S), bias=bias, logits_type=kind)
+    up = torch.randn(T, K, generator=g, device="cuda")
+    out = torch.full((T, E), float("nan"), dtype=dtype, device="cuda")
+    S.slide_route_experts_backward(T, x, e, up, out, c.of(S), logits_type=kind)
+    torch.cuda.synchronize()
+    chosen = favoured.flip(0)[:K].expand(T, K)
+    assert torch.equal(e.long(), chosen)
+    rel = 2.0 ** -24 * (48 + 2 * (depth + 25))
+    want = torch.softmax(x.double().gather(1, chosen), 1) * 1.5
+    assert bool(((w.double() - want).abs() <= rel * want + 2.0 ** -126).all())
+    want, size = terms64(x, chosen, up, c)
+    tol = rel * size + 2.0 ** -126
+    if dtype == torch.bfloat16:
+        assert bool((out >= (want - tol).bfloat16()).all()) and bool((out <= (want + tol).bfloat16()).all())
+    else:
+        assert bool(((out.double() - want).abs() <= tol).all())
