@@ -545,7 +545,8 @@ SLIDE_API slide_status slide_muon_step(int32_t batch, int32_t rows, int32_t cols
 /* Status of the last slide_orthogonalize or slide_muon_step with this
  * workspace, or of all blocks of the last slide_layer_muon_step with it: waits
  * for `stream` and returns SLIDE_ERR_TIMEOUT if a bounded wait inside a product
- * ran out (2 s; that call's results are undefined), else SLIDE_OK.
+ * ran out (2 s; that call's results are undefined), else SLIDE_OK.  A call
+ * that had nothing to do ran out of no wait.
  * Defined by: no passage; it completes the two calls above. */
 SLIDE_API slide_status slide_ortho_status(const void *workspace, slide_stream_t stream);
 

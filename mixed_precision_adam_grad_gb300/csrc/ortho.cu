@@ -1029,6 +1029,17 @@ slide_status check_workspace(const Work &need, const void *workspace, int64_t by
 
 }  // namespace
 
+slide_status clear_ortho_status(void *workspace, int64_t workspace_bytes, slide_stream_t stream)
+{
+    if (workspace && !misaligned(workspace, 256) && workspace_bytes >= 256) {
+        const cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(unsigned), (cudaStream_t)stream);
+        if (e != cudaSuccess)
+            return fail_cuda(e, "clearing the workspace's status word");
+    }
+    clear_error();
+    return SLIDE_OK;
+}
+
 slide_status check_muon_hparams(const slide_muon_hparams *hp)
 {
     if (!hp)
@@ -1075,10 +1086,8 @@ extern "C" slide_status slide_orthogonalize(int32_t batch, int32_t rows, int32_t
         rc = schedule_of(params, rows < cols ? (rows > 0 ? rows : 1) : (cols > 0 ? cols : 1), &sc);
     if (rc != SLIDE_OK)
         return rc;
-    if (empty(batch, rows, cols)) {
-        clear_error();
-        return SLIDE_OK;
-    }
+    if (empty(batch, rows, cols))
+        return clear_ortho_status(workspace, workspace_bytes, stream);
     if (!x || misaligned(x, x_type == SLIDE_TYPE_FP32 ? 4 : 2) || !bf16_out || misaligned(bf16_out, 2))
         return fail(SLIDE_ERR_INVALID_ARG, "x or bf16_out is NULL or not aligned to its type");
     if (x_row_stride < cols || out_row_stride < cols)
@@ -1128,10 +1137,8 @@ slide_status slide::muon_step(int32_t batch, int32_t rows, int32_t cols, int32_t
         return rc;
     if (!grad_replicas)
         return fail(SLIDE_ERR_INVALID_ARG, "grad_replicas is NULL");
-    if (empty(batch, rows, cols)) {
-        clear_error();
-        return SLIDE_OK;
-    }
+    if (empty(batch, rows, cols))
+        return clear_ortho_status(workspace, workspace_bytes, stream);
     Schedule sc;
     if ((rc = schedule_of(&hp->ortho, rows < cols ? rows : cols, &sc)) != SLIDE_OK)
         return rc;

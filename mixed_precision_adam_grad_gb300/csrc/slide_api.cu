@@ -671,6 +671,8 @@ slide_status slide_layer_muon_step(slide_state *st, int32_t layer, const slide_m
     }
     if (rc == SLIDE_OK)
         rc = adam_range(done, L.n);
+    if (rc == SLIDE_OK && block.index == 0)
+        rc = clear_ortho_status(workspace, workspace_bytes, stream);
     if (rc != SLIDE_OK)
         return rc;
     L.t = t;

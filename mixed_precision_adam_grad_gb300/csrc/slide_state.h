@@ -82,6 +82,10 @@ AdamScalars adam_scalars_for(const slide_adam_hparams &hp, int64_t t);
 slide_status check_hparams(const slide_adam_hparams *hp);
 slide_status check_muon_hparams(const slide_muon_hparams *hp);  // ortho.cu
 
+// What a call of empty matrices leaves: a workspace that has one says that
+// nothing ran out (ortho.cu).
+slide_status clear_ortho_status(void *workspace, int64_t workspace_bytes, slide_stream_t stream);
+
 // slide_muon_step as block number `index` of a layer's step (ortho.cu): the
 // first one clears the workspace's status word, the others add to it, and what
 // they report goes to the layer's own word too.

@@ -101,3 +101,26 @@ def test_a_wait_that_runs_out_in_a_layers_first_block_is_reported(S, monkeypatch
         assert S.slide_ortho_status(ws) == S.SLIDE_OK and S.slide_layer_status(st, 0) == S.SLIDE_OK
     finally:
         S.slide_state_destroy(st)
+
+
+def test_status_after_calls_with_nothing_to_do(S):
+    """Not what the workspace's memory held before."""
+    def fresh():
+        return torch.full((4096,), 0xff, dtype=torch.uint8, device="cuda")
+    ws = fresh()
+    S.slide_orthogonalize(0, 8, 8, None, None, S.ortho_params(), ws)
+    assert S.slide_ortho_status(ws) == S.SLIDE_OK
+    ws, side = fresh(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    S.slide_muon_step(1, 0, 8, [None], None, None, None, S.muon_hparams(), ws, stream=side)
+    assert S.slide_ortho_status(ws, side) == S.SLIDE_OK
+    st = S.slide_state_create([64], 1)
+    try:
+        g = torch.zeros(64, dtype=torch.bfloat16, device="cuda")
+        for blocks in ((), ((0, 0, 8, 8),)):
+            ws = fresh()
+            S.slide_layer_muon_step(st, 0, blocks, [g], S.muon_hparams(), S.hparams(), ws)
+            assert S.slide_ortho_status(ws) == S.SLIDE_OK
+            S.slide_layer_muon_step(st, 0, blocks, [g], S.muon_hparams(), S.hparams(), None)
+    finally:
+        S.slide_state_destroy(st)
