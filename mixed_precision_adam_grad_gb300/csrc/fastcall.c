@@ -4,7 +4,8 @@
  * dozen arguments through ctypes (6 us on a Grace core) costs more than the
  * kernel.  No behaviour of its own: it converts the arguments by the binding's
  * rules and calls the library's function, whose address the binding hands over
- * with bind() once the library is loaded.
+ * with bind() once the library is loaded, without the interpreter's lock: a
+ * launch waits where the device's queue is full, and other threads run then.
  *   pointers: None, an int, or an object with data_ptr() or .ctypes.data
  *   structs:  a ctypes structure (its buffer)
  *   streams:  None, an int, or an object with .cuda_stream
@@ -147,16 +148,18 @@ static PyObject *route_experts(PyObject *self, PyObject *const *a, Py_ssize_t n)
     void *logits, *bias, *mask, *w, *e, *load;
     const void *cfg;
     slide_stream_t s;
+    slide_status rc;
     (void)self;
     if (!ready(F_ROUTE, n, 11) || !to_i64(a[0], &tokens) || !to_ptr(a[1], &logits) || !to_i32(a[2], &type) ||
         !to_i64(a[3], &stride) || !to_ptr(a[4], &bias) || !to_ptr(a[5], &mask) ||
         !to_struct(a[6], sizeof(slide_route_config), &cfg) || !to_ptr(a[7], &w) || !to_ptr(a[8], &e) ||
         !to_ptr(a[9], &load) || !to_stream(a[10], &s))
         return NULL;
-    return PyLong_FromLong(((slide_status(*)(int64_t, const void *, int32_t, int64_t, const float *, const uint8_t *,
-                                             const slide_route_config *, float *, int32_t *, int64_t *,
-                                             slide_stream_t))functions[F_ROUTE])(tokens, logits, type, stride, bias,
-                                                                                 mask, cfg, w, e, load, s));
+    Py_BEGIN_ALLOW_THREADS
+    rc = ((__typeof__(slide_route_experts) *)functions[F_ROUTE])(tokens, logits, type, stride, bias, mask, cfg, w,
+         e, load, s);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
 }
 
 static PyObject *route_experts_backward(PyObject *self, PyObject *const *a, Py_ssize_t n)
@@ -166,16 +169,18 @@ static PyObject *route_experts_backward(PyObject *self, PyObject *const *a, Py_s
     void *logits, *e, *dw, *mask, *dx;
     const void *cfg;
     slide_stream_t s;
+    slide_status rc;
     (void)self;
     if (!ready(F_ROUTE_BACK, n, 11) || !to_i64(a[0], &tokens) || !to_ptr(a[1], &logits) || !to_i32(a[2], &type) ||
         !to_i64(a[3], &stride) || !to_ptr(a[4], &e) || !to_ptr(a[5], &dw) || !to_ptr(a[6], &mask) ||
         !to_struct(a[7], sizeof(slide_route_config), &cfg) || !to_ptr(a[8], &dx) || !to_i64(a[9], &d_stride) ||
         !to_stream(a[10], &s))
         return NULL;
-    return PyLong_FromLong(((slide_status(*)(int64_t, const void *, int32_t, int64_t, const int32_t *, const float *,
-                                             const uint8_t *, const slide_route_config *, void *, int64_t,
-                                             slide_stream_t))functions[F_ROUTE_BACK])(tokens, logits, type, stride, e,
-                                                                                      dw, mask, cfg, dx, d_stride, s));
+    Py_BEGIN_ALLOW_THREADS
+    rc = ((__typeof__(slide_route_experts_backward) *)functions[F_ROUTE_BACK])(tokens, logits, type, stride, e, dw,
+         mask, cfg, dx, d_stride, s);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
 }
 
 static PyObject *route_bias_step(PyObject *self, PyObject *const *a, Py_ssize_t n)
@@ -184,15 +189,17 @@ static PyObject *route_bias_step(PyObject *self, PyObject *const *a, Py_ssize_t 
     void *load, *bias;
     double rate;
     slide_stream_t s;
+    slide_status rc;
     (void)self;
     if (!ready(F_ROUTE_BIAS, n, 5) || !to_i32(a[0], &experts) || !to_ptr(a[1], &load) || !to_ptr(a[2], &bias))
         return NULL;
     rate = PyFloat_AsDouble(a[3]);
     if ((rate == -1.0 && PyErr_Occurred()) || !to_stream(a[4], &s))
         return NULL;
-    return PyLong_FromLong(((slide_status(*)(int32_t, int64_t *, float *, float,
-                                             slide_stream_t))functions[F_ROUTE_BIAS])(experts, load, bias, (float)rate,
-                                                                                      s));
+    Py_BEGIN_ALLOW_THREADS
+    rc = ((__typeof__(slide_route_bias_step) *)functions[F_ROUTE_BIAS])(experts, load, bias, (float)rate, s);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
 }
 
 static PyObject *orthogonalize(PyObject *self, PyObject *const *a, Py_ssize_t n)
@@ -202,16 +209,18 @@ static PyObject *orthogonalize(PyObject *self, PyObject *const *a, Py_ssize_t n)
     void *x, *out, *ws;
     const void *params;
     slide_stream_t s;
+    slide_status rc;
     (void)self;
     if (!ready(F_ORTHO, n, 14) || !to_i32(a[0], &batch) || !to_i32(a[1], &rows) || !to_i32(a[2], &cols) ||
         !to_ptr(a[3], &x) || !to_i32(a[4], &type) || !to_i64(a[5], &xr) || !to_i64(a[6], &xb) || !to_ptr(a[7], &out) ||
         !to_i64(a[8], &outr) || !to_i64(a[9], &outb) || !to_struct(a[10], sizeof(slide_ortho_params), &params) ||
         !to_ptr(a[11], &ws) || !to_i64(a[12], &bytes) || !to_stream(a[13], &s))
         return NULL;
-    return PyLong_FromLong(((slide_status(*)(int32_t, int32_t, int32_t, const void *, int32_t, int64_t, int64_t, void *,
-                                             int64_t, int64_t, const slide_ortho_params *, void *, int64_t,
-                                             slide_stream_t))functions[F_ORTHO])(batch, rows, cols, x, type, xr, xb, out,
-                                                                                 outr, outb, params, ws, bytes, s));
+    Py_BEGIN_ALLOW_THREADS
+    rc = ((__typeof__(slide_orthogonalize) *)functions[F_ORTHO])(batch, rows, cols, x, type, xr, xb, out, outr,
+         outb, params, ws, bytes, s);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
 }
 
 static PyObject *muon_step(PyObject *self, PyObject *const *a, Py_ssize_t n)
@@ -221,6 +230,7 @@ static PyObject *muon_step(PyObject *self, PyObject *const *a, Py_ssize_t n)
     void *th, *mom, *w, *ws;
     const void *grads[SLIDE_MAX_REPLICAS] = {0}, *hp;
     slide_stream_t s;
+    slide_status rc;
     PyObject *seq;
     Py_ssize_t r, count;
     (void)self;
@@ -241,10 +251,11 @@ static PyObject *muon_step(PyObject *self, PyObject *const *a, Py_ssize_t n)
         !to_struct(a[8], sizeof(slide_muon_hparams), &hp) || !to_ptr(a[9], &ws) || !to_i64(a[10], &bytes) ||
         !to_stream(a[11], &s))
         return NULL;
-    return PyLong_FromLong(((slide_status(*)(int32_t, int32_t, int32_t, int32_t, const void *const *, int32_t, float *,
-                                             float *, void *, const slide_muon_hparams *, void *, int64_t,
-                                             slide_stream_t))functions[F_MUON])(
-        batch, rows, cols, count > INT32_MAX ? INT32_MAX : (int32_t)count, grads, type, th, mom, w, hp, ws, bytes, s));
+    Py_BEGIN_ALLOW_THREADS
+    rc = ((__typeof__(slide_muon_step) *)functions[F_MUON])(batch, rows, cols, count > INT32_MAX ? INT32_MAX :
+         (int32_t)count, grads, type, th, mom, w, hp, ws, bytes, s);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
 }
 
 static PyMethodDef methods[] = {

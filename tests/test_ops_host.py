@@ -161,3 +161,33 @@ def test_layer_muon_refusals(S):
         assert e.value.status == S.SLIDE_ERR_STATE
     finally:
         S.slide_state_destroy(st)
+
+
+def test_calls_let_other_threads_run(S):
+    """A launch can block; the interpreter's lock is not held meanwhile."""
+    import threading
+    import time
+
+    from mixed_precision_adam_grad_gb300 import _binding
+    fast = _binding._fast()
+    own = C.cast(S.lib.slide_route_bias_step, C.c_void_p).value
+    usleep = C.CDLL(None).usleep                                 # takes the first argument: a call of 0.4 s
+    runs, stop = [0], threading.Event()
+
+    def count():
+        while not stop.is_set():
+            runs[0] += 1
+            time.sleep(0.001)
+    t = threading.Thread(target=count)
+    fast.bind("slide_route_bias_step", C.cast(usleep, C.c_void_p).value)
+    try:
+        t.start()
+        time.sleep(0.05)
+        before = runs[0]
+        fast.route_bias_step(400000, None, None, 0.0, None)
+        during = runs[0] - before
+    finally:
+        fast.bind("slide_route_bias_step", own)
+        stop.set()
+        t.join()
+    assert during >= 20
