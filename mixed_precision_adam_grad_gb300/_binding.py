@@ -496,6 +496,8 @@ def slide_layer_muon_step(st: SlideState, layer: int, blocks, grad_replicas, muo
     """blocks: (offset, batch, rows, cols) of the layer's matrices, ascending;
     they are updated by Muon, everything else by AdamW."""
     ptrs = [_ptr(g) for g in grad_replicas]
+    if len(ptrs) < st.n_replicas:  # the library reads as many addresses as the state has replicas
+        raise SlideError(SLIDE_ERR_INVALID_ARG, f"{len(ptrs)} gradient replicas for a state of {st.n_replicas}")
     arr = (C.c_void_p * max(1, len(ptrs)))(*ptrs)
     bl = (slide_matrix_block * max(1, len(blocks)))(*[slide_matrix_block(*b) for b in blocks])
     ws, nbytes = _workspace(workspace, workspace_bytes)

@@ -191,3 +191,13 @@ def test_calls_let_other_threads_run(S):
         stop.set()
         t.join()
     assert during >= 20
+
+
+def test_layer_muon_step_of_too_few_replicas(S):
+    """Refused before the library reads past the addresses that it was given."""
+    st = S.SlideState(0, [64], 2, S.SLIDE_RESIDENCY_HBM)
+    for grads in ([], [P]):
+        refused(S, "replicas", S.slide_layer_muon_step, st, 0, [(0, 1, 8, 8)], grads, S.muon_hparams(), S.hparams(), 4 * P,
+                workspace_bytes=1 << 40)
+    refused(S, "state is NULL", S.slide_layer_muon_step, st, 0, [(0, 1, 8, 8)], [P, P], S.muon_hparams(), S.hparams(), 4 * P,
+            workspace_bytes=1 << 40)
