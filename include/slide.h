@@ -472,16 +472,20 @@ SLIDE_API slide_status slide_streamed_timeline(slide_state *st, double *out, int
  *     g   = (sum_r g_r, in FP32, replica order) / R
  *     mom = mu*mom + (1-mu)*g
  *     u   = mu*mom + (1-mu)*g   if nesterov, else mom
- *     O   = X of u, as above, not rounded
+ *     O   = X of u, as above, not rounded to BF16
  *     th  = th*(1 - lr*wd) - (lr*scale)*O,    w = bf16_round_nearest_even(th)
  *   mom and th are FP32 and updated in place; momentum's and theta's lines are
  *   one FP32 operation each, the scalars formed in double and rounded once.
  *   The products run on FP16 operands (scaled by powers of two) with FP32
  *   accumulators; the diagonals of the left factors stay in FP32 and act on the
  *   iterate in 22 bits.  Against the polynomial in 64 bits (2-norm of the difference
- *   over 2-norm) X is off by 5e-4 to 1.3e-3 for gradients' spectra, from noise
- *   to a few strong directions, and by up to 3e-2 for a matrix of one repeated
- *   value, whose roundings all have one sign.
+ *   over 2-norm) X is off by 5e-4 to 1.3e-3 after five steps for noise with or
+ *   without strong directions, by up to 5.5e-3 where a few directions stand 10
+ *   to 10^4 times above the noise (with steeper coefficients, from a = 8.2 on,
+ *   6e-3, 1.1e-2 with a side of at most 128), and by up to 2e-2 there after six
+ *   or seven steps; by up to 3e-2 for a matrix of one repeated value, whose
+ *   roundings all have one sign.  In a Muon step of matrices with both sides above 128 O is
+ *   kept in 11 bits on its way to theta, a tenth of that.
  * Finite values may lie anywhere in their type's range, the norm too.  Zeros
  * give zeros; a NaN or an infinity in a matrix makes that matrix's result NaN
  * and touches no other matrix of the batch. */

@@ -13,10 +13,20 @@
 //     X is multiplied by Q once per group.  A group of p steps costs
 //     3 m^2 n + (4p - 3) m^3 instead of p (3 m^2 n + m^3).
 // The second form needs fewer operations as soon as n > m; shape_of says from
-// where on it is used.  A group is at most kGroupSteps = 3 steps: small singular values are multiplied by a^p in Q
-// while G still holds their squares, and the FP16 operands then cost 6e-4 to
-// 1.2e-3 (2-norm) with groups of 3 + 2, but up to 5e-3 with one group of 5
-// when a few directions dominate.
+// where on it is used, groups_of how long a group is.  What limits that is
+// accuracy: small singular values are multiplied by a in Q at each step while G
+// still holds their squares, beside the roundings of its FP16 operands, which
+// have the size of the large ones.  Worst of eight spectra (noise, and 4 to 128
+// directions over noise of 1e-1 to 1e-4), 2-norm of the error over 2-norm, of
+// five steps:
+//     coefficients     m     3 + 2    2 + 2 + 1   step by step
+//     quintic        200    8.4e-3      5.1e-3        1.7e-3
+//                    500    5.4e-3      3.1e-3        1.0e-3
+//                   2560    2.8e-3      1.4e-3        7.2e-4
+//     a = 8.2 first  200    8.4e-2      1.8e-2        3.3e-3
+//                   2560    1.1e-2      5.8e-3        1.1e-3
+// A group of 3 later than the first, where many singular values are near 1, is
+// up to 0.45 off (six steps of the quintic, m = 238).
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -33,7 +43,9 @@ namespace slide {
 namespace {
 
 constexpr int kMaxSteps = 16;
-constexpr int kGroupSteps = 3;
+constexpr int kGroupSteps = 3;       // at most; only the first group, from a smaller side of kLongGroups on, else 2
+constexpr int kLongGroups = 512;
+constexpr double kGroupSlope = 3.5;  // largest |a| of a step with others behind it in its group
 constexpr int kMaxSide = 1 << 20;
 constexpr int kMaxSmallSide = 16384;
 constexpr int kMaxBatch = 65535;
@@ -484,7 +496,9 @@ Shape shape_of(int batch, int rows, int cols)
     // each 1e12 operations more.  Fitted to 45 shapes from 200 x 260 to 4000 x
     // 32000, of which the rule misses two by 3 and 7 %: 200 x 600 95 us step by
     // step, 110 in groups; 1000 x 3000 229 and 197.
-    const double n = s.n, m = s.m, less = 15.0 + 0.026 * m, more = 0.0121 * n + 0.9e-9 * 9.0 * (n - m) * m * m * batch;
+    // (Of groups of 2 + 2 + 1 the third of these Gram matrices is one of theirs.)
+    const double n = s.n, m = s.m, less = 15.0 + 0.026 * m, part = s.m < kLongGroups ? 2.0 / 3.0 : 1.0;
+    const double more = part * (0.0121 * n + 0.9e-9 * 9.0 * (n - m) * m * m * batch);
     s.grouped = 4 * (int64_t)s.n >= 5 * (int64_t)s.m && more > less;
     return s;
 }
@@ -572,7 +586,22 @@ struct Schedule {
     float sx[kMaxSteps];  // scale of X entering step k
     float sg[kMaxSteps];  // scale of the m x m operands of step k
     double norm[kMaxSteps], r_max[kMaxSteps], t_max[kMaxSteps];  // bounds of |X|, |R| and |R G|
+    int group[kMaxSteps];  // steps of the group that begins with step k
 };
+
+// The groups of a shape that has them.  Q, the product of a group's R, has to
+// stay in FP16's range.
+void groups_of(Schedule &s, int m)
+{
+    for (int k = 0; k < s.steps; k += s.group[k]) {
+        const int most = k == 0 && m >= kLongGroups ? kGroupSteps : 2;
+        int p = 1;
+        double q = s.r_max[k];
+        while (p < most && k + p < s.steps && std::fabs(s.a[k + p - 1]) <= kGroupSlope && q * s.r_max[k + p] <= 16384.0)
+            q *= s.r_max[k + p++];
+        s.group[k] = p;
+    }
+}
 
 float pow2_floor(double x) { return (float)std::exp2(std::floor(std::log2(x))); }
 
@@ -587,7 +616,6 @@ slide_status schedule_of(const slide_ortho_params *p, int m, Schedule *out)
         return fail(SLIDE_ERR_INVALID_ARG, "ortho params: eps must be finite and >= 0");
     out->steps = p->steps;
     double norm = 1.0, s = std::fmin(64.0, pow2_floor(std::sqrt((double)m)));
-    double q = 1.0;
     for (int k = 0; k < p->steps; ++k) {
         const float *t = p->coeffs ? p->coeffs + 3 * k : kQuintic;
         for (int e = 0; e < 3; ++e)
@@ -606,8 +634,7 @@ slide_status schedule_of(const slide_ortho_params *p, int m, Schedule *out)
         out->r_max[k] = r_max;
         out->t_max[k] = t_max;
         next *= 1.01;
-        q = (k % kGroupSteps == 0 ? 1.0 : q) * r_max;
-        if (!(next <= 64.0) || !(q <= 16384.0) || !(big <= 16384.0))
+        if (!(next <= 64.0) || !(r_max <= 16384.0) || !(big <= 16384.0))
             return fail(SLIDE_ERR_INVALID_ARG, "ortho params: the coefficients' polynomial grows beyond the range of "
                                                "the iteration (spectral norm 64)");
         double sx = s;
@@ -618,6 +645,7 @@ slide_status schedule_of(const slide_ortho_params *p, int m, Schedule *out)
         s = std::fmax(1.0, s / std::fmax(1.0, std::exp2(std::ceil(std::log2(std::fmax(1.0, std::fabs(a)))))));
         norm = std::fmax(next, 1e-3);
     }
+    groups_of(*out, m);
     return SLIDE_OK;
 }
 
@@ -701,7 +729,7 @@ cudaError_t enqueue_products(const Shape &s, const Work &w, const Schedule &sc, 
     };
     int cur = 0;
     for (int k0 = 0; k0 < sc.steps;) {
-        const int p = s.grouped ? (sc.steps - k0 < kGroupSteps ? sc.steps - k0 : kGroupSteps) : 1;
+        const int p = s.grouped ? sc.group[k0] : 1;
         const bool last = k0 + p == sc.steps;
         if (plan.n_phases + 3 * kGroupSteps + 1 > kMaxPhases) {
             // the next group goes into a launch of its own, whose counts start at zero again
@@ -859,7 +887,9 @@ cudaError_t launch_behind(Kernel k, dim3 grid, const Args &a, cudaStream_t strea
 
 // The kernels for a small side of at most 128, which run all steps on the Gram
 // matrix; more than kSmallMaxSteps steps would let its rounding errors grow
-// (times a^2 a step in directions that X does not have).
+// (times a^2 a step in directions that X does not have).  Five steps are at most
+// 5e-3 off (spectra as above; 1.1e-2 if they begin with a = 8.2), six 2e-2: as
+// the products step by step are with so small a side.
 bool is_small(const Shape &s, const Schedule &sc) { return s.m <= kSmallSide && sc.steps <= kSmallMaxSteps; }
 
 cudaError_t enqueue_small(const Shape &s, const Work &w, const Schedule &sc, const SourceArgs &a, const Finish &f,

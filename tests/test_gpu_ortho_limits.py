@@ -77,6 +77,38 @@ def test_muon_step_of_values_at_the_ends_of_the_range(S, rows, cols, size):
     check_muon(S, th, mom, w, want, lr, scale, th0)
 
 
+QUINTIC5 = [(3.4445, -4.7750, 2.0315)] * 5
+# coefficients of a steep start, which the last ones bring to 1
+STEEP = [(a / 1.01, b / 1.01 ** 3, c / 1.01 ** 5) for a, b, c in (
+    (8.28721, -23.59589, 17.30039), (4.10706, -2.94785, 0.54484), (3.94869, -2.9089, 0.55182), (3.31842, -2.48849, 0.51005),
+    (2.30065, -1.6689, 0.41881), (1.9101, -1.3064, 0.39602), (1.9101, -1.3064, 0.39602))]
+
+
+def strong_directions(batch, rows, cols, count, noise, seed):
+    g = gen(seed)
+    u, v = torch.randn(batch, rows, count, generator=g, device="cuda"), torch.randn(batch, count, cols, generator=g, device="cuda")
+    x = (u * torch.arange(1, count + 1, device="cuda").rsqrt()) @ v / count ** 0.5
+    return x + noise * torch.randn(batch, rows, cols, generator=g, device="cuda")
+
+
+@pytest.mark.parametrize("batch,rows,cols", [(2, 238, 14962), (1, 8000, 300), (1, 640, 4096), (3, 1000, 3000), (1, 100, 3000)])
+@pytest.mark.parametrize("coeffs", [QUINTIC5, QUINTIC5 + QUINTIC5[:1], STEEP[:5], STEEP], ids=["quintic5", "quintic6", "steep5", "steep7"])
+@pytest.mark.parametrize("count,noise", [(4, 1e-2), (32, 1e-2), (32, 1e-3), (128, 1e-3)])
+def test_strong_directions_over_noise(S, batch, rows, cols, coeffs, count, noise):
+    """What is amplified to singular values near 1 from far below, beside others
+    that are there already.  Five steps are to stay within FACTOR; each step more
+    may let an error grow by the square root of 1.8, the quintic's slope over its
+    cycle of two.  A side of at most 128 has too few entries for the roundings to
+    average: five times that."""
+    x = strong_directions(batch, rows, cols, min(count, rows, cols), noise, 5)
+    n = len(coeffs)
+    allowed = FACTOR * 1.8 ** ((n - 5) / 2) * (5 if min(rows, cols) <= 128 else 1)
+    if n == 6 and min(rows, cols) < 300:
+        allowed *= 1.25                                        # the groups of two of so small a side
+    got = orthogonalize(S, x, S.ortho_params(steps=n, coeffs=coeffs))
+    assert off(got, factor64(x, n, coeffs)) <= allowed + BF16
+
+
 @pytest.mark.parametrize("blocks", [((0, 1, 64, 96), (6144, 1, 200, 72)), ((0, 1, 300, 200), (60000, 1, 64, 96)),
                                     ((0, 1, 200, 200), (40000, 0, 8, 8), (40000, 2, 150, 160), (88000, 3, 40, 8))])
 def test_a_wait_that_runs_out_in_a_layers_first_block_is_reported(S, monkeypatch, blocks):
