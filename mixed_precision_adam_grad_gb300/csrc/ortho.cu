@@ -666,9 +666,10 @@ bool test_stall(const MuonBlock &block)
     return v && (block.index == 0 || strcmp(v, "first") != 0);
 }
 
-// The products, from the matrix in x_hi[0] and x_lo to the caller's array.
+// The products, from the matrix in x_hi[0] and x_lo to the caller's array; with
+// `form` only how they would be computed.
 cudaError_t enqueue_products(const Shape &s, const Work &w, const Schedule &sc, const Finish &f, int device,
-                             cudaStream_t stream)
+                             cudaStream_t stream, int *form)
 {
     const int xc64 = 2 * s.cpad, mc64 = 2 * s.mpad, mdim = s.mpad * 128;
     const int kn = s.tall ? (s.rows + 63) / 64 : (s.cols + 63) / 64;
@@ -730,11 +731,13 @@ cudaError_t enqueue_products(const Shape &s, const Work &w, const Schedule &sc, 
     int cur = 0;
     for (int k0 = 0; k0 < sc.steps;) {
         const int p = s.grouped ? sc.group[k0] : 1;
+        if (form && p > 1)
+            *form |= kFormGroups;
         const bool last = k0 + p == sc.steps;
         if (plan.n_phases + 3 * kGroupSteps + 1 > kMaxPhases) {
             // the next group goes into a launch of its own, whose counts start at zero again
-            cudaError_t e = launch_ortho_products(plan, device, stream);
-            if (e == cudaSuccess)
+            cudaError_t e = launch_ortho_products(plan, device, stream, form);
+            if (e == cudaSuccess && !form)
                 e = cudaMemsetAsync(w.count, 0, sizeof(unsigned) * kMaxPhases * s.batch, stream);
             if (e != cudaSuccess)
                 return e;
@@ -867,7 +870,7 @@ cudaError_t enqueue_products(const Shape &s, const Work &w, const Schedule &sc, 
         cur ^= 1;
         k0 += p;
     }
-    return launch_ortho_products(plan, device, stream);
+    return launch_ortho_products(plan, device, stream, form);
 }
 
 template <typename Kernel, typename Args>
@@ -1023,7 +1026,7 @@ cudaError_t enqueue(const Shape &s, const Work &w, const Schedule &sc, const Sou
     if (is_small(s, sc))
         return enqueue_small(s, w, sc, a, f, fp32, muon, eps, device, stream);
     const cudaError_t e = enqueue_source(s, w, sc, a, f.block.index > 0, fp32, muon, eps, stream);
-    return e == cudaSuccess ? enqueue_products(s, w, sc, f, device, stream) : e;
+    return e == cudaSuccess ? enqueue_products(s, w, sc, f, device, stream, nullptr) : e;
 }
 
 slide_status check_shape(int32_t batch, int32_t rows, int32_t cols)
@@ -1238,4 +1241,24 @@ extern "C" slide_status slide_ortho_status(const void *workspace, slide_stream_t
         return fail(SLIDE_ERR_TIMEOUT, "a pipeline wait inside a product reached its limit; that call is incomplete");
     clear_error();
     return SLIDE_OK;
+}
+
+// Tests only: the OrthoForm of a call, or -1.
+extern "C" SLIDE_API int32_t slide_test_ortho_form(int32_t batch, int32_t rows, int32_t cols, int32_t muon,
+                                                   const slide_ortho_params *params)
+{
+    Schedule sc;
+    if (check_shape(batch, rows, cols) != SLIDE_OK || empty(batch, rows, cols) ||
+        schedule_of(params, rows < cols ? rows : cols, &sc) != SLIDE_OK)
+        return -1;
+    const Shape s = shape_of(batch, rows, cols);
+    if (is_small(s, sc))
+        return kFormSmall;
+    Finish f{};
+    f.epi = muon ? kEpiMuon : kEpiOut;
+    int device = 0, form = 0;
+    if (cudaGetDevice(&device) != cudaSuccess ||
+        enqueue_products(s, layout(s, nullptr), sc, f, device, nullptr, &form) != cudaSuccess)
+        return -1;
+    return form;
 }

@@ -1027,7 +1027,7 @@ double steps(const OrthoPlan &plan, int groups)
 
 }  // namespace
 
-cudaError_t launch_ortho_products(const OrthoPlan &plan, int device, cudaStream_t stream)
+cudaError_t launch_ortho_products(const OrthoPlan &plan, int device, cudaStream_t stream, int *form)
 {
     if (device < 0 || device >= kMaxDevices)
         return cudaErrorInvalidDevice;
@@ -1045,7 +1045,14 @@ cudaError_t launch_ortho_products(const OrthoPlan &plan, int device, cudaStream_
     OrthoPlan split = plan;
     split_gram(split, n1);
     narrow_tiles(split, n1);
-    if (0.39 * steps<2>(plan, n2) <= 0.33 * steps<1>(split, n1))
+    const bool in_pairs = 0.39 * steps<2>(plan, n2) <= 0.33 * steps<1>(split, n1);
+    if (form) {
+        *form |= in_pairs ? kFormPairs : 0;
+        for (int f = 0; f < split.n_phases && !in_pairs; ++f)
+            *form |= (split.ph[f].parts > 1 ? kFormSplit : 0) | (split.ph[f].narrow ? kFormNarrow : 0);
+        return cudaSuccess;
+    }
+    if (in_pairs)
         return launch<2>(plan, n2, stream);
     return launch<1>(split, n1, stream);
 }

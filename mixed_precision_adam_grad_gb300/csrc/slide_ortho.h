@@ -108,7 +108,17 @@ __device__ __forceinline__ void report_wait_limit(unsigned *status, unsigned *la
         atomicOr(layer_status, kStatusWaitLimit);
 }
 
-cudaError_t launch_ortho_products(const OrthoPlan &plan, int device, cudaStream_t stream);
+// How a call computes, for tests that are written for one way.
+enum OrthoForm {
+    kFormSmall = 1,    // the kernels for a small side
+    kFormGroups = 2,   // several steps on the Gram matrix
+    kFormPairs = 4,    // pairs of CTAs
+    kFormSplit = 8,    // K of the Gram matrix split
+    kFormNarrow = 16   // tiles of 128 x 64 in some phase
+};
+
+// With `form` nothing is launched: its bits are added to *form.
+cudaError_t launch_ortho_products(const OrthoPlan &plan, int device, cudaStream_t stream, int *form);
 
 // 1/d as a power of two times a factor, for a d = |X|_F + eps that may lie
 // anywhere among the norms of finite FP32 matrices (1/d itself need not be an
