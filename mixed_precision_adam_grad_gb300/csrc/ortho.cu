@@ -1125,7 +1125,10 @@ extern "C" slide_status slide_orthogonalize(int32_t batch, int32_t rows, int32_t
         return fail(SLIDE_ERR_INVALID_ARG, "x or bf16_out is NULL or not aligned to its type");
     if (x_row_stride < cols || out_row_stride < cols)
         return fail(SLIDE_ERR_INVALID_ARG, "a row stride is smaller than cols");
-    if (batch > 1 && (x_batch_stride < 0 || out_batch_stride < (int64_t)(rows - 1) * out_row_stride + cols))
+    // one after another, or row by row beside one another
+    const bool apart = out_batch_stride >= (int64_t)(rows - 1) * out_row_stride + cols ||
+                       (out_batch_stride >= cols && out_batch_stride <= (out_row_stride - cols) / (batch > 1 ? batch - 1 : 1));
+    if (batch > 1 && (x_batch_stride < 0 || !apart))
         return fail(SLIDE_ERR_INVALID_ARG, "x_batch_stride is negative, or the matrices of bf16_out overlap");
     const Shape s = shape_of(batch, rows, cols);
     const Work w = layout(s, (char *)workspace);

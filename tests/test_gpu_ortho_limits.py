@@ -156,3 +156,25 @@ def test_status_after_calls_with_nothing_to_do(S):
             S.slide_layer_muon_step(st, 0, blocks, [g], S.muon_hparams(), S.hparams(), None)
     finally:
         S.slide_state_destroy(st)
+
+
+@pytest.mark.parametrize("batch,rows,cols,gap", [(3, 50, 200, 0), (3, 50, 203, 5), (2, 300, 333, 3), (4, 333, 300, 0), (2, 1, 5, 1)])
+def test_matrices_beside_one_another(S, batch, rows, cols, gap):
+    """[rows, batch, cols]: the matrices' rows take turns, in x and in the result."""
+    lead = batch * (cols + gap) + 2
+    big = torch.zeros(rows, lead, device="cuda")
+    x = big.as_strided((batch, rows, cols), (cols + gap, lead, 1))
+    x.copy_(matrix(batch, rows, cols, 3))
+    out = torch.full((rows, lead), -7.0, dtype=torch.bfloat16, device="cuda")
+    S.slide_orthogonalize(batch, rows, cols, big, out, S.ortho_params(), workspace(S, batch, rows, cols),
+                          x_type=S.SLIDE_TYPE_FP32, x_row_stride=lead, x_batch_stride=cols + gap, out_row_stride=lead,
+                          out_batch_stride=cols + gap)
+    got = out.as_strided((batch, rows, cols), (cols + gap, lead, 1))
+    assert off(got, factor64(x)) <= FACTOR + BF16
+    keep = torch.ones_like(out, dtype=torch.bool)
+    keep.as_strided((batch, rows, cols), (cols + gap, lead, 1)).fill_(False)
+    assert (out[keep] == -7.0).all()
+    with pytest.raises(S.SlideError):                          # one value less, and they meet
+        S.slide_orthogonalize(batch, rows, cols, big, out, S.ortho_params(), workspace(S, batch, rows, cols),
+                              x_type=S.SLIDE_TYPE_FP32, x_row_stride=lead, x_batch_stride=cols, out_row_stride=lead,
+                              out_batch_stride=cols - 1)
