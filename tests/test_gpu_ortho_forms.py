@@ -118,3 +118,29 @@ def test_a_wait_of_a_pair_that_runs_out_is_reported(S, monkeypatch, rows, cols, 
     S.slide_orthogonalize(1, rows, cols, x, out, S.ortho_params(), ws, x_type=S.SLIDE_TYPE_FP32)
     assert S.slide_ortho_status(ws) == S.SLIDE_OK
     assert off(out, factor64(x)) <= FACTOR + BF16
+
+
+@pytest.mark.parametrize("batch,rows,cols,steps,want", [(1, 2300, 3301, 5, PAIRS | GROUPS), (1, 1537, 1536, 5, PAIRS),
+                                                        (1, 300, 8000, 5, GROUPS), (2, 700, 300, 16, 0), (6, 100, 1500, 5, SMALL)])
+def test_each_form_in_a_graph(S, batch, rows, cols, steps, want):
+    """Sixteen steps step by step take two launches with a clearing between them."""
+    coeffs = [(3.4445, -4.7750, 2.0315)] * 5 + [(1.875, -1.25, 0.375)] * (steps - 5)
+    p = S.ortho_params(steps=steps, coeffs=coeffs)
+    assert form(S, batch, rows, cols, params=p) & (PAIRS | GROUPS | SMALL) == want
+    x = matrix(batch, rows, cols, 2)
+    out, ws = torch.zeros(batch, rows, cols, dtype=torch.bfloat16, device="cuda"), workspace(S, batch, rows, cols)
+
+    def call():
+        S.slide_orthogonalize(batch, rows, cols, x, out, p, ws, x_type=S.SLIDE_TYPE_FP32, stream=torch.cuda.current_stream())
+    call()
+    first = out.clone()
+    assert off(first, factor64(x, steps, coeffs)) <= FACTOR + BF16
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for sign in (-1, 1):
+        x.mul_(-1)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, sign * first)
+    assert S.slide_ortho_status(ws) == S.SLIDE_OK
