@@ -484,8 +484,8 @@ SLIDE_API slide_status slide_streamed_timeline(slide_state *st, double *out, int
  *   to 10^4 times above the noise (with steeper coefficients, from a = 8.2 on,
  *   6e-3, 1.1e-2 with a side of at most 128), and by up to 2e-2 there after six
  *   or seven steps; by up to 3e-2 for a matrix of one repeated value, whose
- *   roundings all have one sign.  In a Muon step of matrices with both sides above 128 O is
- *   kept in 11 bits on its way to theta, a tenth of that.
+ *   roundings all have one sign.  In a Muon step with both sides above 128, or
+ *   more than six steps, O is kept in 11 bits on its way to theta (2.4e-4).
  * Finite values may lie anywhere in their type's range, the norm too.  Zeros
  * give zeros; a NaN or an infinity in a matrix makes that matrix's result NaN
  * and touches no other matrix of the batch. */

@@ -494,8 +494,9 @@ Shape shape_of(int batch, int rows, int cols)
     // phases instead of 17 and 10 with a K of m instead of 15: 15 us + 0.026 m
     // less, against 0.0121 us n for three more Gram matrices and 0.9 ms for
     // each 1e12 operations more.  Fitted to 45 shapes from 200 x 260 to 4000 x
-    // 32000, of which the rule misses two by 3 and 7 %: 200 x 600 95 us step by
-    // step, 110 in groups; 1000 x 3000 229 and 197.
+    // 32000: 200 x 600 95 us step by step, 110 in groups; 1000 x 3000 229 and
+    // 197.  Of 163 shapes from 136 x 1000 to 8 of 500 x 16000 it misses one by
+    // 9 % (30 of 320 x 1000), the others by at most 5 %.
     // (Of groups of 2 + 2 + 1 the third of these Gram matrices is one of theirs.)
     const double n = s.n, m = s.m, less = 15.0 + 0.026 * m, part = s.m < kLongGroups ? 2.0 / 3.0 : 1.0;
     const double more = part * (0.0121 * n + 0.9e-9 * 9.0 * (n - m) * m * m * batch);
@@ -720,9 +721,9 @@ cudaError_t enqueue_products(const Shape &s, const Work &w, const Schedule &sc, 
     mm.sym = 1;
 
     // From m = 512 on T and all but a group's first G are kept without their low
-    // halves: 0.8e-3 to 1.0e-3 instead of 0.5e-3 to 0.8e-3 off there, and half
-    // the epilogue's traffic; a smaller m has fewer entries to average their
-    // roundings (1.6e-3 at m = 256).
+    // halves: 0.8e-3 to 1.0e-3 instead of 0.5e-3 to 0.8e-3 off there (noise with
+    // or without strong directions), and half the epilogue's traffic; a smaller m
+    // has fewer entries to average their roundings (1.6e-3 at m = 256).
     const bool lean = s.m >= 512;
     auto add = [&](const OrthoGemm &g, int epi) {
         plan.ph[plan.n_phases] = g;

@@ -36,8 +36,9 @@
 // Bound by the matrix instructions, or what L2 delivers to them, where there are
 // tiles for all SMs: 5120 x 17408 3.2 ms (1.14 PFLOP/s of the operations that
 // the formula needs, more with whole blocks on the diagonals), 40 of 1000 x 2187
-// 1.18 ms.  Few and small matrices are bound by the 15 to 17 dependent phases,
-// about 4.5 us each besides their products: 228 x 705 122 us.
+// 1.24 ms.  Few and small matrices are bound by the 15 to 17 dependent phases,
+// about 4.5 us each besides their products: a Muon step of 228 x 705 107 us; the
+// tensor pipe is busy 14 % of the time with 2 of 1024 x 2560.
 //
 // Why FP16 and where FP32 stays: FP16 rounds 8 times finer than BF16 at the
 // same rate, and the iterates are bounded (the matrix is normalised first), so
@@ -45,8 +46,8 @@
 // rounded enters the result only through a product with off-diagonal values:
 // the diagonal of every left factor is kept apart in FP32 and applied to the
 // iterate's full 22 bits.  Off by 5e-4 to 1.2e-3 (2-norm over 2-norm) from
-// the polynomial in 64 bits for spectra from flat to a single spike, where
-// BF16 operands are 1e-2 to 1e-1 off.
+// the polynomial in 64 bits for noise with or without strong directions, where
+// BF16 operands are 1e-2 to 1e-1 off; ortho.cu says what a wider spectrum costs.
 #include <cuda_bf16.h>
 
 #include <atomic>

@@ -16,9 +16,9 @@
 // all steps can run on G without going back to X.  For a 64 x 2560 matrix the
 // products themselves take a fifth of the time: what counts is the number of
 // dependent steps, about 1.5 us each inside a CTA, where a product that goes
-// through global memory and a count of all CTAs takes 6 us.  64 x 2560 takes 35
-// us (12, 22 and 8, overlapping a little); 36 matrices of 64 x 16512 126 us for
-// 380 MB, 3.0 TB/s: conversions to 16-bit pairs beside the loads.
+// through global memory and a count of all CTAs takes 6 us.  64 x 2560 takes 31
+// us; 36 matrices of 64 x 16512 124 us for 380 MB, 3.1 TB/s: conversions to
+// 16-bit pairs beside the loads.
 #include <cuda_bf16.h>
 
 #include <atomic>

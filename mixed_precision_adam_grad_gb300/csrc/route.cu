@@ -601,7 +601,8 @@ __global__ void __launch_bounds__(kWarps * 32) k_route_back_sparse(const BackArg
 }
 
 // Gradient of a softmax that is not renormalised: the whole row, one token per
-// warp.
+// warp.  65536 x 256 FP32 33 us (134 MB): five sums over the warp a token, one
+// after another; 28 us with the cancelling difference.
 template <typename T, int NV>
 __global__ void __launch_bounds__(kWarps * 32) k_route_back_dense(const BackArgs a)
 {
