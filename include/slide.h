@@ -486,7 +486,9 @@ SLIDE_API slide_status slide_streamed_timeline(slide_state *st, double *out, int
  *   or seven steps; by up to 3e-2 for a matrix of one repeated value, whose
  *   roundings all have one sign.  In a Muon step with both sides above 128, or
  *   more than six steps, O is kept in 11 bits on its way to theta (2.4e-4).
- * Finite values may lie anywhere in their type's range, the norm too.  Zeros
+ * Finite values may lie anywhere in their type's range, the norm too.  X itself
+ * is held to 2^-34 before the steps: where eps exceeds the norm a million times
+ * and more, little is left of it, and of its result.  Zeros
  * give zeros; a NaN or an infinity in a matrix makes that matrix's result NaN
  * and touches no other matrix of the batch. */
 enum { SLIDE_TYPE_BF16 = 0, SLIDE_TYPE_FP32 = 1 };
