@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kThreads) k_dropout_vec(const DropoutArgs a, i
         const int64_t b = b0 + i * kThreads;
         row[i] = 0;
         if (blocks != cols8)
-            row[i] = (uint64_t)b >> 32 ? b / cols8 : (uint32_t)b / (uint32_t)cols8;
+            row[i] = row_of_block(b, cols8);
         at[i] = (b - row[i] * cols8) * 8;
         if (b < blocks) {
             rx[i] = load_raw8(x + row[i] * a.xs + at[i]);

@@ -24,6 +24,14 @@ slide_status make_drop(const slide_dropout_config *c, Drop *d);
 inline bool misaligned(const void *p, size_t to) { return ((uintptr_t)p % to) != 0; }
 inline size_t type_size(int32_t type) { return type == SLIDE_TYPE_FP32 ? 4 : 2; }
 
+// The row that block b of eight values lies in, of rows of cols8 blocks.  The
+// division, a sequence of instructions that is much longer in 64 bits, is one of
+// 32 where both numbers have no more (a row may have 2^37 blocks).
+inline __host__ __device__ int64_t row_of_block(int64_t b, int64_t cols8)
+{
+    return (uint64_t)(b | cols8) >> 32 ? b / cols8 : (uint32_t)b / (uint32_t)cols8;
+}
+
 // Multiprocessors of the current device (dropout.cu).
 cudaError_t multiprocessors(int *n);
 
