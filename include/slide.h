@@ -764,6 +764,8 @@ SLIDE_API slide_status slide_norm_backward(int64_t rows, int32_t cols, const voi
  *     part in total or d_weight, whatever its x holds.
  *   - A target of vocab or more gives the token a loss of NaN, and NaN in all
  *     that depends on it.
+ *   - A logit of -inf adds nothing; a target's makes the loss infinite, lse is
+ *     that of the other words.
  *   - A NaN among a token's logits, or an infinity other than -inf, makes its
  *     loss and d_x NaN, and NaN what they enter.
  *

@@ -213,8 +213,8 @@ __device__ __forceinline__ void join_rows(const GroupArgs &g, int second)
             g.ref[t] = ref + top;
         }
         g.loss[t] = loss;
-        if (g.lse)
-            g.lse[t] = y != -1 ? own + loss : 0.0f;
+        if (g.lse)  // (a target's logit of -inf adds nothing to the others: its loss is infinite, lse is not)
+            g.lse[t] = y == -1 ? 0.0f : own > -INFINITY ? own + loss : ref + logf(total);
         g.scale[t] = scale;
         if (g.e && y >= 0)
             g.e[t * g.e_stride + y] = __float2bfloat16_rn(-others);

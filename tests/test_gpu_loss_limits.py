@@ -1,0 +1,86 @@
+"""slide_linear_cross_entropy at its limits, against its formulas in 64 bits: infinite
+logits, sums over very many products, and the roundings of its gradients.
+
+u = 2^-24 is half a step of FP32, B = 2^-8 half a step of BF16.
+"""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+U, B = 2.0 ** -24, 2.0 ** -8
+
+
+@pytest.fixture(scope="module")
+def S():
+    from mixed_precision_adam_grad_gb300 import build
+    build.build()
+    import mixed_precision_adam_grad_gb300 as S
+    return S
+
+
+def call(S, x, w, y, d_x=True, d_weight=True, d_loss=None):
+    T, H = x.shape
+    V = w.shape[0]
+    o = {"loss": torch.empty(T, device="cuda"), "lse": torch.empty(T, device="cuda"), "total": torch.empty(1, device="cuda")}
+    if d_x:
+        o["d_x"] = torch.empty_like(x)
+    if d_weight:
+        o["d_weight"] = torch.empty_like(w)
+    ws = torch.empty(S.slide_linear_cross_entropy_workspace(T, H, V, d_x, d_weight), dtype=torch.uint8, device="cuda")
+    s = torch.cuda.current_stream()
+    S.slide_linear_cross_entropy(T, H, V, x, w, y, o["loss"], ws, d_loss=d_loss, lse=o["lse"], total=o["total"], d_x=o.get("d_x"),
+                                 d_weight=o.get("d_weight"), stream=s)
+    assert S.slide_linear_cross_entropy_status(ws, stream=s) == S.SLIDE_OK
+    return o
+
+
+def overflowing(T, H=64, V=200, seed=0):
+    """Finite factors whose logits of word 10 leave FP32 for every other token: 2^100 times -2^100.
+    The remaining logits are a few units, what column 0 adds to them at most one."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    w = (torch.randn(V, H, generator=g, device="cuda") * 0.1).bfloat16()
+    x[:, 0] = 0.0
+    x[::2, 0] = 2.0 ** 100
+    w[:, 0] = (torch.rand(V, generator=g, device="cuda") * 2.0 ** -100).bfloat16()
+    w[10, 0] = -2.0 ** 100
+    y = torch.randint(0, V, (T,), generator=g, device="cuda")
+    y[::4] = 10
+    y[1] = 10                                                    # a token for which the word counts
+    return x, w, y
+
+
+def gradients(x, w, y, up):
+    """In 64 bits, and the sums of the terms' magnitudes."""
+    q = torch.softmax(x.double() @ w.double().T, 1)
+    q[torch.arange(len(y), device="cuda"), y] -= 1
+    q *= up
+    return {"d_x": (q @ w.double(), q.abs() @ w.double().abs()), "d_weight": (q.T @ x.double(), q.abs().T @ x.double().abs())}
+
+
+def within_terms(o, want, rows=slice(None)):
+    """Three roundings of a term and one of the result, the logits' own errors below 1e-4."""
+    for k, (r, size) in want.items():
+        bad = ~((o[k].double() - r).abs() <= (3.05 * B + 1e-4) * size + 1.01 * B * r.abs())
+        if k == "d_x":
+            bad = bad[rows]
+        assert not bad.any(), (k, bad.nonzero()[0].tolist())
+
+
+@pytest.mark.parametrize("T", [6, 100, 700])
+def test_a_target_of_minus_infinity(S, T):
+    """lse is that of the other words, the loss infinite, the gradients those of p = 0."""
+    x, w, y = overflowing(T)
+    o = call(S, x, w, y)
+    z = x.double() @ w.double().T                                # -2^200 in 64 bits: nothing beside the others
+    lse = torch.logsumexp(z, 1)
+    # sums of 64 products below 8 and of 200 words, the exponential and the logarithm
+    assert ((o["lse"].double() - lse).abs() <= 1e-5).all()
+    gone = torch.zeros(T, dtype=torch.bool, device="cuda")
+    gone[::4] = True
+    assert (o["loss"][gone] == INF).all() and o["total"].item() == INF
+    own = z.gather(1, y[:, None])[:, 0]
+    assert ((o["loss"].double() - (lse - own)).abs() <= 1e-5)[~gone].all()
+    within_terms(o, gradients(x, w, y, 1 / T))
