@@ -767,7 +767,7 @@ SLIDE_API slide_status slide_norm_backward(int64_t rows, int32_t cols, const voi
  *   - A logit of -inf adds nothing; a target's makes the loss infinite, lse is
  *     that of the other words.
  *   - A NaN among a token's logits, or an infinity other than -inf, makes its
- *     loss and d_x NaN, and NaN what they enter.
+ *     loss, lse and d_x NaN, and NaN what they enter.
  *
  * slide_linear_cross_entropy_workspace: device bytes of the workspace; d_x and
  * d_weight say which gradients are wanted (0 or not).

@@ -205,6 +205,8 @@ __device__ __forceinline__ void join_rows(const GroupArgs &g, int second)
         const float kept = __bfloat162float(__float2bfloat16_rn(others));
         if (kept >= FLT_MIN && kept <= FLT_MAX)
             scale *= others / kept;
+        if (isnan(loss))  // the gradients too (d_loss/total is 0 where the target's logit is infinite)
+            scale = loss;
     }
     if (lane == 0) {
         if (!second && top > kLceSpread && y != -1) {

@@ -84,3 +84,20 @@ def test_a_target_of_minus_infinity(S, T):
     own = z.gather(1, y[:, None])[:, 0]
     assert ((o["loss"].double() - (lse - own)).abs() <= 1e-5)[~gone].all()
     within_terms(o, gradients(x, w, y, 1 / T))
+
+
+@pytest.mark.parametrize("T", [6, 700])
+def test_a_logit_of_plus_infinity(S, T):
+    """NaN for its tokens, of which it is the target's for some, and in all of the weight's gradient, which
+    they enter; the others are as they are without them."""
+    x, w, y = overflowing(T)
+    w[10, 0] = 2.0 ** 100
+    o = call(S, x, w, y, d_weight=False)
+    x2, y2 = x.clone(), y.clone()
+    y2[::2] = -1
+    x2[::2] = 0
+    o2 = call(S, x2, w, y2, d_weight=False, d_loss=torch.full((T,), 1 / T, device="cuda"))
+    for k in ("loss", "lse", "d_x"):
+        assert torch.isnan(o[k][::2]).all(), k
+        assert torch.equal(o[k][1::2], o2[k][1::2]), k
+    assert torch.isnan(call(S, x, w, y)["d_weight"]).all()
