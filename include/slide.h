@@ -785,9 +785,10 @@ SLIDE_API slide_status slide_linear_cross_entropy_workspace(int64_t tokens, int3
  *   loss: FP32 [tokens]; lse: FP32 [tokens] or NULL; total: one FP32 or NULL.
  *   workspace: 256-byte aligned, contents irrelevant; in use until the enqueued
  *     work has run, so calls that may overlap need one each.
- * Where a token's largest logit lies more than 30 above its target's, the
- * products of its 256 tokens are formed a second time; nothing else depends on
- * the values.  Stream-ordered on the current device.
+ * Where a token's largest logit lies more than 30 above its target's (or below
+ * -30, the target's being -inf), the products of its 256 tokens are formed a
+ * second time; nothing else depends on the values.
+ * Stream-ordered on the current device.
  * Defined by: "An Efficient Heterogeneous Co-Design for Fine-Tuning on a
  * Single GPU", section 2.3 (the fused linear cross entropy: projection and loss
  * in one, the batch x sequence x vocabulary logits never materialised). */

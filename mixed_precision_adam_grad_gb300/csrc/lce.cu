@@ -14,8 +14,10 @@
 // equal numbers is formed anywhere, however sure the model is.
 // Where a logit lies more than 30 above the target's, so that e might leave
 // BF16's useful range, the 256 rows' logits are formed once more with the
-// largest logit as reference.  That is decided on the device: the launches are
-// always there and end at once where nothing is flagged.
+// largest logit as reference; so they are where the target's is -inf, its
+// reference therefore 0, and the largest lies more than 30 below that.  This is
+// decided on the device: the launches are always there and end at once where
+// nothing is flagged.
 //
 // Three products, 2*T*H*V operations each, as many as the formulas have; the
 // alternatives that need no T x V memory at all form the logits twice.  The e
@@ -209,7 +211,9 @@ __device__ __forceinline__ void join_rows(const GroupArgs &g, int second)
             scale = loss;
     }
     if (lane == 0) {
-        if (!second && top > kLceSpread && y != -1) {
+        // a logit far above the reference, or (where that is 0, the target's being -inf) all far below it
+        const bool far = top > kLceSpread || (own == -INFINITY && top < -kLceSpread && top > -INFINITY);
+        if (!second && far && y != -1) {
             g.again[0] = 1;
             g.again[1 + t / kLceRows] = 1;
             g.ref[t] = ref + top;

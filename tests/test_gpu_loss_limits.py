@@ -101,3 +101,20 @@ def test_a_logit_of_plus_infinity(S, T):
         assert torch.isnan(o[k][::2]).all(), k
         assert torch.equal(o[k][1::2], o2[k][1::2]), k
     assert torch.isnan(call(S, x, w, y)["d_weight"]).all()
+
+
+@pytest.mark.parametrize("T", [6, 700])
+def test_a_target_of_minus_infinity_and_others_far_below_zero(S, T):
+    """No logit is a reference of the others' size at first: all others lie near -100 or -1000, whose
+    exponentials are 0 in FP32."""
+    x, w, y = overflowing(T)
+    x[:, 1] = 1.0
+    x[::8, 1] = 8.0
+    w[:, 1] = -120.0
+    o = call(S, x, w, y)
+    z = x.double() @ w.double().T
+    lse = torch.logsumexp(z, 1)
+    # sums of magnitudes up to 1000 in at most eight steps, each off by a step of FP32 at most
+    assert ((o["lse"].double() - lse).abs() <= 16 * U * lse.abs() + 1e-5).all()
+    assert (o["loss"][::4] == INF).all() and torch.isfinite(o["loss"][1::2]).all()
+    within_terms(o, gradients(x, w, y, 1 / T))
