@@ -212,15 +212,16 @@ __device__ __forceinline__ void join_rows(const GroupArgs &g, int second)
     }
     if (lane == 0) {
         // a logit far above the reference, or (where that is 0, the target's being -inf) all far below it
-        const bool far = top > kLceSpread || (own == -INFINITY && top < -kLceSpread && top > -INFINITY);
+        const bool far = top - ref > kLceSpread || (own == -INFINITY && top < -kLceSpread && top > -INFINITY);
         if (!second && far && y != -1) {
             g.again[0] = 1;
             g.again[1 + t / kLceRows] = 1;
-            g.ref[t] = ref + top;
+            g.ref[t] = top;
         }
         g.loss[t] = loss;
-        if (g.lse)  // (a target's logit of -inf adds nothing to the others: its loss is infinite, lse is not)
-            g.lse[t] = y == -1 ? 0.0f : own > -INFINITY ? own + loss : ref + logf(total);
+        // (own + loss would lose lse's digits where the target lies far below, and all of them where it is -inf)
+        if (g.lse)
+            g.lse[t] = y == -1 ? 0.0f : ref == own || own == INFINITY ? own + loss : ref + logf(total);
         g.scale[t] = scale;
         if (g.e && y >= 0)
             g.e[t * g.e_stride + y] = __float2bfloat16_rn(-others);

@@ -254,7 +254,7 @@ __device__ __forceinline__ void epilogue_logits(const LceProduct &p, int row0, i
         float v[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e)
-            v[e] = __uint_as_float(raw[e]) - ref;
+            v[e] = __uint_as_float(raw[e]);
         // what does not count: columns beyond the last, the target's, rows of padding
         const int lim = p.cols - col, at = target - col;
         if (__any_sync(kFullMask, none || (unsigned)at < 32u) || lim < 32) {
@@ -267,7 +267,7 @@ __device__ __forceinline__ void epilogue_logits(const LceProduct &p, int row0, i
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
             top = fmaxf(top, v[e]);
-            v[e] = exp2_approx(v[e] * kLog2e);
+            v[e] = exp2_approx((v[e] - ref) * kLog2e);
             s += v[e];
         }
         sum += s;
@@ -354,7 +354,7 @@ __device__ __forceinline__ void epilogue_fp32(const LceProduct &p, int row0, int
     }
 }
 
-// LONG: logits of more than one run, which take 168 registers instead of 96.
+// LONG: logits of more than one run, which take 168 registers instead of 84.
 template <int CG, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1) k_lce_product(const __grid_constant__ LceProduct p)
 {

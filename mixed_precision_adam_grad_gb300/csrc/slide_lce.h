@@ -13,7 +13,7 @@ constexpr float kLceSpread = 30.0f;   // how far a logit may lie above its row's
 // What becomes of a product, with r a row and c a column of the result.
 enum LceKind {
     kLceLogits = 0,  // e = exp(value - ref[r]), 0 for the target's column: written as BF16 (with `keep`), its sum and the
-                     // largest value - ref[r] over 128 columns left in `sum` and `top`
+                     // largest value over 128 columns left in `sum` and `top`
     kLceScaled = 1,  // scale[r]*value as BF16
     kLcePlain = 2,   // value as BF16
     kLcePart = 3,    // value as FP32, part after part

@@ -118,3 +118,24 @@ def test_a_target_of_minus_infinity_and_others_far_below_zero(S, T):
     assert ((o["lse"].double() - lse).abs() <= 16 * U * lse.abs() + 1e-5).all()
     assert (o["loss"][::4] == INF).all() and torch.isfinite(o["loss"][1::2]).all()
     within_terms(o, gradients(x, w, y, 1 / T))
+
+
+@pytest.mark.parametrize("T", [6, 700])
+@pytest.mark.parametrize("k", [10, 20, 40, 100])
+def test_a_target_far_below_the_others(S, T, k):
+    """The others' logits lie around 120 or 960; the target's at -2^k, where FP32's steps are up to 2^77,
+    so nothing may pass through a difference from it but the loss."""
+    x, w, y = overflowing(T)
+    x[::2, 0] = 1.0
+    w[10, 0] = -2.0 ** k
+    x[:, 1] = 1.0
+    x[::8, 1] = 8.0
+    w[:, 1] = 120.0
+    o = call(S, x, w, y)
+    z = x.double() @ w.double().T
+    lse = torch.logsumexp(z, 1)
+    # sums of magnitudes up to 1000 in at most eight steps, each off by a step of FP32 at most
+    assert ((o["lse"].double() - lse).abs() <= 16 * U * lse.abs() + 1e-5).all()
+    loss = lse - z.gather(1, y[:, None])[:, 0]
+    assert ((o["loss"].double() - loss).abs() <= 16 * U * (lse.abs() + loss) + 1e-5).all()
+    within_terms(o, gradients(x, w, y, 1 / T))
