@@ -40,15 +40,16 @@ constexpr int kEpiBytes = kEpiWarps * kEpiBuffers * kPiece;
 constexpr int kBlock = 16384;                     // an operand of 128 x 64
 constexpr unsigned kFullMask = 0xffffffffu;
 constexpr unsigned kStatusWaitLimit = 2u;
-// Steps of 64 that the accumulators of a logit add up.  The matrix unit cuts
-// each of its additions, on average a quarter of 2^-24 of the sum so far, always
-// towards 0, so a long sum comes out small: by 4.3e-6 of its value over 5120
-// random products, by 6.6e-5 over 65536 (3.8e-4 where all have one sign).  The
-// epilogue's warps therefore take the sums of every kRun steps and add them in
-// registers, rounded: 7e-7 at any length.  This costs the logits' launch 1 to 2 %
-// (loss of 1021 x 2560 over 50257 words 181 us instead of 179, with 8 steps 183);
-// the gradients' sums, which end as BF16, stay in the accumulators.
-constexpr int kRun = 16;
+// Steps of 64 that the accumulators add up.  The matrix unit cuts each of its
+// additions, on average a quarter of 2^-24 of the sum so far, always towards 0, so
+// a long sum comes out small: by 4.3e-6 of its value over 5120 random products, by
+// 6.6e-5 over 65536; where all have one sign by 3.8e-4 over 65536 and 6.4e-3 over
+// a million.  The epilogue's warps therefore take the sums of every kRun steps and
+// add them in registers, rounded.  For logits this costs the launch 1 to 2 % (loss
+// of 1021 x 2560 over 50257 words 181 us instead of 179, with 8 steps 183).  The
+// gradients' sums end as BF16 and may be longer: 2.4e-5 over 4096 products of one
+// sign, where BF16 rounds by up to 3.9e-3.
+constexpr int kRun = 16, kGradientRun = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int CG>
@@ -354,11 +355,16 @@ __device__ __forceinline__ void epilogue_fp32(const LceProduct &p, int row0, int
     }
 }
 
-// LONG: logits of more than one run, which take 168 registers instead of 84.
-template <int CG, bool LONG>
+// Sums of one run, or logits' or gradients' of more: these take 168 registers
+// instead of 84.
+enum LceForm { kOneRun = 0, kLogitRuns = 1, kGradientRuns = 2 };
+
+template <int CG, int FORM>
 __global__ void __launch_bounds__(kThreads, 1) k_lce_product(const __grid_constant__ LceProduct p)
 {
     using R = Ring<CG>;
+    constexpr bool LONG = FORM != kOneRun;
+    constexpr int RUN = FORM == kLogitRuns ? kRun : kGradientRun;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Shared sh;
 
@@ -448,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lce_product(const __grid_consta
                     continue;
                 const int last = first_step(p, x.part + 1);
                 for (int k0 = first_step(p, x.part), k1; ok && k0 < last; k0 = k1, ++n) {
-                    k1 = LONG && last - k0 > kRun ? k0 + kRun : last;
+                    k1 = LONG && last - k0 > RUN ? k0 + RUN : last;
                     const uint32_t buf = n & 1, use = n >> 1;
                     ok = __all_sync(kFullMask, mbar_wait(smem_addr(&sh.acc_empty[buf]), (use & 1) ^ 1, &sh.abort));
                     if (!ok)
@@ -489,7 +495,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_lce_product(const __grid_consta
         const int quad = warp & 3, half = (warp - 2) >> 2;
         const uint32_t mine = ring + R::kStages * R::kStage + ((warp - 2) * kEpiBuffers) * kPiece;
         uint32_t n = 0, pieces = 0;
-        const int runs = (p.k64 + kRun - 1) / kRun;
         bool ok = true;
         auto acc = [&] { return tmem + ((uint32_t)(quad * 32) << 16) + (n & 1) * kLceCols + half * 128; };
         auto wait_acc = [&] {
@@ -511,6 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lce_product(const __grid_consta
                 continue;
             const int row0 = (x.i * CG + (int)rank) * 128 + quad * 32, col0 = x.j * kLceCols + half * 128;
             if constexpr (LONG) {
+                const int runs = (first_step(p, x.part + 1) - first_step(p, x.part) + RUN - 1) / RUN;
                 float z[128];
 #pragma unroll
                 for (int e = 0; e < 128; ++e)
@@ -527,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lce_product(const __grid_consta
             }
             if (!ok)
                 break;
-            if (LONG || p.kind == kLceLogits)
+            if (FORM == kLogitRuns || (FORM == kOneRun && p.kind == kLceLogits))
                 epilogue_logits(p, row0, col0, lane, acc(), mine, pieces);
             else if (p.kind == kLceScaled || p.kind == kLcePlain)
                 epilogue_bf16(p, row0, col0, lane, acc(), mine, pieces);
@@ -583,16 +589,15 @@ cudaError_t resident_groups(int device, int *groups)
         return cudaSuccess;
     int sms = 0;
     cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k_lce_product<CG, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<CG>::kSmem);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k_lce_product<CG, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<CG>::kSmem);
+    for (auto *kernel : {k_lce_product<CG, kOneRun>, k_lce_product<CG, kLogitRuns>, k_lce_product<CG, kGradientRuns>})
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<CG>::kSmem);
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute at[2];
     configure<CG>(cfg, at, sms / CG, nullptr);
     cfg.numAttrs = 1;
     if (e == cudaSuccess)
-        e = cudaOccupancyMaxActiveClusters(groups, k_lce_product<CG, true>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(groups, k_lce_product<CG, kLogitRuns>, &cfg);
     if (e != cudaSuccess)
         return e;
     if (*groups < 1)
@@ -613,8 +618,11 @@ cudaError_t launch(const LceProduct &p, int device, cudaStream_t stream)
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute at[2];
     configure<CG>(cfg, at, tiles < groups ? tiles : groups, stream);
-    return p.kind == kLceLogits && p.k64 > kRun ? cudaLaunchKernelEx(&cfg, k_lce_product<CG, true>, p)
-                                                : cudaLaunchKernelEx(&cfg, k_lce_product<CG, false>, p);
+    const bool logits = p.kind == kLceLogits;
+    const int most = (p.k64 + p.parts - 1) / p.parts;  // steps of a part
+    return most <= (logits ? kRun : kGradientRun) ? cudaLaunchKernelEx(&cfg, k_lce_product<CG, kOneRun>, p)
+           : logits                               ? cudaLaunchKernelEx(&cfg, k_lce_product<CG, kLogitRuns>, p)
+                                                  : cudaLaunchKernelEx(&cfg, k_lce_product<CG, kGradientRuns>, p);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,

@@ -139,3 +139,40 @@ def test_a_target_far_below_the_others(S, T, k):
     loss = lse - z.gather(1, y[:, None])[:, 0]
     assert ((o["loss"].double() - loss).abs() <= 16 * U * (lse.abs() + loss) + 1e-5).all()
     within_terms(o, gradients(x, w, y, 1 / T))
+
+
+@pytest.mark.parametrize("T", [65536, 262144, 1000001])
+def test_d_weight_of_very_many_tokens(S, T):
+    """Every term of these sums is positive, so an addition that cuts shows in their mean.  The
+    matrix unit adds 4096 products at a time (256 additions, each off by a step of FP32 at most) and
+    the sums of those are rounded.  The terms' roundings and those of the results have no sign of
+    their own: at most B/sqrt(3) each in the mean square, over 63 * 256 results five deviations."""
+    H, V = 256, 64
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = (torch.rand(T, H, generator=g, device="cuda") + 0.5).bfloat16()
+    w = (torch.randn(V, H, generator=g, device="cuda") * 0.02).bfloat16()
+    o = call(S, x, w, torch.zeros(T, dtype=torch.int64, device="cuda"), d_x=False)
+    want = torch.zeros(V, H, dtype=torch.float64, device="cuda")
+    for a in range(0, T, 65536):
+        part = x[a:a + 65536].double()
+        want += torch.softmax(part @ w.double().T, 1).T @ part / T
+    off = (o["d_weight"].double() / want - 1)[1:]                # word 0 is the target
+    assert abs(float(off.mean())) <= (256 + 2) * 2 * U + (T / 4096) * U + 5 * B / 3 ** 0.5 / off.numel() ** 0.5
+    assert float(off.abs().max()) <= 3.05 * B
+
+
+def test_d_x_of_a_very_long_vocabulary(S):
+    """The same for d_x, its sums over 98304 words in one part; a token's factor takes the target's rounding
+    (B/sqrt(3) at most) onto all of its results, so 9728 of them count, not 9728 * 512."""
+    T, H, V = 9728, 512, 98304
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = (torch.randn(T, H, generator=g, device="cuda") * 0.05).bfloat16()
+    w = (torch.rand(V, H, generator=g, device="cuda") + 0.5).bfloat16()
+    w[0] = 0                                                     # the target, so that all terms are positive
+    o = call(S, x, w, torch.zeros(T, dtype=torch.int64, device="cuda"), d_weight=False)
+    wd, mean = w.double(), 0.0
+    for a in range(0, T, 1216):
+        off = o["d_x"][a:a + 1216].double() / (torch.softmax(x[a:a + 1216].double() @ wd.T, 1) @ wd / T) - 1
+        assert float(off.abs().max()) <= 3.05 * B
+        mean += float(off.sum()) / (T * H)
+    assert abs(mean) <= (256 + 2) * 2 * U + (V / 4096) * U + 5 * B / 3 ** 0.5 / T ** 0.5
