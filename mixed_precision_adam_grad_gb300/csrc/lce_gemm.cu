@@ -266,8 +266,10 @@ __device__ __forceinline__ void epilogue_logits(const LceProduct &p, int row0, i
         }
         float s = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
+        for (int e = 0; e < 32; ++e)
             top = fmaxf(top, v[e]);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
             v[e] = exp2_approx((v[e] - ref) * kLog2e);
             s += v[e];
         }
