@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, min_blocks<T>(MODE, NV, WHAT)) k_nor
                 if (c0 + i * gap < end)
                     part = add(part, s[i].get());
             }
-            mean = team_sum(part.sum(), red[half][team], team, warps) * a.inv_cols;
+            mean = quotient(team_sum(part.sum(), red[half][team], team, warps), (float)a.cols, a.inv_cols);
             half ^= 1;
             part.clear();
         }
