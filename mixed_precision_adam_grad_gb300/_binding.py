@@ -566,6 +566,8 @@ def dropout_config(p: float, seed: int, site=0, step=0, step_dev=None, first=0) 
     step when the kernel runs; it must outlive the calls that use it."""
     if not 0 <= seed < 1 << 64 or not 0 <= site < 1 << 32 or not 0 <= step < 1 << 32:
         raise ValueError("dropout: seed must fit in 64 bits, site and step in 32")
+    if not -1 << 63 <= first < 1 << 63:  # (a longer number would be cut to 64 bits without a word)
+        raise ValueError("dropout: first must lie in [0, 2^62]")
     cfg = slide_dropout_config(seed, first, _ptr(step_dev), site, step, p)
     cfg._keep = step_dev
     return cfg
