@@ -45,8 +45,10 @@ constexpr unsigned kStatusWaitLimit = 2u;
 // a long sum comes out small: by 4.3e-6 of its value over 5120 random products, by
 // 6.6e-5 over 65536; where all have one sign by 3.8e-4 over 65536 and 6.4e-3 over
 // a million.  The epilogue's warps therefore take the sums of every kRun steps and
-// add them in registers, rounded.  For logits this costs the launch 1 to 2 % (loss
-// of 1021 x 2560 over 50257 words 181 us instead of 179, with 8 steps 183).  The
+// add them in registers, rounded: 1.0e-6 of a logit of one sign's products at any
+// length, 2e-7 of the magnitudes where signs are random.  For logits this costs the
+// launch 1 to 2 % (loss of 1021 x 2560 over 50257 words 181 us instead of 179, with
+// 8 steps 183).  The
 // gradients' sums end as BF16 and may be longer: 2.4e-5 over 4096 products of one
 // sign, where BF16 rounds by up to 3.9e-3.
 constexpr int kRun = 16, kGradientRun = 64;
