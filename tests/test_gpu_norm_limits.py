@@ -44,3 +44,55 @@ def test_constant_rows(S, cols, kind):
     assert torch.equal(mean[held], values.float()[held])
     assert torch.equal(out[held], bias[None].expand_as(out)[held])
     assert ((rstd - 1e-5 ** -0.5).abs() <= 8 * U * 1e-5 ** -0.5)[held].all()
+
+
+def place(rows, cols, stride, shift, dt, seed):
+    """rows x cols values, rows `stride` apart, `shift` elements off an aligned address."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(shift + rows * stride, generator=g, device="cuda").to(dt)[shift:].view(rows, stride)[:, :cols]
+
+
+# contiguous odd rows, padded odd rows, rows off an aligned address, strides that differ modulo eight between the pairs
+LAYOUTS = [(513, 0, 0, 0), (1601, 0, 0, 0), (4099, 0, 0, 0), (1000, 7, 0, 0), (77, 0, 0, 3), (520, 0, 1, 1), (1601, 0, 4, 0), (2048, 8, 8, 0)]
+
+
+@pytest.mark.parametrize("cols,pad,more,shift", LAYOUTS)
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows", [5, 700])
+def test_in_place_at_any_width(S, rows, cols, pad, more, shift, kind):
+    """out over x and sum over residual, and the other way round; d_x over d_out and d_residual over d_sum, and the
+    other way round: what separate results of the same layouts hold, bit for bit, and nothing between the rows."""
+    dt = TYPES[kind]
+    cfg, drop, s = config(S, True, dt), S.dropout_config(0.2, 3, first=5), torch.cuda.current_stream()
+    one, two = cols + pad, cols + pad + more                     # strides of x and d_out, of residual and d_sum
+
+    def tensors():
+        return [place(rows, cols, one, shift, dt, 1), place(rows, cols, two, shift, dt, 2), place(rows, cols, one, shift, dt, 3),
+                place(rows, cols, two, shift, dt, 4)]
+    w = place(1, cols, cols, 0, dt, 5)[0].clone()
+    mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+
+    def forward(x, res, total, out):
+        S.slide_norm(rows, cols, x, w, out, cfg, residual=res, dropout=drop, sum=total, mean=mean, rstd=rstd, x_stride=x.stride(0),
+                     residual_stride=res.stride(0), sum_stride=total.stride(0), out_stride=out.stride(0), stream=s)
+
+    def backward(d, ds, dx, dr):
+        S.slide_norm_backward(rows, cols, normed, w, d, dx, cfg, rstd, mean=mean, d_sum=ds, dropout=drop, d_residual=dr,
+                              x_stride=normed.stride(0), d_out_stride=d.stride(0), d_sum_stride=ds.stride(0), d_x_stride=dx.stride(0),
+                              d_residual_stride=dr.stride(0), stream=s)
+
+    def gaps(t):
+        whole = torch.as_strided(t, (rows, t.stride(0)), (t.stride(0), 1), t.storage_offset())
+        return whole[:, cols:].clone()
+    normed = place(rows, cols, one, shift, dt, 6)
+    for call in (forward, backward):
+        for swapped in (False, True):
+            def results(t, k):                                   # forward: sum, out; backward: d_x, d_residual
+                return (t[k], t[k + 1]) if swapped == (call is forward) else (t[k + 1], t[k])
+            t, u = tensors(), tensors()
+            call(t[0], t[1], *results(t, 2))                     # beside the inputs
+            left = [gaps(v) for v in u[:2]]
+            call(u[0], u[1], *results(u, 0))                     # over them
+            torch.cuda.synchronize()
+            assert all(torch.equal(p, q) for p, q in zip(results(u, 0), results(t, 2))), (call.__name__, swapped)
+            assert all(torch.equal(gaps(v), k) for v, k in zip(u[:2], left))
