@@ -50,13 +50,16 @@ enum What { kNone = 0, kResidual = 1, kDropped = 2, kAnySum = 3 };  // s = x; re
 enum Norm { kAnyNorm = 0, kLayer = 1, kRms = 2 };                   // any; with weight and bias; with weight alone
 
 // Blocks that have to fit on an SM.  Other teams work while one waits for its
-// row, so registers are given up for warps: BF16 rows of 8192 take 55 us with 64
-// registers and 71 us with 93, a residual and a dropout 139 us with 80 and 156 us
-// with 99 (16384 x 5120); FP32 rows need theirs (2560: 33 us with 80, 42 with 64).
+// row, so registers are given up for warps: BF16 rows of 2560 take 20.9 us with four
+// blocks, 22.7 with three and 25.0 with two, a residual and a dropout 127 us with
+// three, 132 with four (spilled) and 140 with two (16384 x 5120); FP32 rows need
+// theirs (8192 x 1601: 26.7 us with two, 33.9 with three and 37.0 with four).  Single
+// values: 8192 x 2561 113 us with three, 195 with one; 4096 x 8191 214 us with one,
+// 296 with two.
 template <typename T>
 constexpr int min_blocks(int mode, int nv, int what)
 {
-    return mode == kSingle ? 1 : sizeof(T) == 4 ? (nv <= 3 ? 3 : 2) : nv <= 5 && what == kNone ? 4 : 3;
+    return mode == kSingle ? (nv <= 8 ? 4 : nv <= 16 ? 3 : 1) : sizeof(T) == 4 ? (nv <= 3 ? 3 : 2) : nv <= 5 && what == kNone ? 4 : 3;
 }
 
 // The thread's NV runs start VEC*32*warps values apart.
@@ -280,11 +283,18 @@ cudaError_t launch(NormArgs a, Mode mode, int sms, cudaStream_t s)
         }
         return launch_runs<T, kShifted, kOpen, kAnyNorm, -1>(a, sms, s);
     }
-    constexpr int kRuns[] = {8, 64};
-    const Form f = form_for(kRuns, a.cols, a.rows, sms);
-    a.warps = f.warps;
-    return f.nv == 8 ? launch<T, kSingle, 8, kOpen, kAnyNorm, -1>(a, sms, s)
-                     : launch<T, kSingle, 64, kOpen, kAnyNorm, -1>(a, sms, s);
+    // value by value: as few to a thread as the row allows, since each has a load, an
+    // address and two parameters of its own (8192 x 2561 BF16: 118 us, with two warps
+    // and 64 values to a thread 419)
+    constexpr int kRuns[] = {8};
+    if (a.cols <= 8 * kThreads) {
+        a.warps = form_for(kRuns, a.cols, a.rows, sms).warps;
+        return launch<T, kSingle, 8, kOpen, kAnyNorm, -1>(a, sms, s);
+    }
+    a.warps = kMaxWarps;
+    return a.cols <= 16 * kThreads   ? launch<T, kSingle, 16, kOpen, kAnyNorm, -1>(a, sms, s)
+           : a.cols <= 32 * kThreads ? launch<T, kSingle, 32, kOpen, kAnyNorm, -1>(a, sms, s)
+                                     : launch<T, kSingle, 64, kOpen, kAnyNorm, -1>(a, sms, s);
 }
 
 }  // namespace
