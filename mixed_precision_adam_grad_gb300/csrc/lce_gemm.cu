@@ -17,8 +17,8 @@
 //
 // Bound by the matrix instructions: 4096 x 5120 x 152064 takes 3.2 ms forwards
 // (1.98 PFLOP/s), 3.4 and 3.2 ms for the gradients; at 2048 x 2560 x 50257 the
-// tensor pipe is active 85, 89 and 85 % of the time.  In a series of calls the
-// power limit sets the pace (11.3 ms for the three, 1.69 PFLOP/s).  A pair's step of
+// tensor pipe is active 84, 87 and 84 % of the time.  In a series of calls the
+// power limit sets the pace (11.5 ms for the three, 1.66 PFLOP/s).  A pair's step of
 // 64 along K takes 0.34 us and brings 64 KiB from L2.
 #include <cuda_bf16.h>
 

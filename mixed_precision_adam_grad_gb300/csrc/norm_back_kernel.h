@@ -12,14 +12,16 @@
 // added atomically.  A second kernel joins the blocks' sums, always in the same
 // order.
 //
-// Bound by instructions: 8192 x 8192 BF16 takes 110 us (floor 60), 30 an element:
-// x, d_out and the weight are unpacked for the row's sums and again for its
-// gradient, x and d_out a third time for the columns.  With the residual's
-// gradient and a dropout 16384 x 5120 takes 200 us (floor 126), 49 an element,
-// issue slots busy 57 % of the time.  The columns' part alone (no d_x) runs at the
-// memory's rate: 55 us for 336 MB.  A block is 16 warps: 32 were slower (64
-// registers spill: 16384 x 5120 244 us instead of 227), two blocks of 8 faster by
-// 3 to 8 % up to 4096 columns and slower beyond 8192.
+// Bound by latency: 16 warps an SM (25 %) hide too little of it for the instructions
+// that they have, 30 an element: x, d_out and the weight are read from shared memory
+// and unpacked for the row's sums and again for its gradient, x and d_out a third
+// time for the columns.  8192 x 8192 BF16 takes 110 us (floor 60), FP32 8192 x 5120
+// 141 (75); with the residual's gradient and a dropout 16384 x 5120 takes 201 us
+// (floor 126), 49 instructions an element, issue slots busy 57 % of the time.  The
+// columns' part alone (no d_x) runs at the memory's rate: 55 us for 336 MB.  A block
+// is 16 warps: 32 were slower (64 registers spill: 16384 x 5120 244 us instead of
+// 227), two blocks of 8 faster by 3 to 8 % up to 4096 columns and slower beyond 8192;
+// one form serves both.
 #pragma once
 #include <algorithm>
 #include <atomic>

@@ -9,11 +9,13 @@
 // share of a row large, since what a row costs besides its values (addresses,
 // two sums over the team, a root) costs each of its threads the same.
 //
-// Bound by memory where rows are wide and plain: 8192 x 8192 BF16 49 us, 5.5 TB/s
-// of its 268 MB (83 % of a plain copy's rate), FP32 8192 x 5120 60 us (83 %).
-// Dropout, residual and norm of 16384 x 5120 BF16 take 127 us (79 %): 35
-// instructions an element, eight of them the generator's integers, issue slots
-// busy 62 % of the time with 24 warps an SM.
+// Bound by memory where rows are wide and plain: RMS of 8192 x 8192 BF16 48 us, 5.6
+// TB/s of its 268 MB (83 % of a plain copy's rate), FP32 8192 x 5120 61 us (83 %);
+// narrower ones by latency, since a team has no load in flight while it sums and
+// stores (8192 x 2560 BF16 21 us, 60 %, x 4096 33 us, 61 %).  Dropout, residual and
+// norm of 16384 x 5120 BF16 take 127 us (79 %): 35 instructions an element, eight of
+// them the generator's integers, issue slots busy 62 % of the time with 24 warps an
+// SM.
 #pragma once
 #include <atomic>
 
@@ -179,8 +181,11 @@ __global__ void __launch_bounds__(kThreads, min_blocks<T>(MODE, NV, WHAT)) k_nor
 
 // Runs of a thread and warps of a team: the fewest warps that hold the row, of
 // those the fewest runs; more warps where there are too few rows to fill the
-// device (32 warps an SM: RMS norms of 2048 x 4096 BF16 take 8.3 us, of 1024 x
-// 4096 7.9; at 16 warps 9.9 and 8.7; at 64 those of 2048 x 2560 take 10.3, not 8.6).
+// device (32 warps an SM: RMS norms of 2048 x 4096 BF16 take 9.0 us, at 24 11.8; at
+// 64 those of 2048 x 2560 took 10.3 instead of 8.6).  The warps that are resident of
+// the kernel at hand, 16 of FP32 rows, are no better count: RMS of 4099 x 1601 FP32
+// 18.5 us instead of 18.6, but 4096 x 2048 18.3 instead of 17.3, and 3000 x 2048 with
+// a residual 30.8 instead of 21.8.
 struct Form {
     int nv, warps;
 };

@@ -272,8 +272,8 @@ __device__ __forceinline__ void team_sync(int team, int warps)
 }
 
 // Sums of two values over a team of `warps` warps, on every lane.  red: the
-// team's [2][16] places; calls alternate between two such sets, since a warp is
-// at most one call ahead of another of its team.
+// team's 16 places; between two calls with the same ones the block's threads meet
+// at a barrier, so that no warp writes its sums while another still reads.
 __device__ __forceinline__ void team_sum2(float &a, float &b, float2 *red, int team, int warps)
 {
     const int lane = threadIdx.x & 31;

@@ -311,7 +311,7 @@ __device__ __forceinline__ void mma_commit(uint32_t bar)
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
-// 32 columns of this warp's 32 lanes.
+// 16 or 32 columns of this warp's 32 lanes.
 __device__ __forceinline__ void tmem_load16(uint32_t taddr, uint32_t (&r)[16])
 {
     asm volatile(
