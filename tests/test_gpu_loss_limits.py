@@ -149,8 +149,11 @@ def test_d_weight_of_very_many_tokens(S, T):
     their own: at most B/sqrt(3) each in the mean square, over 63 * 256 results five deviations."""
     H, V = 256, 64
     g = torch.Generator(device="cuda").manual_seed(T)
-    x = (torch.rand(T, H, generator=g, device="cuda") + 0.5).bfloat16()
-    w = (torch.randn(V, H, generator=g, device="cuda") * 0.02).bfloat16()
+    # (each column has a size of its own: a mean over many tokens is nearly the same in all, and would be
+    # rounded the same way)
+    size = 1 + torch.rand(H, generator=g, device="cuda")
+    x = ((torch.rand(T, H, generator=g, device="cuda") + 0.5) * size).bfloat16()
+    w = (torch.randn(V, H, generator=g, device="cuda") * 0.02 / size).bfloat16()
     o = call(S, x, w, torch.zeros(T, dtype=torch.int64, device="cuda"), d_x=False)
     want = torch.zeros(V, H, dtype=torch.float64, device="cuda")
     for a in range(0, T, 65536):
@@ -167,7 +170,7 @@ def test_d_x_of_a_very_long_vocabulary(S):
     T, H, V = 9728, 512, 98304
     g = torch.Generator(device="cuda").manual_seed(1)
     x = (torch.randn(T, H, generator=g, device="cuda") * 0.05).bfloat16()
-    w = (torch.rand(V, H, generator=g, device="cuda") + 0.5).bfloat16()
+    w = ((torch.rand(V, H, generator=g, device="cuda") + 0.5) * (1 + torch.rand(H, generator=g, device="cuda"))).bfloat16()
     w[0] = 0                                                     # the target, so that all terms are positive
     o = call(S, x, w, torch.zeros(T, dtype=torch.int64, device="cuda"), d_weight=False)
     wd, mean = w.double(), 0.0
