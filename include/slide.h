@@ -690,6 +690,7 @@ SLIDE_API slide_status slide_dropout(int64_t rows, int64_t cols, int32_t type, c
  *          to the type where it is not x, and it is the rounded s that is normed
  *   layer: mean = sum(s)/cols, rstd = 1/sqrt(sum((s - mean)^2)/cols + eps), out = (s - mean)*rstd*weight + bias
  *   rms:   rstd = 1/sqrt(sum(s^2)/cols + eps),                              out = s*rstd*weight + bias
+ *          (a sum of squares beyond FP32's range makes rstd 0)
  * and its gradient, with h = (s - mean)*rstd (s*rstd) and g = d_out*weight:
  *   d_s      = rstd*(g - [sum(g)/cols, of a layer norm] - h*sum(g*h)/cols) + d_sum
  *   d_x      = d_s through the dropout's mask;    d_residual = d_s
@@ -759,7 +760,7 @@ SLIDE_API slide_status slide_norm_backward(int64_t rows, int32_t cols, const voi
  * 2-norm of the error over 2-norm, the result's own rounding included: 1.7e-3 to
  * 1.9e-3 for d_x and for d_weight of few tokens, 2.3e-3 to 2.5e-3 for d_weight of
  * many; sums of any length are as near, since no more than 4096 products are
- * added at a time by the matrix unit, which cuts (2.4e-5 where all have one sign).
+ * added at a time by the matrix unit, which cuts (below 5e-5 where all have one sign).
  * The exponentials of a group of tokens are kept in the workspace between the
  * products that need them; a group is as large as fits into 2 GiB (at least 256
  * tokens).

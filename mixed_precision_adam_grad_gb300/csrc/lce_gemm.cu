@@ -48,9 +48,8 @@ constexpr unsigned kStatusWaitLimit = 2u;
 // add them in registers, rounded: 1.0e-6 of a logit of one sign's products at any
 // length, 2e-7 of the magnitudes where signs are random.  For logits this costs the
 // launch 1 to 2 % (loss of 1021 x 2560 over 50257 words 181 us instead of 179, with
-// 8 steps 183).  The
-// gradients' sums end as BF16 and may be longer: 2.4e-5 over 4096 products of one
-// sign, where BF16 rounds by up to 3.9e-3.
+// 8 steps 183).  The gradients' sums end as BF16 and may be longer: below 5e-5 over
+// 4096 products of one sign, where BF16 rounds by up to 3.9e-3.
 constexpr int kRun = 16, kGradientRun = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 
